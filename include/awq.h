@@ -436,6 +436,174 @@ awq_status_t awq_gemm_packed_w8(const void* x_f16, const void* packed, const voi
                                 int64_t M, int64_t K, int64_t N, int64_t group_size, void* y_f16,
                                 void* workspace, size_t workspace_bytes, awq_stream_t stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Operators between a decoder layer's linears: rotary positions, attention over a paged cache
+ * whose sequences share a prefix, routing of tokens to experts, and the dispatch / combine pair
+ * around the grouped linears above.  Elements are fp16 or bf16 (dtype AWQ_DTYPE_F16 or
+ * AWQ_DTYPE_BF16) unless stated; strides are in elements; arithmetic is fp32 (or wider), rounded
+ * once to the element type.  The conventions at the top of this file hold: device pointers, no
+ * allocation, asynchronous on `stream`, argument errors on the host before any launch.  Values
+ * that only the device sees (positions, slots, pages, lengths, expert ids, rows) are checked
+ * there: one outside its range never leads to an access outside the tensors.
+ * ------------------------------------------------------------------------------------------ */
+
+/* Scaling of the rotary frequencies f_i = base^(-2 i / rotary_dim) for contexts `factor` times
+ * the trained one. */
+typedef enum awq_rope_scaling {
+  AWQ_ROPE_NONE = 0,
+  AWQ_ROPE_LINEAR = 1, /* f / factor */
+  AWQ_ROPE_NTK = 2,    /* base * factor^(rotary_dim / (rotary_dim - 2)) in place of base */
+  AWQ_ROPE_YARN = 3,   /* pairs that turn over p0 times in original_max_position positions keep f,
+                        * pairs below p1 turns take f / factor, a ramp over the pair index between */
+  AWQ_ROPE_BANDED = 4  /* turns t = original_max_position * f / (2 pi): above p1 keeps f, below p0
+                        * takes f / factor, between f (b + (1 - b) / factor), b = (t - p0) / (p1 - p0) */
+} awq_rope_scaling_t;
+
+/*
+ * awq_rope_table -- the fp32 table [max_position, rotary_dim] that awq_rope reads: line p holds
+ * cos(p f_i) * attention_factor for the rotary_dim / 2 pairs, then the sines.  Angles, sines and
+ * cosines are computed in 64 bits and rounded once.  Written once per model.
+ * Requirements: rotary_dim even and in 2..65536 (NTK: >= 4), 0 <= max_position < 2^31, base > 1 and
+ * finite, factor > 0 (NONE: ignored); YARN: original_max_position > 0, p0 > p1 > 0; BANDED:
+ * original_max_position > 0, p1 > p0 > 0; attention_factor > 0; table 4-byte aligned.
+ */
+awq_status_t awq_rope_table(float* table, int64_t max_position, int64_t rotary_dim, double base,
+                            awq_rope_scaling_t scaling, double factor, int64_t original_max_position,
+                            double p0, double p1, double attention_factor, awq_stream_t stream);
+
+/*
+ * awq_rope -- rotates the first rotary_dim elements of every query and key head by the angles of
+ * its token's position and copies the rest:
+ *
+ *   (a, b) -> (a c - b s, b c + a s)   c, s: the table's line positions[t]
+ *
+ * with pairs (i, i + rotary_dim / 2), or (2 i, 2 i + 1) when interleaved.
+ *   q [T, Hq, D], k [T, Hkv, D]: strides given, a head's D elements contiguous (slices of a fused
+ *   projection's output do)
+ *   positions int32 [T]; table fp32 [max_position, rotary_dim] (awq_rope_table)
+ *   q_out [T, Hq, D], k_out [T, Hkv, D] dense; or q_out == q (k_out == k): in place, in q's (k's)
+ *   strides.  Outputs must not overlap inputs otherwise.
+ * A position outside [0, max_position) gives NaN in the rotated part.  T == 0: AWQ_OK, no launch.
+ * Requirements: rotary_dim even, 2 <= rotary_dim <= D <= 65536; Hq + 2 Hkv <= 65536; 16-bit tensors
+ * 2-byte, the others 4-byte aligned.  One launch.
+ */
+awq_status_t awq_rope(const void* q, const void* k, const int32_t* positions, const float* table,
+                      int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t rotary_dim,
+                      int64_t max_position, int64_t q_token_stride, int64_t q_head_stride,
+                      int64_t k_token_stride, int64_t k_head_stride, void* q_out, void* k_out,
+                      int interleaved, awq_dtype_t dtype, awq_stream_t stream);
+
+/* A paged key/value cache: cell (page, token, head) of keys starts at element page * page_stride +
+ * token * token_stride + head * head_stride of k, of values at the same element of v; head_dim
+ * elements contiguous.  Slot s is token s % page_size of page s / page_size. */
+typedef struct awq_paged_kv {
+  void* k;
+  void* v;
+  int64_t num_pages, page_size, heads, head_dim;
+  int64_t page_stride, token_stride, head_stride;
+} awq_paged_kv_t;
+
+/*
+ * awq_rope_append -- awq_rope whose rotated keys, with the values, go straight to a paged cache:
+ * token t's key and value heads to cell slots[t] (int32 [T]).  A slot outside the cache keeps
+ * nothing (padding tokens: -1).  Two tokens must not share a slot.  v [T, Hkv, D] as k; the cache
+ * has Hkv heads of D elements and must not overlap the inputs.  Otherwise as awq_rope.
+ */
+awq_status_t awq_rope_append(const void* q, const void* k, const void* v, const int32_t* positions,
+                             const float* table, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                             int64_t rotary_dim, int64_t max_position, int64_t q_token_stride,
+                             int64_t q_head_stride, int64_t k_token_stride, int64_t k_head_stride,
+                             int64_t v_token_stride, int64_t v_head_stride, void* q_out,
+                             const awq_paged_kv_t* cache, const int32_t* slots, int interleaved,
+                             awq_dtype_t dtype, awq_stream_t stream);
+
+/*
+ * awq_attention_shared -- attention of the n newest tokens of B sequences that share a prefix, the
+ * prefix read and multiplied once for all of them:
+ *
+ *   out[b][i][h] = sum_j softmax_j(scale * q[b][i][h] . k_j) v_j
+ *
+ * over the prefix's prefix_len keys and those keys of sequence b that query token i sees: the
+ * first lens[b] - n + i + 1 of its own (the n tokens are its last).  Query head h reads
+ * key/value head h / (Hq / heads).
+ *   q [B, n, Hq, D]: strides given, a head contiguous; out [B, n, Hq, D] dense
+ *   cache: D = 64, 96, 128 or 256, Hq a multiple of its heads
+ *   prefix_pages int32 [ceil(prefix_len / page_size)]: the prefix's pages, in order
+ *   pages int32 [B, W] (row stride pages_stride), lens int32 [B]: each sequence's own pages and its
+ *   number of own tokens; max_len >= every lens[b] (a longer one is cut to max_len), max_len <=
+ *   W * page_size.  prefix_len, max_len are host values: the plan depends on them.
+ * What the cache holds past a length is never used (it may be NaN).  A page outside [0, num_pages)
+ * gives unspecified values for its sequence.  A row that sees no key is zero.  B, n or Hq 0:
+ * AWQ_OK, no launch.
+ *   workspace: awq_attention_shared_workspace_size bytes (partial sums; same host values), 256-byte
+ *   aligned; any content.  Calls that overlap in time need workspaces of their own.
+ * Repeated calls give the same bits.  Requirements: q, the cache's tensors and out 16-byte aligned,
+ * q's and the cache's strides multiples of 8; sizes below 2^31.
+ */
+awq_status_t awq_attention_shared_workspace_size(int64_t B, int64_t n, int64_t Hq, int64_t heads,
+                                                 int64_t D, int64_t prefix_len, int64_t max_len,
+                                                 size_t* bytes);
+awq_status_t awq_attention_shared(const void* q, int64_t B, int64_t n, int64_t Hq,
+                                  int64_t q_batch_stride, int64_t q_token_stride, int64_t q_head_stride,
+                                  const awq_paged_kv_t* cache, const int32_t* prefix_pages,
+                                  int64_t prefix_len, const int32_t* pages, int64_t W,
+                                  int64_t pages_stride, const int32_t* lens, int64_t max_len,
+                                  float scale, void* out, awq_dtype_t dtype, void* workspace,
+                                  size_t workspace_bytes, awq_stream_t stream);
+
+/*
+ * awq_moe_route -- k experts and their weights for each token from the router's logits [T, E]
+ * (row stride given; dtype fp16, bf16 or AWQ_DTYPE_F32):
+ *
+ *   score = softmax over the row, or sigmoid;  key = score (+ bias, fp32 [E] or NULL)
+ *   groups > 1: experts form `groups` equal runs; a group's score is the sum of its group_best (1 or
+ *     2) best keys; experts outside the topk_groups best groups are out
+ *   the k best keys, best first; equal keys (and groups): the lower index first
+ *   weight = score (not the key), over the sum of the k scores if renormalize (0 if that is 0),
+ *     times scale
+ *
+ * A logit of -inf takes its expert out; a place left without an expert gets id -1, weight 0.  A row
+ * whose scores hold a NaN gets NaN weights and the ids 0 .. k - 1.
+ *   weights fp32 [T, k], experts int32 [T, k], dense
+ * Requirements: 1 <= E <= 1024, 1 <= k <= min(32, E / groups * topk_groups), 1 <= topk_groups <=
+ * groups <= 32, E % groups == 0.  T == 0: AWQ_OK, no launch.  One launch.
+ */
+awq_status_t awq_moe_route(const void* logits, int64_t T, int64_t E, int64_t row_stride,
+                           awq_dtype_t dtype, int64_t k, int sigmoid, const float* bias, int64_t groups,
+                           int64_t topk_groups, int64_t group_best, int renormalize, float scale,
+                           float* weights, int32_t* experts, awq_stream_t stream);
+
+/*
+ * awq_moe_dispatch -- sorts the T k places (token t, place j) by expert, equal experts in the order
+ * of the places, and gathers the tokens' rows accordingly: what awq_gemm_grouped and
+ * awq_gemm_packed_grouped take.
+ *   x 16-bit [T, W] (row stride given), experts int32 [T, k]
+ *   routed [T k, W] dense, offsets int32 [E + 1], rows int32 [T, k]: the place's row of routed
+ * A place whose id lies outside [0, E) (-1: no expert) gets rows = -1; offsets[E] counts the places
+ * with an expert, and routed's rows from there on are zero.
+ *   workspace: awq_moe_dispatch_workspace_size bytes, 256-byte aligned; any content.  Calls that
+ *   overlap in time need workspaces of their own.
+ * Requirements: 1 <= E <= 4096, 1 <= k <= 1024, T k < 2^31, outputs do not overlap inputs.  T == 0:
+ * offsets are set to 0.  W == 0: no rows are copied.
+ */
+awq_status_t awq_moe_dispatch_workspace_size(int64_t T, int64_t k, int64_t E, size_t* bytes);
+awq_status_t awq_moe_dispatch(const void* x, int64_t T, int64_t W, int64_t row_stride,
+                              const int32_t* experts, int64_t k, int64_t E, void* routed,
+                              int32_t* offsets, int32_t* rows, void* workspace, size_t workspace_bytes,
+                              awq_stream_t stream);
+
+/*
+ * awq_moe_combine -- out[t] = base[t] + sum_j weights[t][j] * y[rows[t][j]], in fp32 in the order of
+ * the places, rounded once.  Places whose row lies outside [0, R) (-1) are left out, whatever their
+ * weight.
+ *   y [R, W], base [T, W] (a residual or a shared expert's output) or NULL, out [T, W] (may be base),
+ *   dense; weights fp32 [T, k], rows int32 [T, k]
+ * Requirements: 0 <= k <= 1024, R and T k < 2^31.  T == 0 or W == 0: AWQ_OK, no launch.  One launch.
+ */
+awq_status_t awq_moe_combine(const void* y, int64_t R, int64_t W, const float* weights,
+                             const int32_t* rows, int64_t T, int64_t k, const void* base, void* out,
+                             awq_dtype_t dtype, awq_stream_t stream);
+
 /* Synchronizes `stream`, then reads and clears the library's device status word on the
  * current device.  Returns AWQ_ERR_TIMEOUT if a kernel gave up a bounded wait since the
  * last check (its output is then unspecified), AWQ_OK otherwise. */

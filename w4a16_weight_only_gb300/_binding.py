@@ -20,8 +20,19 @@ PATHS = {"auto": 0, "decode": 1, "prefill": 2, "generic": 3}
 PATH_NAMES = {v: k for k, v in PATHS.items()}
 DTYPE_F16, DTYPE_F32, DTYPE_BF16 = 0, 1, 2
 
+_i64, _vp, _i32, _f64, _f32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_double, ctypes.c_float
+
+
+class PagedKV(ctypes.Structure):
+    """awq_paged_kv_t."""
+    _fields_ = [("k", _vp), ("v", _vp)] + [(n, _i64) for n in ("num_pages", "page_size", "heads", "head_dim",
+                                                              "page_stride", "token_stride", "head_stride")]
+
+
+_kv = ctypes.POINTER(PagedKV)
+_size = ctypes.POINTER(ctypes.c_size_t)
+
 # Every entry point of include/awq.h: name -> (restype, argtypes)
-_i64, _vp, _i32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int
 SIGNATURES = {
     "awq_runtime_available": (_i32, []),
     "awq_last_error": (ctypes.c_char_p, []),
@@ -54,6 +65,16 @@ SIGNATURES = {
     "awq_gemm_packed_grouped": (_i32, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _vp, _i32, _vp]),
     "awq_repack_w8": (_i32, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp]),
     "awq_gemm_packed_w8": (_i32, [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp, ctypes.c_size_t, _vp]),
+    "awq_rope_table": (_i32, [_vp, _i64, _i64, _f64, _i32, _f64, _i64, _f64, _f64, _f64, _vp]),
+    "awq_rope": (_i32, [_vp] * 4 + [_i64] * 10 + [_vp, _vp, _i32, _i32, _vp]),
+    "awq_rope_append": (_i32, [_vp] * 5 + [_i64] * 12 + [_vp, _kv, _vp, _i32, _i32, _vp]),
+    "awq_attention_shared_workspace_size": (_i32, [_i64] * 7 + [_size]),
+    "awq_attention_shared": (_i32, [_vp] + [_i64] * 6 + [_kv, _vp, _i64, _vp, _i64, _i64, _vp, _i64, _f32, _vp, _i32, _vp,
+                                    ctypes.c_size_t, _vp]),
+    "awq_moe_route": (_i32, [_vp, _i64, _i64, _i64, _i32, _i64, _i32, _vp, _i64, _i64, _i64, _i32, _f32, _vp, _vp, _vp]),
+    "awq_moe_dispatch_workspace_size": (_i32, [_i64, _i64, _i64, _size]),
+    "awq_moe_dispatch": (_i32, [_vp, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    "awq_moe_combine": (_i32, [_vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _i32, _vp]),
 }
 GEMM_STATIC_WEIGHTS = 1
 

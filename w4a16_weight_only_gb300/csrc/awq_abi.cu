@@ -7,6 +7,7 @@
 
 #include "../../include/awq.h"
 #include "awq_internal.cuh"
+#include "awq_layer.cuh"
 
 namespace {
 
@@ -660,6 +661,343 @@ awq_status_t awq_selftest_wait_timeout(uint64_t limit_ns, awq_stream_t stream) {
   const cudaError_t e = awq::launch_selftest_wait(static_cast<unsigned long long>(limit_ns),
                                                   reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "launching the wait self test");
+  return ok();
+}
+
+// ------------------------------------------------ operators between a layer's linears ----
+
+namespace {
+
+awq_status_t check_half(awq_dtype_t dtype) {
+  if (dtype != AWQ_DTYPE_F16 && dtype != AWQ_DTYPE_BF16)
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "dtype must be AWQ_DTYPE_F16 or AWQ_DTYPE_BF16");
+  return AWQ_OK;
+}
+
+awq_status_t check_cache(const awq_paged_kv_t* c, awq::PagedKV* out) {
+  if (!c) return fail(AWQ_ERR_INVALID_ARGUMENT, "null cache");
+  if (c->num_pages < 0 || c->page_size <= 0 || c->heads <= 0 || c->head_dim <= 0)
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "cache: num_pages >= 0, page_size, heads, head_dim > 0 needed");
+  if (c->page_stride < 0 || c->token_stride < 0 || c->head_stride < 0)
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "cache strides must not be negative");
+  if (c->num_pages > kDimLimit || c->page_size > kDimLimit || c->heads > 65536 || c->head_dim > 65536 ||
+      c->num_pages * c->page_size > kDimLimit)
+    return fail(AWQ_ERR_UNSUPPORTED_SHAPE, "cache: num_pages * page_size must be below 2^31, heads and head_dim <= 65536");
+  if (c->num_pages > 0 && (!c->k || !c->v)) return fail(AWQ_ERR_INVALID_ARGUMENT, "cache: null k or v");
+  if (!al(c->k, 2) || !al(c->v, 2)) return fail(AWQ_ERR_MISALIGNED, "cache tensors must be 2-byte aligned");
+  *out = {static_cast<uint16_t*>(c->k), static_cast<uint16_t*>(c->v), static_cast<int>(c->num_pages),
+          static_cast<int>(c->page_size), static_cast<int>(c->heads), static_cast<int>(c->head_dim),
+          c->page_stride, c->token_stride, c->head_stride};
+  return AWQ_OK;
+}
+
+awq_status_t rope(awq::RopeProblem* p, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t rotary_dim,
+                  int64_t max_position, awq_dtype_t dtype, const char* what) {
+  awq_status_t st = check_half(dtype);
+  if (st != AWQ_OK) return st;
+  if (T < 0 || Hq < 0 || Hkv < 0 || max_position < 0)
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "T, Hq, Hkv, max_position must be >= 0");
+  if (rotary_dim < 2 || rotary_dim % 2 || rotary_dim > D)
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "rotary_dim must be even, in 2..D (got %lld of D %lld)",
+                (long long)rotary_dim, (long long)D);
+  if (D > 65536 || Hq > 65536 || Hkv > 65536 || Hq + 2 * Hkv > 65536 || T > kDimLimit || max_position > kDimLimit)
+    return fail(AWQ_ERR_UNSUPPORTED_SHAPE, "D and Hq + 2 Hkv must be <= 65536, T and max_position below 2^31");
+  if ((Hq + 2 * Hkv) * D > kDimLimit) return fail(AWQ_ERR_UNSUPPORTED_SHAPE, "a token's heads must be below 2^31 elements");
+  if (p->append && (p->kv.heads != Hkv || p->kv.head_dim != D))
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "the cache must have Hkv heads of D elements");
+  if (T == 0 || Hq + Hkv == 0) return ok();
+  if ((Hq && (!p->q || !p->q_out)) || (Hkv && (!p->k || (p->append ? !p->v : !p->k_out))) || !p->positions || !p->table ||
+      (p->append && !p->slots))
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "%s: null pointer", what);
+  if (!al(p->q, 2) || !al(p->k, 2) || !al(p->v, 2) || !al(p->q_out, 2) || !al(p->k_out, 2))
+    return fail(AWQ_ERR_MISALIGNED, "16-bit tensors must be 2-byte aligned");
+  if (!al(p->positions, 4) || !al(p->table, 4) || !al(p->slots, 4))
+    return fail(AWQ_ERR_MISALIGNED, "positions, slots and table must be 4-byte aligned");
+  st = check_device();
+  if (st != AWQ_OK) return st;
+  p->T = T;
+  p->Hq = static_cast<int>(Hq);
+  p->Hkv = static_cast<int>(Hkv);
+  p->D = static_cast<int>(D);
+  p->rot = static_cast<int>(rotary_dim);
+  p->max_position = static_cast<int>(max_position);
+  p->bf16 = dtype == AWQ_DTYPE_BF16;
+  // dense outputs; in place: the input's strides
+  p->qo_st = p->q_out == p->q ? p->q_st : Hq * D;
+  p->qo_sh = p->q_out == p->q ? p->q_sh : D;
+  p->ko_st = p->k_out == p->k ? p->k_st : Hkv * D;
+  p->ko_sh = p->k_out == p->k ? p->k_sh : D;
+  const cudaError_t e = awq::launch_rope(*p);
+  if (e != cudaSuccess) return cuda_fail(e, what);
+  return ok();
+}
+
+// Shape rules of awq_attention_shared and its workspace; fills the host-side sizes of p.
+awq_status_t attention_shape(int64_t B, int64_t n, int64_t Hq, int64_t heads, int64_t D, int64_t prefix_len,
+                             int64_t max_len, awq::AttentionProblem* p) {
+  if (B < 0 || n < 0 || Hq < 0 || prefix_len < 0 || max_len < 0)
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "B, n, Hq, prefix_len, max_len must be >= 0");
+  if (heads <= 0 || Hq % heads)
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "Hq must be a multiple of the cache's heads (got %lld of %lld)",
+                (long long)Hq, (long long)heads);
+  if (!awq::attention_head_dim_supported(D))
+    return fail(AWQ_ERR_UNSUPPORTED_SHAPE, "head_dim must be 64, 96, 128 or 256 (got %lld)", (long long)D);
+  if (Hq > 65536 || B > kDimLimit || n > kDimLimit || prefix_len > kDimLimit || max_len > kDimLimit || B * n > kDimLimit ||
+      B * n * Hq > kDimLimit)
+    return fail(AWQ_ERR_UNSUPPORTED_SHAPE, "B * n * Hq, prefix_len and max_len must be below 2^31, Hq <= 65536");
+  p->B = static_cast<int>(B);
+  p->n = static_cast<int>(n);
+  p->Hq = static_cast<int>(Hq);
+  p->kv.heads = static_cast<int>(heads);
+  p->kv.head_dim = static_cast<int>(D);
+  p->prefix_len = prefix_len;
+  p->max_len = max_len;
+  return AWQ_OK;
+}
+
+awq_status_t dispatch_shape(int64_t T, int64_t k, int64_t E) {
+  if (T < 0) return fail(AWQ_ERR_INVALID_ARGUMENT, "T must be >= 0 (got %lld)", (long long)T);
+  if (E < 1 || E > awq::kDispatchMaxE)
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "E must be in 1..%d (got %lld)", awq::kDispatchMaxE, (long long)E);
+  if (k < 1 || k > 1024) return fail(AWQ_ERR_INVALID_ARGUMENT, "k must be in 1..1024 (got %lld)", (long long)k);
+  if (T > kDimLimit || T * k > kDimLimit) return fail(AWQ_ERR_UNSUPPORTED_SHAPE, "T * k must be below 2^31");
+  return AWQ_OK;
+}
+
+}  // namespace
+
+awq_status_t awq_rope_table(float* table, int64_t max_position, int64_t rotary_dim, double base,
+                            awq_rope_scaling_t scaling, double factor, int64_t original_max_position, double p0,
+                            double p1, double attention_factor, awq_stream_t stream) {
+  if (max_position < 0) return fail(AWQ_ERR_INVALID_ARGUMENT, "max_position must be >= 0");
+  if (rotary_dim < 2 || rotary_dim % 2) return fail(AWQ_ERR_INVALID_ARGUMENT, "rotary_dim must be even and >= 2");
+  if (max_position > kDimLimit || rotary_dim > 65536)
+    return fail(AWQ_ERR_UNSUPPORTED_SHAPE, "max_position must be below 2^31, rotary_dim <= 65536");
+  if (!(base > 1.0) || !(base < 1e300)) return fail(AWQ_ERR_INVALID_ARGUMENT, "base must be finite and > 1");
+  if (scaling < AWQ_ROPE_NONE || scaling > AWQ_ROPE_BANDED)
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "unknown scaling %d", static_cast<int>(scaling));
+  if (scaling != AWQ_ROPE_NONE && (!(factor > 0.0) || !(factor < 1e300)))
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "factor must be finite and > 0");
+  if (scaling == AWQ_ROPE_NTK && rotary_dim < 4) return fail(AWQ_ERR_INVALID_ARGUMENT, "NTK scaling needs rotary_dim >= 4");
+  if (scaling >= AWQ_ROPE_YARN && original_max_position <= 0)
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "original_max_position must be positive");
+  if (scaling == AWQ_ROPE_YARN && !(p0 > p1 && p1 > 0.0 && p0 < 1e300))
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "YARN needs p0 > p1 > 0");
+  if (scaling == AWQ_ROPE_BANDED && !(p1 > p0 && p0 > 0.0 && p1 < 1e300))
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "BANDED needs p1 > p0 > 0");
+  if (!(attention_factor > 0.0) || !(attention_factor < 1e30))
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "attention_factor must be finite and > 0");
+  if (max_position == 0) return ok();
+  if (!table) return fail(AWQ_ERR_INVALID_ARGUMENT, "null table");
+  if (!al(table, 4)) return fail(AWQ_ERR_MISALIGNED, "table must be 4-byte aligned");
+  const awq_status_t st = check_device();
+  if (st != AWQ_OK) return st;
+  const awq::RopeTableProblem p{table, max_position, static_cast<int>(rotary_dim), base, static_cast<int>(scaling), factor,
+                                static_cast<double>(original_max_position), p0, p1, attention_factor,
+                                reinterpret_cast<cudaStream_t>(stream)};
+  const cudaError_t e = awq::launch_rope_table(p);
+  if (e != cudaSuccess) return cuda_fail(e, "awq_rope_table launch");
+  return ok();
+}
+
+awq_status_t awq_rope(const void* q, const void* k, const int32_t* positions, const float* table, int64_t T, int64_t Hq,
+                      int64_t Hkv, int64_t D, int64_t rotary_dim, int64_t max_position, int64_t q_token_stride,
+                      int64_t q_head_stride, int64_t k_token_stride, int64_t k_head_stride, void* q_out, void* k_out,
+                      int interleaved, awq_dtype_t dtype, awq_stream_t stream) {
+  awq::RopeProblem p{};
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint16_t*>(k);
+  p.positions = positions;
+  p.table = table;
+  p.q_st = q_token_stride;
+  p.q_sh = q_head_stride;
+  p.k_st = k_token_stride;
+  p.k_sh = k_head_stride;
+  p.q_out = static_cast<uint16_t*>(q_out);
+  p.k_out = static_cast<uint16_t*>(k_out);
+  p.interleaved = interleaved != 0;
+  p.stream = reinterpret_cast<cudaStream_t>(stream);
+  return rope(&p, T, Hq, Hkv, D, rotary_dim, max_position, dtype, "awq_rope");
+}
+
+awq_status_t awq_rope_append(const void* q, const void* k, const void* v, const int32_t* positions, const float* table,
+                             int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t rotary_dim, int64_t max_position,
+                             int64_t q_token_stride, int64_t q_head_stride, int64_t k_token_stride, int64_t k_head_stride,
+                             int64_t v_token_stride, int64_t v_head_stride, void* q_out, const awq_paged_kv_t* cache,
+                             const int32_t* slots, int interleaved, awq_dtype_t dtype, awq_stream_t stream) {
+  awq::RopeProblem p{};
+  const awq_status_t st = check_cache(cache, &p.kv);
+  if (st != AWQ_OK) return st;
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.positions = positions;
+  p.table = table;
+  p.q_st = q_token_stride;
+  p.q_sh = q_head_stride;
+  p.k_st = k_token_stride;
+  p.k_sh = k_head_stride;
+  p.v_st = v_token_stride;
+  p.v_sh = v_head_stride;
+  p.q_out = static_cast<uint16_t*>(q_out);
+  p.slots = slots;
+  p.append = true;
+  p.interleaved = interleaved != 0;
+  p.stream = reinterpret_cast<cudaStream_t>(stream);
+  return rope(&p, T, Hq, Hkv, D, rotary_dim, max_position, dtype, "awq_rope_append");
+}
+
+awq_status_t awq_attention_shared_workspace_size(int64_t B, int64_t n, int64_t Hq, int64_t heads, int64_t D,
+                                                 int64_t prefix_len, int64_t max_len, size_t* bytes) {
+  if (!bytes) return fail(AWQ_ERR_INVALID_ARGUMENT, "null bytes pointer");
+  awq::AttentionProblem p{};
+  const awq_status_t st = attention_shape(B, n, Hq, heads, D, prefix_len, max_len, &p);
+  if (st != AWQ_OK) return st;
+  *bytes = B * n * Hq == 0 ? 0 : awq::attention_workspace_bytes(p, sm_count());
+  return ok();
+}
+
+awq_status_t awq_attention_shared(const void* q, int64_t B, int64_t n, int64_t Hq, int64_t q_batch_stride,
+                                  int64_t q_token_stride, int64_t q_head_stride, const awq_paged_kv_t* cache,
+                                  const int32_t* prefix_pages, int64_t prefix_len, const int32_t* pages, int64_t W,
+                                  int64_t pages_stride, const int32_t* lens, int64_t max_len, float scale, void* out,
+                                  awq_dtype_t dtype, void* workspace, size_t workspace_bytes, awq_stream_t stream) {
+  awq::AttentionProblem p{};
+  awq_status_t st = check_half(dtype);
+  if (st == AWQ_OK) st = check_cache(cache, &p.kv);
+  if (st == AWQ_OK) st = attention_shape(B, n, Hq, p.kv.heads, p.kv.head_dim, prefix_len, max_len, &p);
+  if (st != AWQ_OK) return st;
+  if (W < 0 || W > kDimLimit) return fail(AWQ_ERR_INVALID_ARGUMENT, "W must be in 0..2^31 - 1");
+  if (max_len > W * p.kv.page_size)
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "max_len %lld is more than W = %lld pages of %d tokens", (long long)max_len,
+                (long long)W, p.kv.page_size);
+  if (B * n * Hq == 0) return ok();
+  if (!q || !out || (prefix_len && !prefix_pages) || (max_len && (!pages || !lens)))
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "awq_attention_shared: null pointer");
+  if (!al(q, 16) || !al(out, 16) || !al(p.kv.k, 16) || !al(p.kv.v, 16))
+    return fail(AWQ_ERR_MISALIGNED, "q, out and the cache's tensors must be 16-byte aligned");
+  if (q_batch_stride % 8 || q_token_stride % 8 || q_head_stride % 8 || p.kv.page_stride % 8 || p.kv.token_stride % 8 ||
+      p.kv.head_stride % 8)
+    return fail(AWQ_ERR_MISALIGNED, "strides of q and the cache must be multiples of 8 elements");
+  if (!al(prefix_pages, 4) || !al(pages, 4) || !al(lens, 4))
+    return fail(AWQ_ERR_MISALIGNED, "prefix_pages, pages and lens must be 4-byte aligned");
+  st = check_device();
+  if (st != AWQ_OK) return st;
+  const int sms = sm_count();
+  const size_t need = awq::attention_workspace_bytes(p, sms);
+  if (need && !workspace) return fail(AWQ_ERR_INVALID_ARGUMENT, "null workspace");
+  if (!al(workspace, 256)) return fail(AWQ_ERR_MISALIGNED, "workspace must be 256-byte aligned");
+  if (workspace_bytes < need)
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "the workspace has %zu bytes, this call needs %zu", workspace_bytes, need);
+  p.q = static_cast<const uint16_t*>(q);
+  p.q_sb = q_batch_stride;
+  p.q_sn = q_token_stride;
+  p.q_sh = q_head_stride;
+  p.prefix_pages = prefix_pages;
+  p.pages = pages;
+  p.pages_ld = pages_stride;
+  p.W = static_cast<int>(W);
+  p.lens = lens;
+  p.scale = scale;
+  p.out = static_cast<uint16_t*>(out);
+  p.bf16 = dtype == AWQ_DTYPE_BF16;
+  p.workspace = workspace;
+  p.stream = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = awq::launch_attention(p, sms);
+  if (e != cudaSuccess) return cuda_fail(e, "awq_attention_shared launch");
+  return ok();
+}
+
+awq_status_t awq_moe_route(const void* logits, int64_t T, int64_t E, int64_t row_stride, awq_dtype_t dtype, int64_t k,
+                           int sigmoid, const float* bias, int64_t groups, int64_t topk_groups, int64_t group_best,
+                           int renormalize, float scale, float* weights, int32_t* experts, awq_stream_t stream) {
+  if (dtype != AWQ_DTYPE_F16 && dtype != AWQ_DTYPE_BF16 && dtype != AWQ_DTYPE_F32)
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "unknown dtype %d", static_cast<int>(dtype));
+  if (T < 0) return fail(AWQ_ERR_INVALID_ARGUMENT, "T must be >= 0 (got %lld)", (long long)T);
+  if (E < 1 || E > awq::kRouteMaxE)
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "E must be in 1..%d (got %lld)", awq::kRouteMaxE, (long long)E);
+  if (groups < 1 || groups > 32 || E % groups || topk_groups < 1 || topk_groups > groups)
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "groups must divide E, 1 <= topk_groups <= groups <= 32");
+  if (group_best != 1 && group_best != 2) return fail(AWQ_ERR_INVALID_ARGUMENT, "group_best must be 1 or 2");
+  if (k < 1 || k > awq::kRouteMaxK || k > E / groups * topk_groups)
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "k must be in 1..min(%d, E / groups * topk_groups) (got %lld)", awq::kRouteMaxK,
+                (long long)k);
+  if (T > kDimLimit || T * E >= kProdLimit) return fail(AWQ_ERR_UNSUPPORTED_SHAPE, "T must be below 2^31, T * E below 2^40");
+  if (T == 0) return ok();
+  if (!logits || !weights || !experts) return fail(AWQ_ERR_INVALID_ARGUMENT, "awq_moe_route: null pointer");
+  if (!al(logits, dtype == AWQ_DTYPE_F32 ? 4 : 2) || !al(bias, 4) || !al(weights, 4) || !al(experts, 4))
+    return fail(AWQ_ERR_MISALIGNED, "awq_moe_route: a tensor is not aligned to its elements");
+  const awq_status_t st = check_device();
+  if (st != AWQ_OK) return st;
+  const awq::RouteProblem p{logits, T, row_stride, static_cast<int>(E), static_cast<int>(k), static_cast<int>(dtype),
+                            sigmoid != 0, bias, static_cast<int>(groups), static_cast<int>(topk_groups),
+                            static_cast<int>(group_best), renormalize != 0, scale, weights, experts,
+                            reinterpret_cast<cudaStream_t>(stream)};
+  const cudaError_t e = awq::launch_route(p);
+  if (e != cudaSuccess) return cuda_fail(e, "awq_moe_route launch");
+  return ok();
+}
+
+awq_status_t awq_moe_dispatch_workspace_size(int64_t T, int64_t k, int64_t E, size_t* bytes) {
+  if (!bytes) return fail(AWQ_ERR_INVALID_ARGUMENT, "null bytes pointer");
+  const awq_status_t st = dispatch_shape(T, k, E);
+  if (st != AWQ_OK) return st;
+  *bytes = awq::dispatch_workspace_bytes(T * k, static_cast<int>(E));
+  return ok();
+}
+
+awq_status_t awq_moe_dispatch(const void* x, int64_t T, int64_t W, int64_t row_stride, const int32_t* experts, int64_t k,
+                              int64_t E, void* routed, int32_t* offsets, int32_t* rows, void* workspace,
+                              size_t workspace_bytes, awq_stream_t stream) {
+  awq_status_t st = dispatch_shape(T, k, E);
+  if (st != AWQ_OK) return st;
+  if (W < 0) return fail(AWQ_ERR_INVALID_ARGUMENT, "W must be >= 0 (got %lld)", (long long)W);
+  if (W > kDimLimit || T * k * W >= kProdLimit)
+    return fail(AWQ_ERR_UNSUPPORTED_SHAPE, "W must be below 2^31, T * k * W below 2^40");
+  if (!offsets || (T && (!experts || !rows || (W && (!x || !routed)))))
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "awq_moe_dispatch: null pointer");
+  if (!al(x, 2) || !al(routed, 2)) return fail(AWQ_ERR_MISALIGNED, "16-bit tensors must be 2-byte aligned");
+  if (!al(experts, 4) || !al(offsets, 4) || !al(rows, 4))
+    return fail(AWQ_ERR_MISALIGNED, "experts, offsets and rows must be 4-byte aligned");
+  st = check_device();
+  if (st != AWQ_OK) return st;
+  if (T == 0) {
+    const cudaError_t e = cudaMemsetAsync(offsets, 0, static_cast<size_t>(E + 1) * 4, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ok() : cuda_fail(e, "awq_moe_dispatch offsets");
+  }
+  const size_t need = awq::dispatch_workspace_bytes(T * k, static_cast<int>(E));
+  if (need && !workspace) return fail(AWQ_ERR_INVALID_ARGUMENT, "null workspace");
+  if (!al(workspace, 256)) return fail(AWQ_ERR_MISALIGNED, "workspace must be 256-byte aligned");
+  if (workspace_bytes < need)
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "the workspace has %zu bytes, this call needs %zu", workspace_bytes, need);
+  const awq::DispatchProblem p{static_cast<const uint16_t*>(x), T, row_stride, static_cast<int>(W), experts,
+                               static_cast<int>(k), static_cast<int>(E), static_cast<uint16_t*>(routed), offsets, rows,
+                               workspace, reinterpret_cast<cudaStream_t>(stream)};
+  const cudaError_t e = awq::launch_dispatch(p);
+  if (e != cudaSuccess) return cuda_fail(e, "awq_moe_dispatch launch");
+  return ok();
+}
+
+awq_status_t awq_moe_combine(const void* y, int64_t R, int64_t W, const float* weights, const int32_t* rows, int64_t T,
+                             int64_t k, const void* base, void* out, awq_dtype_t dtype, awq_stream_t stream) {
+  awq_status_t st = check_half(dtype);
+  if (st != AWQ_OK) return st;
+  if (R < 0 || W < 0 || T < 0) return fail(AWQ_ERR_INVALID_ARGUMENT, "R, W, T must be >= 0");
+  if (k < 0 || k > 1024) return fail(AWQ_ERR_INVALID_ARGUMENT, "k must be in 0..1024 (got %lld)", (long long)k);
+  if (R > kDimLimit || W > kDimLimit || T > kDimLimit || T * k > kDimLimit || R * W >= kProdLimit || T * W >= kProdLimit)
+    return fail(AWQ_ERR_UNSUPPORTED_SHAPE, "R, W, T * k must be below 2^31, R * W and T * W below 2^40");
+  if (T == 0 || W == 0) return ok();
+  if (!out || (R && !y) || (k && (!weights || !rows)))
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "awq_moe_combine: null pointer");
+  if (!al(y, 2) || !al(base, 2) || !al(out, 2)) return fail(AWQ_ERR_MISALIGNED, "16-bit tensors must be 2-byte aligned");
+  if (!al(weights, 4) || !al(rows, 4)) return fail(AWQ_ERR_MISALIGNED, "weights and rows must be 4-byte aligned");
+  st = check_device();
+  if (st != AWQ_OK) return st;
+  const awq::CombineProblem p{static_cast<const uint16_t*>(y), R, static_cast<int>(W), weights, rows, T,
+                              static_cast<int>(k), static_cast<const uint16_t*>(base), static_cast<uint16_t*>(out),
+                              dtype == AWQ_DTYPE_BF16, reinterpret_cast<cudaStream_t>(stream)};
+  const cudaError_t e = awq::launch_combine(p);
+  if (e != cudaSuccess) return cuda_fail(e, "awq_moe_combine launch");
   return ok();
 }
 
