@@ -12,58 +12,13 @@
 // Statistics, sums and parts are fp32; probabilities are rounded to the element type for the
 // second matrix product (the first factor of an mma has that type; the sum l uses the unrounded
 // ones), and the result is rounded once.
-#include "awq_layer.cuh"
-#include "awq_ptx.cuh"
+#include "awq_attn.cuh"
 
 namespace awq {
 namespace {
 
 using namespace ptx;
-
-constexpr float kLog2e = 1.4426950408889634f;
-
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-template <bool kBF>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  return static_cast<uint32_t>(float_to_elem<kBF>(lo)) | (static_cast<uint32_t>(float_to_elem<kBF>(hi)) << 16);
-}
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
-  const int bytes = valid ? 16 : 0;  // 0: the 16 bytes are zero-filled, nothing is read
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// How a call is cut.  Row r = (b n + i) Hq + h of the output; part s of row r is at
-// part_o[(r parts + s) D], part_ml[r parts + s]; parts [0, prefix_parts) are the prefix's, then one
-// per started `chunk` of the sequence's own keys.
-struct Plan {
-  int group;         // query heads per key/value head
-  int prefix_parts;  // cuts of the prefix
-  int prefix_chunk;  // its keys per part
-  int prefix_tiles;  // row tiles of the prefix, per key/value head
-  int chunk;         // private keys per part
-  int private_parts;  // parts of the longest sequence
-  int private_tiles;  // row tiles of one sequence
-  int parts;          // prefix_parts + private_parts
-  int mt;             // 16-row tiles per block
-};
-
-struct AttnArgs {
-  AttentionProblem p;
-  Plan plan;
-  float* part_o;
-  float2* part_ml;
-};
+using namespace attn;
 
 // ------------------------------------------------------------------------ streaming kernel ----
 
@@ -87,7 +42,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_stream_kernel(const AttnArgs
 
   // which rows, which keys
   int unit = blockIdx.x;
-  const int prefix_units = p.kv.heads * pl.prefix_tiles * pl.prefix_parts;
+  const int prefix_units = pl.tc ? 0 : p.kv.heads * pl.prefix_tiles * pl.prefix_parts;
   int b, hk, tile, part, rows, key0, key1, limit0;
   const int* table;
   if (unit < prefix_units) {
@@ -337,19 +292,28 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
   const int b = static_cast<int>(r / (static_cast<int64_t>(p.n) * p.Hq));
   int len = 0;
   if (pl.private_parts) len = min(max(__ldg(p.lens + b), 0), static_cast<int>(p.max_len));
-  const int parts = pl.prefix_parts + (pl.chunk ? (len + pl.chunk - 1) / pl.chunk : 0);
+  int first = pl.prefix_parts;  // parts of the prefix; the private ones follow at slot prefix_parts
+  if (pl.tc) {
+    const int h = static_cast<int>(r % p.Hq), hk = h / pl.group;
+    const int64_t stacked = r / p.Hq * pl.group + h % pl.group;
+    const int t = hk * pl.tc_tiles + static_cast<int>(stacked / kTcRows);
+    first = tc_last_block(pl, t) - tc_first_block(pl, t) + 1;
+  }
+  const int own = pl.chunk ? (len + pl.chunk - 1) / pl.chunk : 0;
+  const int parts = first + own, skip = pl.prefix_parts - first;  // slot of part s: s, from `first` on s + skip
   const float2* ml = a.part_ml + r * pl.parts;
   const float* src = a.part_o + r * pl.parts * D;
   float all = -INFINITY;
-  for (int s = 0; s < parts; ++s) all = fmaxf(all, ml[s].x);
+  for (int s = 0; s < parts; ++s) all = fmaxf(all, ml[s < first ? s : s + skip].x);
   const float ref = all == -INFINITY ? 0.f : all;
   constexpr int N = D / 32;
   float acc[N] = {}, l = 0.f;
   for (int s = 0; s < parts; ++s) {
-    const float f = exp2_approx(ml[s].x - ref);
-    l += ml[s].y * f;
+    const int slot = s < first ? s : s + skip;
+    const float f = exp2_approx(ml[slot].x - ref);
+    l += ml[slot].y * f;
 #pragma unroll
-    for (int c = 0; c < N; ++c) acc[c] += src[static_cast<int64_t>(s) * D + c * 32 + lane] * f;
+    for (int c = 0; c < N; ++c) acc[c] += src[static_cast<int64_t>(slot) * D + c * 32 + lane] * f;
   }
   const float inv = l > 0.f ? 1.f / l : 0.f;  // a row that sees no key is zero
 #pragma unroll
@@ -365,8 +329,17 @@ Plan make_plan(const AttentionProblem& p, int sms) {
   pl.mt = own_rows > 16 && p.kv.head_dim <= 128 ? 2 : 1;
   const int tile = 16 * pl.mt;
   const int64_t want = 2 * sms;  // blocks that fill the GPU
-  if (p.prefix_len > 0) {
-    pl.prefix_tiles = ceil_div(static_cast<int64_t>(p.B) * own_rows, tile);
+  const int64_t stacked = static_cast<int64_t>(p.B) * own_rows;  // rows that share a prefix key
+  pl.tc = p.prefix_len > 0 && tc_head_dim_supported(p.kv.head_dim) && stacked > 32;
+  if (pl.tc) {
+    pl.tc_tiles = ceil_div(stacked, kTcRows);
+    pl.tc_steps = ceil_div(p.prefix_len, kTcKeys);
+    const int64_t total = static_cast<int64_t>(p.kv.heads) * pl.tc_tiles * pl.tc_steps;
+    pl.tc_per = max(2, ceil_div(total, sms));
+    pl.tc_blocks = ceil_div(total, pl.tc_per);
+    pl.prefix_parts = min((pl.tc_steps - 1) / pl.tc_per + 2, pl.tc_blocks);
+  } else if (p.prefix_len > 0) {
+    pl.prefix_tiles = ceil_div(stacked, tile);
     const int64_t units = static_cast<int64_t>(p.kv.heads) * pl.prefix_tiles;
     const int cuts = static_cast<int>(max(int64_t{1}, min(static_cast<int64_t>(ceil_div(want, units)),
                                                           static_cast<int64_t>(ceil_div(p.prefix_len, 128)))));
@@ -391,7 +364,7 @@ cudaError_t run_stream(const AttnArgs& a) {
   constexpr int join = kWarps * 16 * MT * (2 + D + 4) * 4;
   constexpr int smem = ring > join ? ring : join;
   const Plan& pl = a.plan;
-  const int64_t units = static_cast<int64_t>(a.p.kv.heads) * pl.prefix_tiles * pl.prefix_parts +
+  const int64_t units = (pl.tc ? 0 : static_cast<int64_t>(a.p.kv.heads) * pl.prefix_tiles * pl.prefix_parts) +
                         static_cast<int64_t>(a.p.B) * a.p.kv.heads * pl.private_tiles * pl.private_parts;
   if (units == 0) return cudaSuccess;
   if (units > 0x7fffffff) return cudaErrorInvalidConfiguration;
@@ -403,7 +376,8 @@ cudaError_t run_stream(const AttnArgs& a) {
 
 template <bool kBF, int D>
 cudaError_t run(const AttnArgs& a) {
-  cudaError_t e;
+  cudaError_t e = a.plan.tc ? launch_prefix_tc(a) : cudaSuccess;
+  if (e != cudaSuccess) return e;
   if constexpr (D <= 128) e = a.plan.mt == 2 ? run_stream<kBF, D, 2>(a) : run_stream<kBF, D, 1>(a);
   else e = run_stream<kBF, D, 1>(a);
   if (e != cudaSuccess) return e;
@@ -433,7 +407,11 @@ size_t attention_workspace_bytes(const AttentionProblem& p, int sms) {
 }
 
 cudaError_t launch_attention(const AttentionProblem& p, int sms) {
-  AttnArgs a{p, make_plan(p, sms), nullptr, nullptr};
+  AttnArgs a{p, make_plan(p, sms), nullptr, nullptr, nullptr};
+  if (a.plan.tc) {
+    const cudaError_t e = status_word_ptr(&a.status);
+    if (e != cudaSuccess) return e;
+  }
   const size_t slots = static_cast<size_t>(p.B) * p.n * p.Hq * a.plan.parts;
   a.part_o = static_cast<float*>(p.workspace);
   a.part_ml = reinterpret_cast<float2*>(a.part_o + slots * p.kv.head_dim);

@@ -1,0 +1,520 @@
+// The prefix of awq_attention_shared on the tensor cores: the query rows of all sequences that
+// share a key/value head, stacked into tiles of 256, against the prefix's keys.
+//
+//   S = Q K^T (128 x 128 fp32 in TMEM),  P = exp2(scale log2(e) S - m),  O += P V (128 x D in TMEM)
+//
+// One block per SM.  All (tile, 128-key step) pairs form one sequence that is cut evenly over the
+// blocks (a tile's keys cut between blocks give one part each; the join kernel adds them), so the
+// SMs finish together whatever the number of tiles.
+//
+// Warps: 0-3 and 4-7 softmax of the tile's first and second 128 rows, one row per thread (a row's
+// maximum and sum need no shuffles); 8 and 9 load keys and values into a ring of five 128-token slots;
+// 10 issues the MMAs.  While one half's softmax runs, the tensor core works for the other half:
+// PV(a), QK(a) of the next step, PV(b), QK(b).  P, rounded to the element type, overwrites the S it
+// came from and is the MMA's A operand in TMEM; MMAs of one thread run in the order of issue, so the
+// next QK into S starts after the PV that reads P.
+//
+// The running maximum m of a row is raised only when it is exceeded by more than 2^8: until then P
+// holds values up to 256 and nothing is rescaled (O and the sum l use the same m, so the result is
+// unchanged; P keeps its relative accuracy).  A raise waits for the row's last PV and rescales O in
+// TMEM.
+#include "awq_attn.cuh"
+
+namespace awq {
+namespace {
+
+using namespace ptx;
+using namespace attn;
+
+constexpr int kThreads = 384;
+constexpr int kLoadWarps = 2;
+constexpr int kSlots = 5;  // ring of key / value tiles
+constexpr uint64_t kWaitLimitNs = 200ull * 1000 * 1000;
+constexpr unsigned int kStatusAttnTimeout = 0x8u;
+constexpr float kRaise = 8.f;  // log2 of the growth that raises a row's maximum
+constexpr uint32_t kTmemCols = 512;
+
+// TMEM columns: S / P of the two halves, then O of the two halves.
+constexpr uint32_t kColS = 0, kColO = 256;
+
+template <int D>
+struct Shape {
+  static constexpr int PANELS = (D + 63) / 64;       // 64 elements (128 bytes) of every row
+  static constexpr int PANEL = 128 * 128;            // 128 rows of 128 bytes, 128-byte swizzle
+  static constexpr int TILE = PANELS * PANEL;        // 128 rows of Q, K or V
+  static constexpr int Q_OFF = 0;
+  static constexpr int RING_OFF = 2 * TILE;
+  static constexpr int BAR_OFF = RING_OFF + kSlots * TILE;
+  // full[kSlots], empty[kSlots], q_full[2], s_full[2], p_full[2], pv_done[2], drain
+  static constexpr int NBARS = 2 * kSlots + 9;
+  static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;  // TMEM base, abort flag
+  static constexpr int SMEM = 1024 + MISC_OFF + 16;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Shared-memory operand descriptor, 128-byte swizzle.  K-major (Q, K: rows of 64 elements along the
+// contraction): sbo = 1024 between 8-row groups, lbo unused.  MN-major (V: rows are the contraction,
+// 64 elements along N): lbo between the 64-element panels, sbo = 1024 between 8-row groups.
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t lbo) {
+  uint64_t d = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;  // descriptor version
+  d |= static_cast<uint64_t>(2u) << 61;  // 128-byte swizzle
+  return d;
+}
+
+// Instruction descriptor, kind::f16, fp32 accumulators, M = 128.
+template <bool kBF, int N, bool kBMnMajor>
+__host__ __device__ constexpr uint32_t idesc() {
+  return (1u << 4) | (kBF ? (1u << 7) | (1u << 10) : 0u) | (kBMnMajor ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(128 >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]),
+        "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]),
+        "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]),
+        "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
+// Waits for every tcgen05.ld before it; the registers pass through, so no use moves above the wait.
+__device__ __forceinline__ void tmem_wait_ld32(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]),
+                 "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]),
+                 "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]),
+                 "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+               :
+               : "memory");
+}
+// 16 columns, complete on return.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]),
+        "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+      "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Two fp32 at a time.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// One 32-byte store.
+__device__ __forceinline__ void st_global8(float* p, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]),
+               "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
+template <bool kBF, int D>
+__global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_constant__ AttnArgs a) {
+  using SH = Shape<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + SH::BAR_OFF);
+  uint64_t* empty = full + kSlots;
+  uint64_t* q_full = empty + kSlots;
+  uint64_t* s_full = q_full + 2;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* pv_done = p_full + 2;
+  uint64_t* drain = pv_done + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SH::MISC_OFF);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+
+  const AttentionProblem& p = a.p;
+  const Plan& pl = a.plan;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&full[i], kLoadWarps);
+      mbar_init(&empty[i], 1);
+    }
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(&q_full[h], 4);  // the half's softmax warps
+      mbar_init(&s_full[h], 1);
+      mbar_init(&p_full[h], 4);
+      mbar_init(&pv_done[h], 1);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0u;
+    fence_mbar_init();
+  }
+  if (warp == 10) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "n"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // Bounded waits; a role that gives up sets the flag, and the others leave at their next wait.
+  // wait: all lanes of a warp, with one answer; wait1: one thread.
+  const auto gave_up = [&](uint64_t t0) -> bool {
+    if (*abort_flag) return true;
+    if (globaltimer_ns() - t0 <= kWaitLimitNs) return false;
+    atomicOr(a.status, kStatusAttnTimeout);
+    *abort_flag = 1u;
+    return true;
+  };
+  const auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (true) {
+      if (__all_sync(0xffffffffu, mbar_try_wait_hint(bar, parity, AWQ_MBAR_SUSPEND_HINT_NS))) return true;
+      if (__any_sync(0xffffffffu, gave_up(t0))) return false;
+    }
+  };
+  const auto wait1 = [&](uint64_t* bar, uint32_t parity) -> bool {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (true) {
+      if (mbar_try_wait_hint(bar, parity, AWQ_MBAR_SUSPEND_HINT_NS)) return true;
+      if (gave_up(t0)) return false;
+    }
+  };
+
+  // this block's steps, tile by tile
+  const int64_t total = static_cast<int64_t>(p.kv.heads) * pl.tc_tiles * pl.tc_steps;
+  const int64_t s_begin = static_cast<int64_t>(blockIdx.x) * pl.tc_per;
+  const int64_t s_end = min(total, s_begin + pl.tc_per);
+  const int stacked = p.B * p.n * pl.group;
+  struct Segment {
+    int hk, row0, halves, step0, steps, part;
+  };
+  const auto segment = [&](int64_t at) {
+    Segment s;
+    const int t = static_cast<int>(at / pl.tc_steps);
+    s.hk = t / pl.tc_tiles;
+    s.row0 = (t - s.hk * pl.tc_tiles) * kTcRows;
+    s.halves = stacked - s.row0 > 128 ? 2 : 1;
+    s.step0 = static_cast<int>(at - static_cast<int64_t>(t) * pl.tc_steps);
+    s.steps = static_cast<int>(min(static_cast<int64_t>(pl.tc_steps - s.step0), s_end - at));
+    s.part = static_cast<int>(blockIdx.x) - tc_first_block(pl, t);
+    return s;
+  };
+
+  if (warp < 8) {
+    // ------------------------------------------------------------------ softmax ----
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    [&] {
+      const int h = warp >> 2;
+      const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const uint32_t ts = tmem + lanes + kColS + h * 128, to = tmem + lanes + kColO + h * 128;
+      uint8_t* q_tile = smem + SH::Q_OFF + h * SH::TILE;
+      const int row = (warp & 3) * 32 + lane;  // of the half
+      // a negative scale goes to the query's sign bits, so that the largest S is the largest logit
+      const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
+      const float sl = fabsf(p.scale) * kLog2e;
+      uint32_t steps_done = 0, segs = 0;
+      for (int64_t at = s_begin; at < s_end;) {
+        const Segment sg = segment(at);
+        at += sg.steps;
+        if (h >= sg.halves) continue;
+        const int r = sg.row0 + h * 128 + row;
+        const bool in = r < stacked;
+        const int g = r % pl.group, bi = r / pl.group;
+        {
+          const uint16_t* src = p.q + static_cast<int64_t>(bi / p.n) * p.q_sb + static_cast<int64_t>(bi % p.n) * p.q_sn +
+                                static_cast<int64_t>(sg.hk * pl.group + g) * p.q_sh;
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) {
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (in) v = __ldg(reinterpret_cast<const uint4*>(src) + c);
+            v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
+            *reinterpret_cast<uint4*>(q_tile + (c >> 3) * SH::PANEL + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&q_full[h]);
+        }
+        float m = -INFINITY;
+        float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
+        for (int j = 0; j < sg.steps; ++j, ++steps_done) {
+          if (!wait(&s_full[h], steps_done & 1u)) return;
+          tc_fence_after();
+          float s[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, s + 32 * c);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_wait_ld32(s + 32 * c);
+          const int left = static_cast<int>(p.prefix_len) - (sg.step0 + j) * kTcKeys;
+          if (left < kTcKeys) {
+#pragma unroll
+            for (int i = 0; i < 128; ++i) s[i] = i < left ? s[i] : -INFINITY;
+          }
+          float mx[4] = {m, m, m, m};
+#pragma unroll
+          for (int i = 0; i < 128; i += 8) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], fmaxf(s[i + 2 * c], s[i + 2 * c + 1]));
+          }
+          const float now = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          const bool raise = (now - m) * sl > kRaise || (m == -INFINITY && now > m);
+          if (__any_sync(0xffffffffu, raise)) {
+            const float next = raise ? now : m;
+            const float f = raise ? exp2_approx((m - now) * sl) : 1.f;
+            sum0.x *= f, sum0.y *= f, sum1.x *= f, sum1.y *= f;
+            m = next;
+            if (j > 0) {
+              if (!wait(&pv_done[h], (steps_done - 1) & 1u)) return;
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t o[16];
+                tmem_ld16(to + 16 * c, o);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st16(to + 16 * c, o);
+              }
+            }
+          }
+          const float ref = m == -INFINITY ? 0.f : -m * sl;
+          const float2 sl2 = make_float2(sl, sl), ref2 = make_float2(ref, ref);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t u[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 z = fma2(make_float2(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), sl2, ref2);
+              const float2 e = make_float2(exp2_approx(z.x), exp2_approx(z.y));
+              if (i & 1) sum1 = add2(sum1, e);
+              else sum0 = add2(sum0, e);
+              u[i] = pack2<kBF>(e.x, e.y);
+            }
+            tmem_st16(ts + 16 * c, u);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[h]);
+        }
+        if (!wait(&pv_done[h], (steps_done - 1) & 1u)) return;
+        tc_fence_after();
+        const int64_t out_row = static_cast<int64_t>(bi) * p.Hq + sg.hk * pl.group + g;
+        const int64_t slot = out_row * pl.parts + sg.part;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          float o[32];
+          tmem_ld32(to + 32 * c, o);
+          tmem_wait_ld32(o);
+          if (in) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) st_global8(a.part_o + slot * D + 32 * c + i, o + i);
+          }
+        }
+        tc_fence_before();
+        if (in) a.part_ml[slot] = make_float2(m * sl, (sum0.x + sum0.y) + (sum1.x + sum1.y));
+        ++segs;
+      }
+    }();
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");  // one instruction for the four warps
+  }
+  if (warp >= 8 && warp < 8 + kLoadWarps) {
+    // ------------------------------------------------------------------- loads ----
+    constexpr int kMine = kTcKeys / kLoadWarps;  // keys of a tile that one warp loads
+    const int w = warp - 8;
+    uint32_t item = 0;       // tiles issued: keys, values, keys, ...
+    constexpr int kLag = 3;  // tiles in flight before the oldest is handed over
+    const auto hand_over = [&](uint32_t i) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[i % kSlots]);
+    };
+    [&] {
+      for (int64_t at = s_begin; at < s_end;) {
+        const Segment sg = segment(at);
+        at += sg.steps;
+        for (int j = 0; j < sg.steps; ++j) {
+          // off[i]: where this warp's key 32 i + lane starts
+          int64_t off[kMine / 32];
+#pragma unroll
+          for (int i = 0; i < kMine / 32; ++i) {
+            const int key = (sg.step0 + j) * kTcKeys + kMine * w + 32 * i + lane;
+            off[i] = -1;
+            if (key < p.prefix_len) {
+              const int slot = key / p.kv.page_size, page = __ldg(p.prefix_pages + slot);
+              if (page >= 0 && page < p.kv.num_pages)
+                off[i] = page * p.kv.page_stride + static_cast<int64_t>(key - slot * p.kv.page_size) * p.kv.token_stride +
+                         sg.hk * p.kv.head_stride;
+            }
+          }
+          for (int kv = 0; kv < 2; ++kv, ++item) {
+            if (item >= kSlots && !wait(&empty[item % kSlots], (item / kSlots - 1) & 1u)) return;
+            const uint16_t* base = kv ? p.kv.v : p.kv.k;
+            const uint32_t dst = smem_u32(smem + SH::RING_OFF + (item % kSlots) * SH::TILE) + kMine * w * 128;
+            constexpr int CH = D / 8;
+#pragma unroll
+            for (int b = 0; b < kMine / 32; ++b) {
+#pragma unroll 4
+              for (int i = 0; i < CH; ++i) {
+                const int x = i * 32 + lane, k = x / CH, c = x % CH;  // chunk c of the batch's key k
+                const int64_t o = __shfl_sync(0xffffffffu, off[b], k);
+                cp_async16(dst + (32 * b + k) * 128 + (c >> 3) * SH::PANEL + (((c & 7) ^ (k & 7)) << 4),
+                           base + (o < 0 ? 0 : o + c * 8), o >= 0);
+              }
+            }
+            cp_async_commit();
+            if (item >= kLag) {
+              cp_async_wait<kLag>();
+              hand_over(item - kLag);
+            }
+          }
+        }
+      }
+    }();
+    cp_async_wait<0>();
+    for (uint32_t i = item < kLag ? 0 : item - kLag; i < item; ++i) hand_over(i);
+  } else if (warp == 10) {
+    // -------------------------------------------------------------------- MMAs ----
+    if (lane == 0) {
+      [&] {
+        constexpr uint32_t kQK = idesc<kBF, kTcKeys, false>(), kPV = idesc<kBF, D, true>();
+        const uint32_t q_addr = smem_u32(smem + SH::Q_OFF), ring = smem_u32(smem + SH::RING_OFF);
+        uint32_t item = 0, segs[2] = {0, 0}, done[2] = {0, 0};
+        const auto qk = [&](int h, uint32_t slot) {
+          const uint64_t ad = sw128_desc(q_addr + h * SH::TILE, 0), bd = sw128_desc(ring + slot * SH::TILE, 0);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t o = ((k >> 2) * SH::PANEL + (k & 3) * 32) >> 4;
+            mma_ss(tmem + kColS + h * 128, ad + o, bd + o, kQK, k > 0);
+          }
+          mma_commit(&s_full[h]);
+        };
+        const auto pv = [&](int h, uint32_t slot, bool accumulate) {
+          const uint64_t bd = sw128_desc(ring + slot * SH::TILE, SH::PANEL);
+#pragma unroll
+          for (int k = 0; k < kTcKeys / 16; ++k)
+            mma_ts(tmem + kColO + h * 128, tmem + kColS + h * 128 + 8 * k, bd + ((k * 2048) >> 4), kPV, accumulate || k > 0);
+          mma_commit(&pv_done[h]);
+        };
+        for (int64_t at = s_begin; at < s_end;) {
+          const Segment sg = segment(at);
+          at += sg.steps;
+          const auto full_wait = [&](uint32_t i) { return wait1(&full[i % kSlots], (i / kSlots) & 1u); };
+          for (int h = 0; h < sg.halves; ++h) {
+            if (!wait1(&q_full[h], segs[h] & 1u)) return;
+            ++segs[h];
+          }
+          if (!full_wait(item)) return;
+          tc_fence_after();
+          for (int h = 0; h < sg.halves; ++h) qk(h, item % kSlots);
+          mma_commit(&empty[item % kSlots]);
+          for (int j = 0; j < sg.steps; ++j) {
+            const uint32_t v = item + 1, k_next = item + 2;
+            const bool more = j + 1 < sg.steps;
+            for (int h = 0; h < sg.halves; ++h) {
+              if (h == 0 && !full_wait(v)) return;
+              if (!wait1(&p_full[h], done[h] & 1u)) return;
+              ++done[h];
+              tc_fence_after();
+              pv(h, v % kSlots, j > 0);
+              if (h + 1 == sg.halves) mma_commit(&empty[v % kSlots]);
+              if (more) {
+                if (h == 0 && !full_wait(k_next)) return;
+                tc_fence_after();
+                qk(h, k_next % kSlots);
+                if (h + 1 == sg.halves) mma_commit(&empty[k_next % kSlots]);
+              }
+            }
+            item += 2;
+          }
+        }
+      }();
+      // nothing of this block may still run when TMEM is freed
+      mma_commit(drain);
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait_hint(drain, 0u, AWQ_MBAR_SUSPEND_HINT_NS) && globaltimer_ns() - t0 < kWaitLimitNs) {
+      }
+    }
+    __syncwarp();
+  }
+  __syncthreads();
+  if (warp == 10) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols) : "memory");
+  }
+}
+
+template <bool kBF, int D>
+cudaError_t run(const AttnArgs& a) {
+  const cudaError_t e =
+      cudaFuncSetAttribute(attn_prefix_kernel<kBF, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::SMEM);
+  if (e != cudaSuccess) return e;
+  attn_prefix_kernel<kBF, D><<<a.plan.tc_blocks, kThreads, Shape<D>::SMEM, a.p.stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool attn::tc_head_dim_supported(int D) { return D == 64 || D == 96 || D == 128; }
+
+cudaError_t attn::launch_prefix_tc(const AttnArgs& a) {
+  switch (a.p.kv.head_dim) {
+    case 64: return a.p.bf16 ? run<true, 64>(a) : run<false, 64>(a);
+    case 96: return a.p.bf16 ? run<true, 96>(a) : run<false, 96>(a);
+    default: return a.p.bf16 ? run<true, 128>(a) : run<false, 128>(a);
+  }
+}
+
+}  // namespace awq
