@@ -28,6 +28,12 @@ def awq():
     return awq
 
 
+@pytest.fixture(autouse=True)
+def no_wait_gave_up(awq):
+    yield
+    awq.device_status()
+
+
 def f64(t):
     return t.detach().cpu().double().numpy()
 
@@ -101,6 +107,44 @@ def test_attention(awq, case, dtype):
     d = make(B, n, hq, hkv, D, prefix, lens, page, dtype, seed=case)
     check(awq.awq_attention_shared(**d), d, dtype)
     assert torch.equal(awq.awq_attention_shared(**d), awq.awq_attention_shared(**d))
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("B,n,hq,hkv,D,prefix,private,page", [
+    (300, 1, 32, 16, 64, 2565, 40, 16),    # several steps of several tiles per block, the prefix's end among them
+    (75, 2, 32, 8, 128, 4097, 100, 32),
+    (130, 1, 16, 16, 96, 3000, 33, 24),    # pages that no TMA box divides
+    (64, 1, 64, 8, 128, 5000, 50, 128),
+])
+def test_many_rows(awq, B, n, hq, hkv, D, prefix, private, page, dtype):
+    g = torch.Generator(device="cuda").manual_seed(B)
+    lens = torch.randint(n, private + 1, (B,), generator=g, device="cuda")
+    shared, per = -(-prefix // page), -(-private // page)
+    order = torch.randperm(shared + B * per + 1, generator=g, device="cuda")
+    pp, pages = order[:shared], order[shared:shared + B * per].view(B, per)
+    live = torch.zeros((order.numel(), page), dtype=torch.bool, device="cuda")
+    live[pp] = (torch.arange(shared * page, device="cuda") < prefix).view(shared, page)
+    live[pages.reshape(-1)] = (torch.arange(per * page, device="cuda")[None] < lens[:, None]).view(B * per, page)
+    k, v = (torch.randn((order.numel(), page, hkv, D), generator=g, device="cuda").to(DT[dtype]).masked_fill_(
+        ~live[..., None, None], float("nan")) for _ in range(2))
+    q = (1.5 * torch.randn((B, n, hq, D), generator=g, device="cuda")).to(DT[dtype])
+    out = awq.awq_attention_shared(q, k, v, pp.int(), prefix, pages.int(), lens.int()).double()
+    scale, group, zmax = 1 / math.sqrt(D), hq // hkv, 0.0
+    pk, pv = (x[pp].reshape(-1, hkv, D)[:prefix].double() for x in (k, v))
+    for b in range(B):
+        count = int(lens[b])
+        kk, vv = (torch.cat([p, x[pages[b]].reshape(-1, hkv, D)[:count].double()]) for p, x in ((pk, k), (pv, v)))
+        qb = q[b].double().view(n, hkv, group, D)
+        z = scale * torch.einsum("nhgd,jhd->nhgj", qb, kk)
+        if b == 0:
+            zmax = 1.5 * float((scale * torch.einsum("nhgd,jhd->nhgj", qb.abs(), kk.abs())).max())
+        last = prefix + count - n + torch.arange(n, device="cuda")
+        z.masked_fill_(torch.arange(z.shape[-1], device="cuda") > last[:, None, None, None], float("-inf"))
+        w = torch.softmax(z, dim=-1)
+        want, spread = (torch.einsum("nhgj,jhd->nhgd", w, x).reshape(n, hq, D) for x in (vv, vv.abs()))
+        fp32 = 2 * 2.0 ** -22 * (D + 8) * zmax + 2.0 ** -22 * (prefix + private + 64)
+        tol = U[dtype] * want.abs() + (U[dtype] + fp32) * spread * (1 + U[dtype]) + (2.0 ** -24 if dtype == "fp16" else 0)
+        assert ((out[b] - want).abs() <= tol).all()
 
 
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])

@@ -8,8 +8,9 @@
 // SMs finish together whatever the number of tiles.
 //
 // Warps: 0-3 and 4-7 softmax of the tile's first and second 128 rows, one row per thread (a row's
-// maximum and sum need no shuffles); 8 and 9 load keys and values into a ring of five 128-token slots;
-// 10 issues the MMAs.  While one half's softmax runs, the tensor core works for the other half:
+// maximum and sum need no shuffles); 8 and 9 load keys and values into a ring of five 128-token slots
+// (TMA boxes of whole runs of a page's tokens; cp.async where pages are odd and where the prefix
+// ends); 10 issues the MMAs.  While one half's softmax runs, the tensor core works for the other half:
 // PV(a), QK(a) of the next step, PV(b), QK(b).  P, rounded to the element type, overwrites the S it
 // came from and is the MMA's A operand in TMEM; MMAs of one thread run in the order of issue, so the
 // next QK into S starts after the PV that reads P.
@@ -27,7 +28,6 @@ using namespace ptx;
 using namespace attn;
 
 constexpr int kThreads = 384;
-constexpr int kLoadWarps = 2;
 constexpr int kSlots = 5;  // ring of key / value tiles
 constexpr uint64_t kWaitLimitNs = 200ull * 1000 * 1000;
 constexpr unsigned int kStatusAttnTimeout = 0x8u;
@@ -54,6 +54,17 @@ struct Shape {
 
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)::"memory");
+  return r != 0u;
+}
 
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -163,8 +174,23 @@ __device__ __forceinline__ void st_global8(float* p, const float* v) {
                : "memory");
 }
 
+struct TcArgs : AttnArgs {
+  CUtensorMap map_k, map_v;  // the cache as [page][head][token][element]
+  int box_tokens;
+  bool tma;
+};
+
+// Copies a 64-element wide box of tokens.
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+
 template <bool kBF, int D>
-__global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_constant__ TcArgs a) {
   using SH = Shape<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -184,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&full[i], kLoadWarps);
+      mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
     for (int h = 0; h < 2; ++h) {
@@ -208,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
   const uint32_t tmem = *tmem_slot;
 
   // Bounded waits; a role that gives up sets the flag, and the others leave at their next wait.
-  // wait: all lanes of a warp, with one answer; wait1: one thread.
+  // All lanes of a warp wait together and get one answer.
   const auto gave_up = [&](uint64_t t0) -> bool {
     if (*abort_flag) return true;
     if (globaltimer_ns() - t0 <= kWaitLimitNs) return false;
@@ -222,14 +248,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
     while (true) {
       if (__all_sync(0xffffffffu, mbar_try_wait_hint(bar, parity, AWQ_MBAR_SUSPEND_HINT_NS))) return true;
       if (__any_sync(0xffffffffu, gave_up(t0))) return false;
-    }
-  };
-  const auto wait1 = [&](uint64_t* bar, uint32_t parity) -> bool {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    while (true) {
-      if (mbar_try_wait_hint(bar, parity, AWQ_MBAR_SUSPEND_HINT_NS)) return true;
-      if (gave_up(t0)) return false;
     }
   };
 
@@ -370,12 +388,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");  // one instruction for the four warps
   }
-  if (warp >= 8 && warp < 8 + kLoadWarps) {
+  if (warp == 8 || warp == 9) {
     // ------------------------------------------------------------------- loads ----
-    constexpr int kMine = kTcKeys / kLoadWarps;  // keys of a tile that one warp loads
-    const int w = warp - 8;
-    uint32_t item = 0;       // tiles issued: keys, values, keys, ...
-    constexpr int kLag = 3;  // tiles in flight before the oldest is handed over
+    // warp 8 loads the steps' keys (ring tiles 0, 2, ...), warp 9 their values (1, 3, ...)
+    const int kv = warp - 8;
+    const uint16_t* base = kv ? p.kv.v : p.kv.k;
+    const CUtensorMap* map = kv ? &a.map_v : &a.map_k;
+    const int boxes = kTcKeys / a.box_tokens;  // TMA boxes of a whole step
+    uint32_t item = kv, pending = ~0u;         // pending: tile copied by cp.async, not handed over yet
     const auto hand_over = [&](uint32_t i) {
       fence_proxy_async_smem();
       __syncwarp();
@@ -385,107 +405,145 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
       for (int64_t at = s_begin; at < s_end;) {
         const Segment sg = segment(at);
         at += sg.steps;
-        for (int j = 0; j < sg.steps; ++j) {
-          // off[i]: where this warp's key 32 i + lane starts
-          int64_t off[kMine / 32];
+        for (int j = 0; j < sg.steps; ++j, item += 2) {
+          const int key0 = (sg.step0 + j) * kTcKeys;
+          if (item >= kSlots && !wait(&empty[item % kSlots], (item / kSlots - 1) & 1u)) return;
+          uint8_t* tile = smem + SH::RING_OFF + (item % kSlots) * SH::TILE;
+          if (a.tma && key0 + kTcKeys <= p.prefix_len) {
+            // whole step: one box of 64 elements per panel and run of tokens within a page
+            int page = 0, token = 0;
+            if (lane < boxes) {
+              const int key = key0 + lane * a.box_tokens, slot = key / p.kv.page_size;
+              page = __ldg(p.prefix_pages + slot);
+              token = key - slot * p.kv.page_size;
+            }
+            if (elect_one()) mbar_arrive_expect_tx(&full[item % kSlots], SH::TILE);
+            __syncwarp();
+            for (int i = 0; i < boxes; ++i) {
+              const int pg = __shfl_sync(0xffffffffu, page, i), tk = __shfl_sync(0xffffffffu, token, i);
+              if (elect_one()) {
 #pragma unroll
-          for (int i = 0; i < kMine / 32; ++i) {
-            const int key = (sg.step0 + j) * kTcKeys + kMine * w + 32 * i + lane;
-            off[i] = -1;
+                for (int n = 0; n < SH::PANELS; ++n)
+                  tma_load_4d(tile + n * SH::PANEL + i * a.box_tokens * 128, map, &full[item % kSlots], 64 * n, tk, sg.hk, pg);
+              }
+              __syncwarp();
+            }
+            continue;
+          }
+          // odd pages, or the step the prefix ends in (zero-filled: what follows may be anything)
+          constexpr int CH = D / 8;
+          const uint32_t dst = smem_u32(tile);
+#pragma unroll 1
+          for (int b = 0; b < kTcKeys / 32; ++b) {
+            const int key = key0 + 32 * b + lane;
+            int64_t off = -1;
             if (key < p.prefix_len) {
               const int slot = key / p.kv.page_size, page = __ldg(p.prefix_pages + slot);
               if (page >= 0 && page < p.kv.num_pages)
-                off[i] = page * p.kv.page_stride + static_cast<int64_t>(key - slot * p.kv.page_size) * p.kv.token_stride +
-                         sg.hk * p.kv.head_stride;
+                off = page * p.kv.page_stride + static_cast<int64_t>(key - slot * p.kv.page_size) * p.kv.token_stride +
+                      sg.hk * p.kv.head_stride;
             }
-          }
-          for (int kv = 0; kv < 2; ++kv, ++item) {
-            if (item >= kSlots && !wait(&empty[item % kSlots], (item / kSlots - 1) & 1u)) return;
-            const uint16_t* base = kv ? p.kv.v : p.kv.k;
-            const uint32_t dst = smem_u32(smem + SH::RING_OFF + (item % kSlots) * SH::TILE) + kMine * w * 128;
-            constexpr int CH = D / 8;
 #pragma unroll
-            for (int b = 0; b < kMine / 32; ++b) {
-#pragma unroll 4
-              for (int i = 0; i < CH; ++i) {
-                const int x = i * 32 + lane, k = x / CH, c = x % CH;  // chunk c of the batch's key k
-                const int64_t o = __shfl_sync(0xffffffffu, off[b], k);
-                cp_async16(dst + (32 * b + k) * 128 + (c >> 3) * SH::PANEL + (((c & 7) ^ (k & 7)) << 4),
-                           base + (o < 0 ? 0 : o + c * 8), o >= 0);
-              }
-            }
-            cp_async_commit();
-            if (item >= kLag) {
-              cp_async_wait<kLag>();
-              hand_over(item - kLag);
+            for (int i = 0; i < CH; ++i) {
+              const int x = i * 32 + lane, k = x / CH, c = x % CH;  // chunk c of the batch's key k
+              const int64_t o = __shfl_sync(0xffffffffu, off, k);
+              cp_async16(dst + (32 * b + k) * 128 + (c >> 3) * SH::PANEL + (((c & 7) ^ (k & 7)) << 4),
+                         base + (o < 0 ? 0 : o + c * 8), o >= 0);
             }
           }
+          cp_async_commit();
+          if (a.tma) {  // the prefix's last step: the next ones come by TMA
+            cp_async_wait<0>();
+            hand_over(item);
+            continue;
+          }
+          if (pending != ~0u) {
+            cp_async_wait<1>();
+            hand_over(pending);
+          }
+          pending = item;
         }
       }
     }();
     cp_async_wait<0>();
-    for (uint32_t i = item < kLag ? 0 : item - kLag; i < item; ++i) hand_over(i);
+    if (pending != ~0u) hand_over(pending);
   } else if (warp == 10) {
     // -------------------------------------------------------------------- MMAs ----
-    if (lane == 0) {
-      [&] {
-        constexpr uint32_t kQK = idesc<kBF, kTcKeys, false>(), kPV = idesc<kBF, D, true>();
-        const uint32_t q_addr = smem_u32(smem + SH::Q_OFF), ring = smem_u32(smem + SH::RING_OFF);
-        uint32_t item = 0, segs[2] = {0, 0}, done[2] = {0, 0};
-        const auto qk = [&](int h, uint32_t slot) {
-          const uint64_t ad = sw128_desc(q_addr + h * SH::TILE, 0), bd = sw128_desc(ring + slot * SH::TILE, 0);
+    // The whole warp runs the loop and one elected lane issues: every operand is the same in all
+    // lanes, so it lives in uniform registers (inside a one-lane branch each MMA would cost a loop
+    // over the lanes' values, 130 cycles instead of the tensor core's 64).
+    [&] {
+      constexpr uint32_t kQK = idesc<kBF, kTcKeys, false>(), kPV = idesc<kBF, D, true>();
+      const uint32_t q_addr = smem_u32(smem + SH::Q_OFF), ring = smem_u32(smem + SH::RING_OFF);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      uint32_t slot = 0, phase = 0;  // of the next ring tile
+      uint32_t segs0 = 0, segs1 = 0, done0 = 0, done1 = 0;
+      const auto next = [&] {
+        if (++slot == kSlots) slot = 0, phase ^= 1u;
+      };
+      const auto qk = [&](uint32_t h, uint32_t sl, bool last) {
+        const uint64_t ad = sw128_desc(q_addr + h * SH::TILE, 0), bd = sw128_desc(ring + sl * SH::TILE, 0);
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint32_t o = ((k >> 2) * SH::PANEL + (k & 3) * 32) >> 4;
-            mma_ss(tmem + kColS + h * 128, ad + o, bd + o, kQK, k > 0);
+            mma_ss(tm + kColS + h * 128, ad + o, bd + o, kQK, k > 0);
           }
           mma_commit(&s_full[h]);
-        };
-        const auto pv = [&](int h, uint32_t slot, bool accumulate) {
-          const uint64_t bd = sw128_desc(ring + slot * SH::TILE, SH::PANEL);
+          if (last) mma_commit(&empty[sl]);
+        }
+        __syncwarp();
+      };
+      const auto pv = [&](uint32_t h, uint32_t sl, bool accumulate, bool last) {
+        const uint64_t bd = sw128_desc(ring + sl * SH::TILE, SH::PANEL);
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < kTcKeys / 16; ++k)
-            mma_ts(tmem + kColO + h * 128, tmem + kColS + h * 128 + 8 * k, bd + ((k * 2048) >> 4), kPV, accumulate || k > 0);
+            mma_ts(tm + kColO + h * 128, tm + kColS + h * 128 + 8 * k, bd + ((k * 2048) >> 4), kPV, accumulate || k > 0);
           mma_commit(&pv_done[h]);
-        };
-        for (int64_t at = s_begin; at < s_end;) {
-          const Segment sg = segment(at);
-          at += sg.steps;
-          const auto full_wait = [&](uint32_t i) { return wait1(&full[i % kSlots], (i / kSlots) & 1u); };
-          for (int h = 0; h < sg.halves; ++h) {
-            if (!wait1(&q_full[h], segs[h] & 1u)) return;
-            ++segs[h];
-          }
-          if (!full_wait(item)) return;
+          if (last) mma_commit(&empty[sl]);
+        }
+        __syncwarp();
+      };
+      for (int64_t at = s_begin; at < s_end;) {
+        const Segment sg = segment(at);
+        at += sg.steps;
+        const bool two = sg.halves == 2;
+        if (!wait(&q_full[0], segs0++ & 1u)) return;
+        if (two && !wait(&q_full[1], segs1++ & 1u)) return;
+        if (!wait(&full[slot], phase)) return;
+        tc_fence_after();
+        qk(0, slot, !two);
+        if (two) qk(1, slot, true);
+        next();
+        for (int j = 0; j < sg.steps; ++j) {
+          const bool more = j + 1 < sg.steps;
+          const uint32_t v = slot, v_phase = phase;
+          next();
+          const uint32_t k = slot, k_phase = phase;
+          if (more) next();
+          if (!wait(&full[v], v_phase) || !wait(&p_full[0], done0++ & 1u)) return;
           tc_fence_after();
-          for (int h = 0; h < sg.halves; ++h) qk(h, item % kSlots);
-          mma_commit(&empty[item % kSlots]);
-          for (int j = 0; j < sg.steps; ++j) {
-            const uint32_t v = item + 1, k_next = item + 2;
-            const bool more = j + 1 < sg.steps;
-            for (int h = 0; h < sg.halves; ++h) {
-              if (h == 0 && !full_wait(v)) return;
-              if (!wait1(&p_full[h], done[h] & 1u)) return;
-              ++done[h];
-              tc_fence_after();
-              pv(h, v % kSlots, j > 0);
-              if (h + 1 == sg.halves) mma_commit(&empty[v % kSlots]);
-              if (more) {
-                if (h == 0 && !full_wait(k_next)) return;
-                tc_fence_after();
-                qk(h, k_next % kSlots);
-                if (h + 1 == sg.halves) mma_commit(&empty[k_next % kSlots]);
-              }
-            }
-            item += 2;
+          pv(0, v, j > 0, !two);
+          if (more) {
+            if (!wait(&full[k], k_phase)) return;
+            tc_fence_after();
+            qk(0, k, !two);
+          }
+          if (two) {
+            if (!wait(&p_full[1], done1++ & 1u)) return;
+            tc_fence_after();
+            pv(1, v, j > 0, true);
+            if (more) qk(1, k, true);
           }
         }
-      }();
-      // nothing of this block may still run when TMEM is freed
-      mma_commit(drain);
-      const uint64_t t0 = globaltimer_ns();
-      while (!mbar_try_wait_hint(drain, 0u, AWQ_MBAR_SUSPEND_HINT_NS) && globaltimer_ns() - t0 < kWaitLimitNs) {
       }
+    }();
+    // nothing of this block may still run when TMEM is freed
+    if (elect_one()) mma_commit(drain);
+    __syncwarp();
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait_hint(drain, 0u, AWQ_MBAR_SUSPEND_HINT_NS) && globaltimer_ns() - t0 < kWaitLimitNs) {
     }
     __syncwarp();
   }
@@ -496,8 +554,31 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
   }
 }
 
+bool make_map(CUtensorMap* map, const void* base, const AttentionProblem& p, int box) {
+  const uint64_t dims[4] = {static_cast<uint64_t>(p.kv.head_dim), static_cast<uint64_t>(p.kv.page_size),
+                            static_cast<uint64_t>(p.kv.heads), static_cast<uint64_t>(p.kv.num_pages)};
+  const uint64_t strides[3] = {static_cast<uint64_t>(p.kv.token_stride) * 2, static_cast<uint64_t>(p.kv.head_stride) * 2,
+                               static_cast<uint64_t>(p.kv.page_stride) * 2};
+  const uint32_t boxes[4] = {64, static_cast<uint32_t>(box), 1, 1};
+  return make_tmap_4d(map, p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, dims, strides,
+                      boxes, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Tokens of a TMA box: a step is whole boxes and no box crosses a page; 0: the pages do not allow it
+// (a box's rows must start at a multiple of 8, where the swizzle pattern repeats).
+int box_tokens(int page_size) {
+  if (page_size % kTcKeys == 0) return kTcKeys;
+  return page_size >= 8 && kTcKeys % page_size == 0 ? page_size : 0;
+}
+
 template <bool kBF, int D>
-cudaError_t run(const AttnArgs& a) {
+cudaError_t run(const AttnArgs& attn) {
+  TcArgs a{};
+  static_cast<AttnArgs&>(a) = attn;
+  a.box_tokens = box_tokens(attn.p.kv.page_size);
+  a.tma = a.box_tokens > 0 && attn.p.prefix_len >= kTcKeys &&
+          make_map(&a.map_k, attn.p.kv.k, attn.p, a.box_tokens) && make_map(&a.map_v, attn.p.kv.v, attn.p, a.box_tokens);
+  if (!a.tma) a.box_tokens = kTcKeys;
   const cudaError_t e =
       cudaFuncSetAttribute(attn_prefix_kernel<kBF, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::SMEM);
   if (e != cudaSuccess) return e;

@@ -77,6 +77,10 @@ bool make_tmap_2d(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t elem_byt
                   const void* base, uint64_t dim0, uint64_t dim1, uint32_t box0, uint32_t box1,
                   CUtensorMapSwizzle swizzle, const char** why);
 
+// 4D tensor map with explicit byte strides (dimensions 1 to 3); false if the driver rejects it.
+bool make_tmap_4d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, const uint64_t (&dims)[4],
+                  const uint64_t (&strides)[3], const uint32_t (&box)[4], CUtensorMapSwizzle swizzle);
+
 // Device address of the status word on the current device (bounded waits that give up
 // OR a code into it).
 cudaError_t status_word_ptr(unsigned int** ptr);
