@@ -22,265 +22,342 @@ using namespace attn;
 
 // ------------------------------------------------------------------------ streaming kernel ----
 
-constexpr int kWarps = 4;
-constexpr int kKeys = 16;    // keys of one warp's step
-constexpr int kStages = 3;   // steps in flight per warp
+// An 8 x 8 tile of 16-bit elements, one row per four lanes, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
 
-// One block: one row tile (16 MT query rows that share a key/value head) against one run of keys.
-// Warp w takes the steps w, w + 4, ...; it copies its own keys and values (cp.async, zero-filled
-// past the run's end: what lies there may be anything) and keeps its own (m, l, o), so that warps
-// meet only at the end.  Shared rows are padded by 16 bytes: eight rows of a matrix fragment fall
-// into different banks for every head size.
-template <bool kBF, int D, int MT>
-__global__ void __launch_bounds__(kWarps * 32) attn_stream_kernel(const AttnArgs a) {
-  constexpr int PITCH = D + 8;
-  constexpr int STEP = 2 * kKeys * PITCH;  // elements of one stage: keys, then values
+template <int D>
+struct Stream {
+  static constexpr int PITCH = D + 8;  // elements: eight rows of a fragment fall into different banks
+  static constexpr int STEP = 2 * kStreamKeys * PITCH;                // keys, then values
+  static constexpr int STAGES = D <= 64 ? 5 : D <= 96 ? 4 : 3;        // steps in flight per warp
+  static constexpr int BLOCKS = D <= 128 ? 2 : 1;                     // blocks per SM
+  static constexpr int COARSE = 256;                                  // entries of the table of lengths
+  static constexpr int RING = kStreamWarps * STAGES * STEP * 2;
+  static constexpr int SMEM = RING + COARSE * 8 + 16;
+  static_assert(BLOCKS * (SMEM + 1024) <= 228 * 1024, "shared memory");
+};
+
+// Where a warp stands: a unit and a step of it.
+struct Cursor {
+  int b;       // sequence, -1: the prefix
+  int unit;    // tile * heads + head
+  int step, steps;
+  int len;
+};
+
+// Each warp works alone: it copies its own keys and values (cp.async into a ring, zero-filled past
+// the sequence's end: what lies there may be anything), keeps its own (m, l, o), and writes a part
+// when its unit or its share ends.  Its copies run ahead across units, so the memory system is busy
+// from the first step to the last; 2 blocks of 4 warps per SM keep about 140 KB per SM in flight.
+//
+// The products are taken transposed, S^T = K Q^T and O^T += V^T P^T: keys (then elements) fill the 16
+// rows of an m16n8k16 and 8 query rows its columns, so that the usual 8 heads of a group waste
+// nothing and the accumulators are half those of Q K^T.
+template <bool kBF, int D, int NT>
+__global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_stream_kernel(const AttnArgs a) {
+  using ST = Stream<D>;
+  constexpr int PITCH = ST::PITCH, STAGES = ST::STAGES;
   extern __shared__ __align__(16) uint16_t smem[];
   const AttentionProblem& p = a.p;
   const Plan& pl = a.plan;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int64_t* coarse = reinterpret_cast<int64_t*>(reinterpret_cast<uint8_t*>(smem) + ST::RING);
+  const int heads = p.kv.heads, max_len = static_cast<int>(p.max_len), prefix_len = static_cast<int>(p.prefix_len);
+  const auto length = [&](int b) { return b < p.B ? min(max(__ldg(p.lens + b), 0), max_len) : 0; };
+  const auto steps_of = [](int len) { return (len + kStreamKeys - 1) / kStreamKeys; };
 
-  // which rows, which keys
-  int unit = blockIdx.x;
-  const int prefix_units = pl.tc ? 0 : p.kv.heads * pl.prefix_tiles * pl.prefix_parts;
-  int b, hk, tile, part, rows, key0, key1, limit0;
-  const int* table;
-  if (unit < prefix_units) {
-    part = unit % pl.prefix_parts;
-    unit /= pl.prefix_parts;
-    tile = unit % pl.prefix_tiles;
-    hk = unit / pl.prefix_tiles;
-    b = 0;
-    rows = p.B * p.n * pl.group;
-    key0 = part * pl.prefix_chunk;
-    key1 = min(static_cast<int>(p.prefix_len), key0 + pl.prefix_chunk);
-    limit0 = key1;  // every row sees the whole run
-    table = p.prefix_pages;
-  } else {
-    unit -= prefix_units;
-    hk = unit % p.kv.heads;
-    unit /= p.kv.heads;
-    tile = unit % pl.private_tiles;
-    unit /= pl.private_tiles;
-    part = unit % pl.private_parts;
-    b = unit / pl.private_parts;
-    rows = p.n * pl.group;
-    const int len = min(max(__ldg(p.lens + b), 0), static_cast<int>(p.max_len));
-    key0 = part * pl.chunk;
-    key1 = min(len, key0 + pl.chunk);
-    limit0 = len - p.n + 1;  // query token i sees keys below limit0 + i
-    if (key0 >= key1) return;
-    part += pl.prefix_parts;
-    table = p.pages + b * p.pages_ld;
-  }
-  const bool own = part >= pl.prefix_parts;
-  const int row0 = tile * 16 * MT;
-
-  // address of a key's elements, or of any valid memory with valid = false
-  const auto locate = [&](int key, const uint16_t* base, bool* valid) -> const uint16_t* {
-    *valid = false;
-    if (key >= key1) return base;
-    const int slot = key / p.kv.page_size, page = __ldg(table + slot);
-    if (page < 0 || page >= p.kv.num_pages) return base;
-    *valid = true;
-    return base + page * p.kv.page_stride + static_cast<int64_t>(key - slot * p.kv.page_size) * p.kv.token_stride +
-           hk * p.kv.head_stride;
-  };
-  uint16_t* ring = smem + warp * kStages * STEP;
-  const auto load_step = [&](int step) {  // step: index among all of the run's 16-key steps
-    const int k0 = key0 + step * kKeys;
-    if (k0 < key1) {
-      uint16_t* st = ring + (step / kWarps) % kStages * STEP;
-      constexpr int CH = D / 8;
-      // each lane copies half of a key's and half of a value's elements
-      const int key = lane >> 1, half = lane & 1;
-      bool valid;
-      const uint16_t* base = locate(k0 + key, p.kv.k, &valid);
-      const int64_t off = base - p.kv.k;
-      const uint32_t dk = smem_u32(st + key * PITCH), dv = smem_u32(st + (kKeys + key) * PITCH);
+  // coarse[g]: steps (of one unit each) of the sequences before g * gran; its last entry: of all
+  const int gran = (p.B + ST::COARSE - 2) / (ST::COARSE - 1);
+  if (pl.private_parts) {
+    for (int g = threadIdx.x; g < ST::COARSE; g += kStreamWarps * 32) {
+      int64_t n = 0;
+      const int b1 = min(p.B, (g + 1) * gran);
+      for (int b = g * gran; b < b1; ++b) n += steps_of(length(b));
+      coarse[g] = n;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      constexpr int E = ST::COARSE / 32;
+      int64_t v[E], run = 0;
 #pragma unroll
-      for (int c = 0; c < CH / 2; ++c) {
-        const int e = (2 * c + half) * 8;
-        const int64_t from = valid ? off + e : 0;
-        cp_async16(dk + e * 2, p.kv.k + from, valid);
-        cp_async16(dv + e * 2, p.kv.v + from, valid);
+      for (int i = 0; i < E; ++i) v[i] = coarse[lane * E + i];
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const int64_t c = v[i];
+        v[i] = run;
+        run += c;
       }
+      int64_t before = run;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, before, d);
+        if (lane >= d) before += o;
+      }
+      before -= run;
+#pragma unroll
+      for (int i = 0; i < E; ++i) coarse[lane * E + i] = before + v[i];
+    }
+    __syncthreads();
+  }
+  const int64_t prefix_total = pl.tc ? 0 : static_cast<int64_t>(steps_of(prefix_len)) * heads * pl.prefix_tiles;
+  const int64_t per_seq = static_cast<int64_t>(heads) * pl.private_tiles;  // units of a sequence
+  const int64_t total = prefix_total + (pl.private_parts ? coarse[ST::COARSE - 1] * per_seq : 0);
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * kStreamWarps;
+  const int64_t per = max(static_cast<int64_t>(pl.per_min), (total + warps - 1) / warps);
+  // neighbouring warps of the sequence sit on different SMs' schedulers only by block; order as numbered
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * kStreamWarps + warp;
+  const int64_t x0 = w * per, x1 = min(total, x0 + per);
+  if (x0 >= x1) return;
+
+  // the first step's unit
+  Cursor at;
+  int64_t unit_start;  // of the unit's first step, among all
+  if (x0 < prefix_total) {
+    at.b = -1;
+    at.len = prefix_len;
+    at.steps = steps_of(prefix_len);
+    at.unit = static_cast<int>(x0 / at.steps);
+    at.step = static_cast<int>(x0 - static_cast<int64_t>(at.unit) * at.steps);
+  } else {
+    const int64_t q = (x0 - prefix_total) / per_seq;  // in steps of one unit per sequence
+    int lo = 0, hi = ST::COARSE - 1;                  // coarse[lo] <= q < coarse[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (coarse[mid] <= q) lo = mid;
+      else hi = mid;
+    }
+    int64_t before = coarse[lo];
+    int b0 = lo * gran;
+    while (true) {  // 32 sequences at a time
+      const int n = steps_of(length(b0 + lane));
+      int incl = n;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += o;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, before + incl > q);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        before += __shfl_sync(0xffffffffu, incl - n, l);
+        at.b = b0 + l;
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, incl, 31);
+      b0 += 32;
+      if (b0 >= p.B) return;  // not reached: q lies below the last entry
+    }
+    at.len = length(at.b);
+    at.steps = steps_of(at.len);
+    const int64_t rem = x0 - prefix_total - before * per_seq;
+    at.unit = static_cast<int>(rem / at.steps);
+    at.step = static_cast<int>(rem - static_cast<int64_t>(at.unit) * at.steps);
+  }
+  unit_start = x0 - at.step;
+  const auto advance = [&](Cursor& c) {  // to the first step of the next unit
+    c.step = 0;
+    const int units = heads * (c.b < 0 ? pl.prefix_tiles : pl.private_tiles);
+    if (++c.unit < units) return;
+    c.unit = 0;
+    do {
+      ++c.b;
+      c.len = length(c.b);
+    } while (c.len == 0 && c.b < p.B);
+    c.steps = steps_of(c.len);
+  };
+
+  // Copies: 32 lanes take whole rows, so that every line is asked for once.  Lane l < 16 holds where
+  // key l of the next step to load starts; its page was read a step earlier.
+  constexpr int CH = D / 8;  // 16-byte chunks of a row
+  uint16_t* ring = smem + warp * STAGES * ST::STEP;
+  Cursor ahead = at;
+  int64_t to_load = x1 - x0;
+  uint32_t loaded = 0;  // steps
+  int page_next = 0;
+  const auto fetch_page = [&] {
+    const int key = ahead.step * kStreamKeys + (lane & 15);
+    const int* table = ahead.b < 0 ? p.prefix_pages : p.pages + ahead.b * p.pages_ld;
+    page_next = key < ahead.len ? __ldg(table + key / p.kv.page_size) : -1;
+  };
+  const auto load_step = [&] {
+    if (to_load > 0) {
+      const int key = ahead.step * kStreamKeys + (lane & 15), page = page_next;
+      const bool valid = page >= 0 && page < p.kv.num_pages;
+      const int64_t off = page * p.kv.page_stride + static_cast<int64_t>(key % p.kv.page_size) * p.kv.token_stride +
+                          (ahead.unit % heads) * p.kv.head_stride;
+      const uint32_t live = __ballot_sync(0xffffffffu, valid);
+      --to_load;
+      if (++ahead.step == ahead.steps && to_load > 0) advance(ahead);
+      if (to_load > 0) fetch_page();
+      const uint32_t dk = smem_u32(ring + loaded % STAGES * ST::STEP);
+#pragma unroll
+      for (int i = 0; i < kStreamKeys * CH / 32; ++i) {
+        const int t = i * 32 + lane, k = t / CH, c = t % CH;  // chunk c of key k
+        const int64_t o = __shfl_sync(0xffffffffu, off, k);
+        const bool in = (live >> k) & 1u;
+        const int64_t from = in ? o + c * 8 : 0;
+        cp_async16(dk + (k * PITCH + c * 8) * 2, p.kv.k + from, in);
+        cp_async16(dk + ((kStreamKeys + k) * PITCH + c * 8) * 2, p.kv.v + from, in);
+      }
+      ++loaded;
     }
     cp_async_commit();
   };
-  const int steps = (key1 - key0 + kKeys - 1) / kKeys;
+  fetch_page();
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) load_step(warp + s * kWarps);
+  for (int s = 0; s < STAGES - 1; ++s) load_step();
 
-  // query fragments, from global memory (rows past the end read as zero)
-  uint32_t qf[MT][D / 16][4];
-  int limit[MT][2];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = row0 + m * 16 + h * 8 + (lane >> 2);
-      const bool in = r < rows;
-      const int g = r % pl.group, bi = r / pl.group;  // bi: query token within the rows' sequences
-      const int i = bi % p.n, bb = b + bi / p.n;
-      limit[m][h] = own ? min(key1, limit0 + i) : limit0;
-      const uint16_t* src = p.q + bb * p.q_sb + i * p.q_sn + (hk * pl.group + g) * p.q_sh + (lane & 3) * 2;
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        qf[m][c][h] = in ? *reinterpret_cast<const uint32_t*>(src + c * 16) : 0u;
-        qf[m][c][h + 2] = in ? *reinterpret_cast<const uint32_t*>(src + c * 16 + 8) : 0u;
-      }
-    }
-  }
-
-  float o[MT][D / 8][4];
-  float top[MT][2], sum[MT][2];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-#pragma unroll
-    for (int c = 0; c < D / 8; ++c) o[m][c][0] = o[m][c][1] = o[m][c][2] = o[m][c][3] = 0.f;
-    top[m][0] = top[m][1] = -INFINITY;
-    sum[m][0] = sum[m][1] = 0.f;
-  }
   const float scale = p.scale * kLog2e;
   const auto mma = [](float(&d)[4], const uint32_t(&x)[4], uint32_t b0, uint32_t b1) {
     if constexpr (kBF) mma16816_bf16(d, x[0], x[1], x[2], x[3], b0, b1);
     else mma16816(d, x[0], x[1], x[2], x[3], b0, b1);
   };
 
-  for (int step = warp; step < steps; step += kWarps) {
-    load_step(step + (kStages - 1) * kWarps);
-    cp_async_wait<kStages - 1>();
-    __syncwarp();
-    const uint16_t* st = ring + (step / kWarps) % kStages * STEP;
-    const uint32_t ks = smem_u32(st), vs = smem_u32(st + kKeys * PITCH);
-    float s[MT][2][4];
+  uint32_t used = 0;  // steps
+  for (int64_t x = x0; x < x1;) {
+    // one run of a unit
+    const int hk = at.unit % heads, row0 = at.unit / heads * (8 * NT);
+    const int rows = at.b < 0 ? p.B * pl.own_rows : pl.own_rows, b0 = max(at.b, 0);
+    const int end = at.step + static_cast<int>(min(static_cast<int64_t>(at.steps - at.step), x1 - x));
+    uint32_t qf[NT][D / 16][2];
+    int limit[NT][2];  // keys that the lane's two rows of each column tile see
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < NT; ++m) {
+      const int r = row0 + m * 8 + (lane >> 2);
+      const int g = r % pl.group, bi = r / pl.group;  // bi: query token within the rows' sequences
+      const uint16_t* src = p.q + (b0 + bi / p.n) * p.q_sb + (bi % p.n) * p.q_sn + (hk * pl.group + g) * p.q_sh + (lane & 3) * 2;
 #pragma unroll
-      for (int t = 0; t < 2; ++t) s[m][t][0] = s[m][t][1] = s[m][t][2] = s[m][t][3] = 0.f;
-#pragma unroll
-    for (int c = 0; c < D / 16; ++c) {
-      uint32_t kf[4];  // (keys 0-7, low), (keys 0-7, high), (keys 8-15, low), (keys 8-15, high)
-      const int r = (lane & 7) + (lane >> 4) * 8, e = c * 16 + ((lane >> 3) & 1) * 8;
-      ldmatrix_x4(kf, ks + (r * PITCH + e) * 2);
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        mma(s[m][0], qf[m][c], kf[0], kf[1]);
-        mma(s[m][1], qf[m][c], kf[2], kf[3]);
+      for (int c = 0; c < D / 16; ++c) {
+        qf[m][c][0] = r < rows ? __ldg(reinterpret_cast<const uint32_t*>(src + c * 16)) : 0u;
+        qf[m][c][1] = r < rows ? __ldg(reinterpret_cast<const uint32_t*>(src + c * 16 + 8)) : 0u;
       }
-    }
-    const int k0 = key0 + step * kKeys;
-    uint32_t pf[MT][4];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
+      for (int h = 0; h < 2; ++h)
+        limit[m][h] = at.b < 0 ? at.len : min(at.len, at.len - p.n + 1 + (row0 + m * 8 + (lane & 3) * 2 + h) / pl.group % p.n);
+    }
+    float o[NT][D / 16][4];
+    float top[NT][2], sum[NT][2];
+#pragma unroll
+    for (int m = 0; m < NT; ++m) {
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) o[m][c][0] = o[m][c][1] = o[m][c][2] = o[m][c][3] = 0.f;
+      top[m][0] = top[m][1] = -INFINITY;
+      sum[m][0] = sum[m][1] = 0.f;
+    }
+
+    for (int step = at.step; step < end; ++step, ++used) {
+      load_step();
+      cp_async_wait<STAGES - 1>();
+      __syncwarp();
+      const uint16_t* st = ring + used % STAGES * ST::STEP;
+      const uint32_t frag = (lane & 15) * PITCH + (lane >> 4) * 8;
+      const uint32_t ks = smem_u32(st) + frag * 2;
+      // values: rows are keys, so the transposed tile's first 8 columns are keys 0-7
+      const uint32_t vs = smem_u32(st + kStreamKeys * PITCH) + (((lane & 7) + (lane >> 4) * 8) * PITCH + ((lane >> 3) & 1) * 8) * 2;
+      float s[NT][2][4];  // two chains
+#pragma unroll
+      for (int m = 0; m < NT; ++m)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) s[m][t][0] = s[m][t][1] = s[m][t][2] = s[m][t][3] = 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        uint32_t kf[4];  // (keys 0-7, low), (keys 8-15, low), (keys 0-7, high), (keys 8-15, high)
+        ldmatrix_x4(kf, ks + c * 32);
+#pragma unroll
+        for (int m = 0; m < NT; ++m) mma(s[m][c & 1], kf, qf[m][c][0], qf[m][c][1]);
+      }
+      const int k0 = step * kStreamKeys + (lane >> 2);
+      uint32_t pf[NT][2];
+#pragma unroll
+      for (int m = 0; m < NT; ++m) {
+        float z[2][2];  // [row][keys lane / 4, + 8]
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const float v = s[m][0][2 * t + h] + s[m][1][2 * t + h];
+            z[h][t] = k0 + 8 * t < limit[m][h] ? v * scale : -INFINITY;
+          }
+        }
+        float best[2] = {fmaxf(z[0][0], z[0][1]), fmaxf(z[1][0], z[1][1])};
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) {
+          best[0] = fmaxf(best[0], __shfl_xor_sync(0xffffffffu, best[0], d));
+          best[1] = fmaxf(best[1], __shfl_xor_sync(0xffffffffu, best[1], d));
+        }
+        if (__any_sync(0xffffffffu, best[0] > top[m][0] || best[1] > top[m][1])) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float now = fmaxf(top[m][h], best[h]);
+            const float shrink = now == -INFINITY ? 1.f : exp2_approx(top[m][h] - now);
+            top[m][h] = now;
+            sum[m][h] *= shrink;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              o[m][c][h] *= shrink;
+              o[m][c][2 + h] *= shrink;
+            }
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float ref = top[m][h] == -INFINITY ? 0.f : top[m][h];  // a row that has seen no key yet
+          z[h][0] = exp2_approx(z[h][0] - ref);
+          z[h][1] = exp2_approx(z[h][1] - ref);
+          sum[m][h] += z[h][0] + z[h][1];
+        }
+        // P^T has keys along the lanes' rows; the second product wants them along the registers
+        pf[m][0] = transpose8(pack2<kBF>(z[0][0], z[1][0]));
+        pf[m][1] = transpose8(pack2<kBF>(z[0][1], z[1][1]));
+      }
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        uint32_t vf[4];  // (elements 0-7, keys 0-7), (8-15, 0-7), (0-7, 8-15), (8-15, 8-15)
+        ldmatrix_x4_trans(vf, vs + c * 32);
+#pragma unroll
+        for (int m = 0; m < NT; ++m) mma(o[m][c], vf, pf[m][0], pf[m][1]);
+      }
+      __syncwarp();  // the next load_step overwrites a stage read here
+    }
+
+    // the part: slot = this warp's number among those that share the unit
+    const int part = static_cast<int>(w - unit_start / per);
+#pragma unroll
+    for (int m = 0; m < NT; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float z[4] = {s[m][0][2 * h], s[m][0][2 * h + 1], s[m][1][2 * h], s[m][1][2 * h + 1]};
-        float best = -INFINITY;
+        float l = sum[m][h];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int key = k0 + (t >> 1) * 8 + (lane & 3) * 2 + (t & 1);
-          z[t] = key < limit[m][h] ? z[t] * scale : -INFINITY;
-          best = fmaxf(best, z[t]);
-        }
-        best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 1));
-        best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 2));
-        const float now = fmaxf(top[m][h], best);
-        const float ref = now == -INFINITY ? 0.f : now;  // a row that has seen no key yet
-        const float shrink = exp2_approx(top[m][h] - ref);
-        top[m][h] = now;
-        sum[m][h] *= shrink;
+        for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+        const int r = row0 + m * 8 + (lane & 3) * 2 + h;
+        if (r >= rows) continue;
+        const int64_t out_row = (static_cast<int64_t>(b0) * p.n + r / pl.group) * p.Hq + hk * pl.group + r % pl.group;
+        const int64_t slot = out_row * pl.parts + (at.b < 0 ? 0 : pl.prefix_parts) + part;
+        if (lane < 4) a.part_ml[slot] = make_float2(top[m][h], l);
+        float* dst = a.part_o + slot * D + (lane >> 2);
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          o[m][c][2 * h] *= shrink;
-          o[m][c][2 * h + 1] *= shrink;
+        for (int c = 0; c < D / 16; ++c) {
+          dst[c * 16] = o[m][c][h];
+          dst[c * 16 + 8] = o[m][c][2 + h];
         }
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          z[t] = exp2_approx(z[t] - ref);
-          sum[m][h] += z[t];
-        }
-        pf[m][h] = pack2<kBF>(z[0], z[1]);
-        pf[m][h + 2] = pack2<kBF>(z[2], z[3]);
       }
+    if (end == at.steps && lane == 0)
+      a.counts[at.b < 0 ? at.unit : (pl.tc ? 0 : pl.prefix_tiles * heads) + at.b * per_seq + at.unit] = part + 1;
+    x += end - at.step;
+    if (x < x1) {
+      advance(at);
+      unit_start = x;
     }
-#pragma unroll
-    for (int c = 0; c < D / 16; ++c) {
-      uint32_t vf[4];  // (keys 0-7, low), (keys 8-15, low), (keys 0-7, high), (keys 8-15, high)
-      const int r = lane & 15, e = c * 16 + (lane >> 4) * 8;
-      ldmatrix_x4_trans(vf, vs + (r * PITCH + e) * 2);
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        mma(o[m][2 * c], pf[m], vf[0], vf[1]);
-        mma(o[m][2 * c + 1], pf[m], vf[2], vf[3]);
-      }
-    }
-    __syncwarp();  // the next load_step overwrites the stage read here
   }
   cp_async_wait<0>();
-  __syncthreads();
-
-  // join the four warps: (m, l) first, then each warp's o scaled to the common maximum
-  float* ml = reinterpret_cast<float*>(smem);            // [kWarps][16 MT][2]
-  float* acc = ml + kWarps * 16 * MT * 2;                // [kWarps][16 MT][D + 4]
-  constexpr int OP = D + 4;
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float l = sum[m][h];
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
-      if ((lane & 3) == 0) {
-        const int r = m * 16 + h * 8 + (lane >> 2);
-        ml[(warp * 16 * MT + r) * 2] = top[m][h];
-        ml[(warp * 16 * MT + r) * 2 + 1] = l;
-      }
-    }
-  __syncthreads();
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = m * 16 + h * 8 + (lane >> 2);
-      float all = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) all = fmaxf(all, ml[(w * 16 * MT + r) * 2]);
-      const float f = exp2_approx(top[m][h] - (all == -INFINITY ? 0.f : all));
-#pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        float2* dst = reinterpret_cast<float2*>(acc + (warp * 16 * MT + r) * OP + c * 8 + (lane & 3) * 2);
-        *dst = make_float2(o[m][c][2 * h] * f, o[m][c][2 * h + 1] * f);
-      }
-    }
-  __syncthreads();
-  for (int x = threadIdx.x; x < 16 * MT * (D / 4); x += kWarps * 32) {
-    const int r = x / (D / 4), c = x % (D / 4) * 4;
-    if (row0 + r >= rows) break;
-    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-    float all = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float4 u = *reinterpret_cast<const float4*>(acc + (w * 16 * MT + r) * OP + c);
-      t.x += u.x, t.y += u.y, t.z += u.z, t.w += u.w;
-      all = fmaxf(all, ml[(w * 16 * MT + r) * 2]);
-    }
-    const int rr = row0 + r, g = rr % pl.group, bi = rr / pl.group;
-    const int64_t out_row = (static_cast<int64_t>(b) * p.n + bi) * p.Hq + hk * pl.group + g;
-    const int64_t at = out_row * pl.parts + part;
-    *reinterpret_cast<float4*>(a.part_o + at * D + c) = t;
-    if (c == 0) {
-      const float ref = all == -INFINITY ? 0.f : all;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w)
-        l += ml[(w * 16 * MT + r) * 2 + 1] * exp2_approx(ml[(w * 16 * MT + r) * 2] - ref);
-      a.part_ml[at] = make_float2(all, l);
-    }
-  }
 }
 
-// Joins a row's parts.  One warp per row.
+// Joins a row's parts.  One warp per row; a lane holds the (m, l) of every 32nd part and D / 32
+// elements of the sums, and the parts' elements are read eight parts at a time.
 template <bool kBF, int D>
 __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
   const AttentionProblem& p = a.p;
@@ -289,33 +366,61 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
   const int64_t rows = static_cast<int64_t>(p.B) * p.n * p.Hq;
   const int64_t r = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   if (r >= rows) return;
-  const int b = static_cast<int>(r / (static_cast<int64_t>(p.n) * p.Hq));
-  int len = 0;
-  if (pl.private_parts) len = min(max(__ldg(p.lens + b), 0), static_cast<int>(p.max_len));
-  int first = pl.prefix_parts;  // parts of the prefix; the private ones follow at slot prefix_parts
-  if (pl.tc) {
-    const int h = static_cast<int>(r % p.Hq), hk = h / pl.group;
-    const int64_t stacked = r / p.Hq * pl.group + h % pl.group;
-    const int t = hk * pl.tc_tiles + static_cast<int>(stacked / kTcRows);
-    first = tc_last_block(pl, t) - tc_first_block(pl, t) + 1;
+  const int64_t bi = r / p.Hq;
+  const int h = static_cast<int>(r - bi * p.Hq), hk = h / pl.group, b = static_cast<int>(bi / p.n);
+  int first = 0, own = 0;  // parts of the prefix, at slots 0 ..; own parts, at slots prefix_parts ..
+  if (p.prefix_len > 0) {
+    const int64_t stacked = bi * pl.group + h % pl.group;
+    if (pl.tc) {
+      const int t = hk * pl.tc_tiles + static_cast<int>(stacked / kTcRows);
+      first = tc_last_block(pl, t) - tc_first_block(pl, t) + 1;
+    } else {
+      first = a.counts[stacked / pl.tile * p.kv.heads + hk];
+    }
   }
-  const int own = pl.chunk ? (len + pl.chunk - 1) / pl.chunk : 0;
-  const int parts = first + own, skip = pl.prefix_parts - first;  // slot of part s: s, from `first` on s + skip
+  if (pl.private_parts && __ldg(p.lens + b) > 0) {
+    const int own_row = static_cast<int>(bi - static_cast<int64_t>(b) * p.n) * pl.group + h % pl.group;
+    own = a.counts[pl.prefix_tiles * p.kv.heads +
+                   (static_cast<int64_t>(b) * pl.private_tiles + own_row / pl.tile) * p.kv.heads + hk];
+  }
+  const int parts = first + own, skip = pl.prefix_parts - first;
   const float2* ml = a.part_ml + r * pl.parts;
   const float* src = a.part_o + r * pl.parts * D;
-  float all = -INFINITY;
-  for (int s = 0; s < parts; ++s) all = fmaxf(all, ml[s < first ? s : s + skip].x);
-  const float ref = all == -INFINITY ? 0.f : all;
-  constexpr int N = D / 32;
-  float acc[N] = {}, l = 0.f;
-  for (int s = 0; s < parts; ++s) {
-    const int slot = s < first ? s : s + skip;
-    const float f = exp2_approx(ml[slot].x - ref);
-    l += ml[slot].y * f;
+  constexpr int N = D / 32, BATCH = 8;
+  float acc[N] = {}, l = 0.f, all = -INFINITY;
+  for (int s0 = 0; s0 < parts; s0 += 32) {
+    const int s = s0 + lane;
+    const float2 mine = s < parts ? ml[s < first ? s : s + skip] : make_float2(-INFINITY, 0.f);
+    float best = mine.x;
 #pragma unroll
-    for (int c = 0; c < N; ++c) acc[c] += src[static_cast<int64_t>(slot) * D + c * 32 + lane] * f;
+    for (int d = 16; d; d >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, d));
+    const float now = fmaxf(all, best), ref = now == -INFINITY ? 0.f : now;
+    const float shrink = exp2_approx(all - ref), f = exp2_approx(mine.x - ref);  // 0 past the last part
+    all = now;
+    l = l * shrink + mine.y * f;  // this lane's share
+#pragma unroll
+    for (int c = 0; c < N; ++c) acc[c] *= shrink;
+    const int n = min(32, parts - s0);
+    for (int i0 = 0; i0 < n; i0 += BATCH) {
+      float v[BATCH][N];
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const int t = s0 + min(i0 + i, n - 1);
+        const float* from = src + static_cast<int64_t>(t < first ? t : t + skip) * D + lane;
+#pragma unroll
+        for (int c = 0; c < N; ++c) v[i][c] = from[c * 32];
+      }
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const float g = i0 + i < n ? __shfl_sync(0xffffffffu, f, i0 + i) : 0.f;
+#pragma unroll
+        for (int c = 0; c < N; ++c) acc[c] = i0 + i < n ? acc[c] + v[i][c] * g : acc[c];
+      }
+    }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;  // a row that sees no key is zero
+#pragma unroll
+  for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+  const float inv = l > 0.f ? 1.f / l : l;  // a row that sees no key is zero; NaN stays
 #pragma unroll
   for (int c = 0; c < N; ++c) p.out[r * D + c * 32 + lane] = float_to_elem<kBF>(acc[c] * inv);
 }
@@ -325,12 +430,12 @@ int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 Plan make_plan(const AttentionProblem& p, int sms) {
   Plan pl{};
   pl.group = p.Hq / p.kv.heads;
-  const int own_rows = p.n * pl.group;
-  pl.mt = own_rows > 16 && p.kv.head_dim <= 128 ? 2 : 1;
-  const int tile = 16 * pl.mt;
-  const int64_t want = 2 * sms;  // blocks that fill the GPU
-  const int64_t stacked = static_cast<int64_t>(p.B) * own_rows;  // rows that share a prefix key
+  pl.own_rows = p.n * pl.group;
+  const int64_t stacked = static_cast<int64_t>(p.B) * pl.own_rows;  // rows that share a prefix key
   pl.tc = p.prefix_len > 0 && tc_head_dim_supported(p.kv.head_dim) && stacked > 32;
+  const int64_t rows = pl.tc || p.prefix_len == 0 ? pl.own_rows : stacked;
+  pl.tile = rows <= 8 ? 8 : rows <= 16 || p.kv.head_dim > 128 ? 16 : 32;
+  const int tile = pl.tile;
   if (pl.tc) {
     pl.tc_tiles = ceil_div(stacked, kTcRows);
     pl.tc_steps = ceil_div(p.prefix_len, kTcKeys);
@@ -340,37 +445,44 @@ Plan make_plan(const AttentionProblem& p, int sms) {
     pl.prefix_parts = min((pl.tc_steps - 1) / pl.tc_per + 2, pl.tc_blocks);
   } else if (p.prefix_len > 0) {
     pl.prefix_tiles = ceil_div(stacked, tile);
-    const int64_t units = static_cast<int64_t>(p.kv.heads) * pl.prefix_tiles;
-    const int cuts = static_cast<int>(max(int64_t{1}, min(static_cast<int64_t>(ceil_div(want, units)),
-                                                          static_cast<int64_t>(ceil_div(p.prefix_len, 128)))));
-    pl.prefix_chunk = (ceil_div(p.prefix_len, cuts) + 63) / 64 * 64;
-    pl.prefix_parts = ceil_div(p.prefix_len, pl.prefix_chunk);
   }
-  if (p.max_len > 0) {
-    pl.private_tiles = ceil_div(own_rows, tile);
-    const int64_t units = static_cast<int64_t>(p.B) * p.kv.heads * pl.private_tiles;
-    const int cuts = static_cast<int>(max(int64_t{1}, min(static_cast<int64_t>(ceil_div(4 * want, units)),
-                                                          static_cast<int64_t>(ceil_div(p.max_len, 128)))));
-    pl.chunk = (ceil_div(p.max_len, cuts) + 63) / 64 * 64;
-    pl.private_parts = ceil_div(p.max_len, pl.chunk);
-  }
+  if (p.max_len > 0) pl.private_tiles = ceil_div(pl.own_rows, tile);
+  // most steps that the streaming kernel can have; the lengths, known on the device only, may add up
+  // to less, so shares go down to a quarter of what this many would give each warp
+  const int64_t prefix_steps = pl.tc ? 0 : ceil_div(p.prefix_len, kStreamKeys);
+  const int64_t own_steps = ceil_div(p.max_len, kStreamKeys);
+  const int64_t total = p.kv.heads * (prefix_steps * pl.prefix_tiles + own_steps * p.B * pl.private_tiles);
+  const int64_t blocks = static_cast<int64_t>(sms) * (p.kv.head_dim <= 128 ? 2 : 1);
+  const int64_t share = (total + blocks * kStreamWarps - 1) / (blocks * kStreamWarps);
+  pl.per_min = static_cast<int>(max(int64_t{2}, min(share / 4, int64_t{1} << 20)));
+  pl.blocks = static_cast<int>(min(blocks, (total + pl.per_min * kStreamWarps - 1) / (pl.per_min * kStreamWarps)));
+  if (pl.prefix_tiles) pl.prefix_parts = static_cast<int>((prefix_steps - 1) / pl.per_min + 2);
+  if (p.max_len > 0) pl.private_parts = static_cast<int>((own_steps - 1) / pl.per_min + 2);
   pl.parts = pl.prefix_parts + pl.private_parts;
   return pl;
 }
 
-template <bool kBF, int D, int MT>
+struct Layout {
+  size_t ml, counts, bytes;  // offsets; part_o first
+};
+
+Layout layout(const AttentionProblem& p, const Plan& pl) {
+  const size_t slots = static_cast<size_t>(p.B) * p.n * p.Hq * pl.parts;
+  const size_t units = (static_cast<size_t>(pl.prefix_tiles) + static_cast<size_t>(p.B) * pl.private_tiles) * p.kv.heads;
+  Layout l;
+  l.ml = slots * p.kv.head_dim * 4;
+  l.counts = l.ml + slots * 8;
+  l.bytes = l.counts + units * 4;
+  return l;
+}
+
+template <bool kBF, int D, int NT>
 cudaError_t run_stream(const AttnArgs& a) {
-  constexpr int ring = kWarps * kStages * 2 * kKeys * (D + 8) * 2;
-  constexpr int join = kWarps * 16 * MT * (2 + D + 4) * 4;
-  constexpr int smem = ring > join ? ring : join;
-  const Plan& pl = a.plan;
-  const int64_t units = (pl.tc ? 0 : static_cast<int64_t>(a.p.kv.heads) * pl.prefix_tiles * pl.prefix_parts) +
-                        static_cast<int64_t>(a.p.B) * a.p.kv.heads * pl.private_tiles * pl.private_parts;
-  if (units == 0) return cudaSuccess;
-  if (units > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  cudaError_t e = cudaFuncSetAttribute(attn_stream_kernel<kBF, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (a.plan.blocks == 0) return cudaSuccess;
+  constexpr int smem = Stream<D>::SMEM;
+  cudaError_t e = cudaFuncSetAttribute(attn_stream_kernel<kBF, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  attn_stream_kernel<kBF, D, MT><<<static_cast<unsigned>(units), kWarps * 32, smem, a.p.stream>>>(a);
+  attn_stream_kernel<kBF, D, NT><<<a.plan.blocks, kStreamWarps * 32, smem, a.p.stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -378,8 +490,9 @@ template <bool kBF, int D>
 cudaError_t run(const AttnArgs& a) {
   cudaError_t e = a.plan.tc ? launch_prefix_tc(a) : cudaSuccess;
   if (e != cudaSuccess) return e;
-  if constexpr (D <= 128) e = a.plan.mt == 2 ? run_stream<kBF, D, 2>(a) : run_stream<kBF, D, 1>(a);
-  else e = run_stream<kBF, D, 1>(a);
+  if (a.plan.tile == 8) e = run_stream<kBF, D, 1>(a);
+  else if (a.plan.tile == 16) e = run_stream<kBF, D, 2>(a);
+  else if constexpr (D <= 128) e = run_stream<kBF, D, 4>(a);
   if (e != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(a.p.B) * a.p.n * a.p.Hq;
   attn_join_kernel<kBF, D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, a.p.stream>>>(a);
@@ -400,21 +513,21 @@ cudaError_t run_dim(const AttnArgs& a) {
 
 bool attention_head_dim_supported(int64_t D) { return D == 64 || D == 96 || D == 128 || D == 256; }
 
-size_t attention_workspace_bytes(const AttentionProblem& p, int sms) {
-  const Plan pl = make_plan(p, sms);
-  const size_t slots = static_cast<size_t>(p.B) * p.n * p.Hq * pl.parts;
-  return slots * p.kv.head_dim * 4 + slots * 8;
-}
+size_t attention_workspace_bytes(const AttentionProblem& p, int sms) { return layout(p, make_plan(p, sms)).bytes; }
 
 cudaError_t launch_attention(const AttentionProblem& p, int sms) {
-  AttnArgs a{p, make_plan(p, sms), nullptr, nullptr, nullptr};
+  AttnArgs a{};
+  a.p = p;
+  a.plan = make_plan(p, sms);
   if (a.plan.tc) {
     const cudaError_t e = status_word_ptr(&a.status);
     if (e != cudaSuccess) return e;
   }
-  const size_t slots = static_cast<size_t>(p.B) * p.n * p.Hq * a.plan.parts;
-  a.part_o = static_cast<float*>(p.workspace);
-  a.part_ml = reinterpret_cast<float2*>(a.part_o + slots * p.kv.head_dim);
+  const Layout l = layout(p, a.plan);
+  uint8_t* ws = static_cast<uint8_t*>(p.workspace);
+  a.part_o = reinterpret_cast<float*>(ws);
+  a.part_ml = reinterpret_cast<float2*>(ws + l.ml);
+  a.counts = reinterpret_cast<int*>(ws + l.counts);
   return p.bf16 ? run_dim<true>(a) : run_dim<false>(a);
 }
 

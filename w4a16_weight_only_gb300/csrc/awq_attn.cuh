@@ -38,23 +38,32 @@ __device__ __forceinline__ void cp_async_wait() {
 }
 
 // How a call is cut.  Row r = (b n + i) Hq + h of the output; part s of row r is at
-// part_o[(r parts + s) D], part_ml[r parts + s]; parts [0, prefix_parts) are the prefix's, then one
-// per started `chunk` of the sequence's own keys.
+// part_o[(r parts + s) D], part_ml[r parts + s]; slots [0, prefix_parts) are the prefix's, the others
+// the sequence's own.
+//
+// Tensor-core kernel (tc, the prefix's keys): tiles of kTcRows rows per key/value head, kTcKeys-key
+// steps per tile; all steps of all tiles form one sequence of which block c takes [c per, (c + 1)
+// per).
+//
+// Streaming kernel (the sequences' own keys, and the prefix's without tc): units are (sequence, row
+// tile, key/value head), the prefix being a sequence of its own in front; a unit of L keys has
+// ceil(L / kStreamKeys) steps; all steps of all units form one sequence of which warp w takes [w per,
+// (w + 1) per), per = max(per_min, total / warps) being found on the device, where the lengths are.
+// The warp that ends a unit writes the unit's number of parts.
 struct Plan {
   int group;  // query heads per key/value head
-  // prefix, streaming kernel: row tiles per key/value head, keys per part
-  int prefix_tiles, prefix_chunk;
-  // prefix, tensor-core kernel (tc): tiles of kTcRows rows per key/value head, kTcKeys-key steps per
-  // tile; all steps of all tiles form one sequence of which block c takes [c per, (c + 1) per)
+  int own_rows;  // rows of one sequence that share a key/value head
   bool tc;
   int tc_tiles, tc_steps, tc_per, tc_blocks;
-  int prefix_parts;   // most parts a row's prefix has
-  int chunk;          // private keys per part
-  int private_parts;  // parts of the longest sequence
-  int private_tiles;  // row tiles of one sequence
-  int parts;          // prefix_parts + private_parts
-  int mt;             // 16-row tiles per block of the streaming kernel
+  int tile;                          // rows of a streaming unit
+  int prefix_tiles, private_tiles;   // row tiles per key/value head of the streaming units
+  int per_min, blocks;               // streaming kernel
+  int prefix_parts, private_parts;   // most parts of a row
+  int parts;                         // their sum
 };
+
+constexpr int kStreamKeys = 16;
+constexpr int kStreamWarps = 4;
 
 constexpr int kTcRows = 256;  // two 128-row tensor-core tiles
 constexpr int kTcKeys = 128;
@@ -72,6 +81,7 @@ struct AttnArgs {
   Plan plan;
   float* part_o;
   float2* part_ml;
+  int* counts;  // parts of each streaming unit: [prefix_tiles][heads], then [B][private_tiles][heads]
   unsigned int* status;
 };
 

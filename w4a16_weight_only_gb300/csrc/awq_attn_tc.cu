@@ -292,14 +292,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
         const bool in = r < stacked;
         const int g = r % pl.group, bi = r / pl.group;
         {
-          const uint16_t* src = p.q + static_cast<int64_t>(bi / p.n) * p.q_sb + static_cast<int64_t>(bi % p.n) * p.q_sn +
-                                static_cast<int64_t>(sg.hk * pl.group + g) * p.q_sh;
+          // the warp's 32 query rows, whole rows at a time
+          const int64_t off = in ? static_cast<int64_t>(bi / p.n) * p.q_sb + static_cast<int64_t>(bi % p.n) * p.q_sn +
+                                       static_cast<int64_t>(sg.hk * pl.group + g) * p.q_sh
+                                 : -1;
+          constexpr int CH = D / 8;
+          uint4 v[CH];
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) {
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (in) v = __ldg(reinterpret_cast<const uint4*>(src) + c);
-            v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
-            *reinterpret_cast<uint4*>(q_tile + (c >> 3) * SH::PANEL + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v;
+          for (int i = 0; i < CH; ++i) {
+            const int x = i * 32 + lane, k = x / CH, c = x % CH;  // chunk c of the warp's row k
+            const int64_t o = __shfl_sync(0xffffffffu, off, k);
+            v[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (sg.row0 + h * 128 + (warp & 3) * 32 + k < stacked) v[i] = __ldg(reinterpret_cast<const uint4*>(p.q + o) + c);
+          }
+#pragma unroll
+          for (int i = 0; i < CH; ++i) {
+            const int x = i * 32 + lane, k = x / CH, c = x % CH;
+            const uint4 w = make_uint4(v[i].x ^ flip, v[i].y ^ flip, v[i].z ^ flip, v[i].w ^ flip);
+            *reinterpret_cast<uint4*>(q_tile + (c >> 3) * SH::PANEL + ((warp & 3) * 32 + k) * 128 + (((c & 7) ^ (k & 7)) << 4)) = w;
           }
           fence_proxy_async_smem();
           __syncwarp();
