@@ -6,6 +6,8 @@
 namespace awq {
 namespace {
 
+using namespace ptx;
+
 constexpr unsigned kAll = 0xffffffffu;
 
 // -------------------------------------------------------------------------------- routing ----
@@ -26,26 +28,53 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
   else return elem_to_float<DT == 2>(__ldg(static_cast<const uint16_t*>(p) + i));
 }
 
+__device__ __forceinline__ float reciprocal(float x) {  // good to the last bit or two
+  float y;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // One warp per token.  Lane l holds experts [l V, l V + V), V = ceil(E / 32) <= VT, so that the
-// lowest lane and the lowest register of the equal keys is the lowest expert.
-template <int DT, int VT>
+// lowest lane and the lowest register of the equal keys is the lowest expert.  kVec: V == VT and rows
+// allow 16-byte loads.  Bound by instructions (about 600 per token at 256 experts, 8 of them chosen);
+// every maximum over the warp is one redux on the keys as ordered integers.
+template <int DT, int VT, bool kVec>
 __global__ void __launch_bounds__(128) route_kernel(const RouteProblem p) {
   const int lane = threadIdx.x & 31;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   if (t >= p.T) return;
-  const int V = (p.E + 31) / 32;
+  const int V = kVec ? VT : (p.E + 31) / 32;
   const int e0 = lane * V;
   const int64_t row = t * p.ld;
   float x[VT];
+  if constexpr (kVec) {
+    constexpr int PER = DT == 1 ? 4 : 8;
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.logits) + (row + e0) * (DT == 1 ? 4 : 2));
 #pragma unroll
-  for (int i = 0; i < VT; ++i) x[i] = i < V && e0 + i < p.E ? load_logit<DT>(p.logits, row + e0 + i) : -INFINITY;
+    for (int i = 0; i < VT / PER; ++i) {
+      const uint4 v = __ldg(src + i);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (DT == 1) {
+          x[i * 4 + j] = __uint_as_float(w[j]);
+        } else {
+          const float2 f = pair_to_float2<DT == 2>(w[j]);
+          x[i * 8 + 2 * j] = f.x;
+          x[i * 8 + 2 * j + 1] = f.y;
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VT; ++i) x[i] = i < V && e0 + i < p.E ? load_logit<DT>(p.logits, row + e0 + i) : -INFINITY;
+  }
 
   // scores; an expert whose logit is -inf is out
   float score[VT];
-  bool bad = false;
   if (p.sigmoid) {
 #pragma unroll
-    for (int i = 0; i < VT; ++i) score[i] = __fdiv_rn(1.f, 1.f + expf(-x[i]));
+    for (int i = 0; i < VT; ++i) score[i] = reciprocal(1.f + expf(-x[i]));
   } else {
     float top = -INFINITY;
 #pragma unroll
@@ -59,9 +88,11 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteProblem p) {
     }
 #pragma unroll
     for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
+    const float inv = __fdiv_rn(1.f, sum);
 #pragma unroll
-    for (int i = 0; i < VT; ++i) score[i] = __fdiv_rn(score[i], sum);
+    for (int i = 0; i < VT; ++i) score[i] *= inv;
   }
+  bool bad = false;
   uint32_t key[VT];
 #pragma unroll
   for (int i = 0; i < VT; ++i) {
@@ -74,37 +105,61 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteProblem p) {
 
   if (p.groups > 1 && !bad) {
     const int per = p.E / p.groups;
-    uint32_t mine = 0u;  // lane g: group g's score
+    const bool even = p.E == 32 * V && 32 % p.groups == 0;  // a group is the experts of 32 / groups whole lanes
+    uint32_t mine = 0u;  // a group's score: in all its lanes (even), or in lane g
+    if (even) {
+      uint32_t first = 0u, second = 0u;  // this lane's two best, then its group's
+#pragma unroll
+      for (int i = 0; i < VT; ++i) {
+        second = max(second, min(first, key[i]));
+        first = max(first, key[i]);
+      }
+      for (int d = 1; d < 32 / p.groups; d <<= 1) {
+        const uint32_t of = __shfl_xor_sync(kAll, first, d), os = __shfl_xor_sync(kAll, second, d);
+        second = max(max(second, os), min(first, of));
+        first = max(first, of);
+      }
+      mine = p.group_best == 2 && second ? ordered(from_ordered(first) + from_ordered(second)) : first;
+    } else {
+      for (int g = 0; g < p.groups; ++g) {
+        uint32_t first = 0u, second = 0u;  // this lane's two best of the group
+#pragma unroll
+        for (int i = 0; i < VT; ++i) {
+          const int e = e0 + i;
+          const uint32_t u = i < V && e >= g * per && e < (g + 1) * per ? key[i] : 0u;
+          second = max(second, min(first, u));
+          first = max(first, u);
+        }
+        const uint32_t best = __reduce_max_sync(kAll, first);
+        uint32_t sum = best;
+        if (p.group_best == 2 && best) {
+          const int owner = __ffs(__ballot_sync(kAll, first == best)) - 1;
+          const uint32_t next = __reduce_max_sync(kAll, lane == owner ? second : first);
+          if (next) sum = ordered(from_ordered(best) + from_ordered(next));
+        }
+        if (lane == g) mine = sum;
+      }
+    }
+    // a group is kept if fewer than topk_groups are better (ties: the lower index)
+    const int width = even ? 32 / p.groups : 1, group = lane / width;
+    int better = 0;
     for (int g = 0; g < p.groups; ++g) {
-      uint32_t first = 0u, second = 0u;  // this lane's two best of the group
+      const uint32_t other = __shfl_sync(kAll, mine, g * width);
+      better += other > mine || (other == mine && g < group);
+    }
+    const bool keep = mine && better < p.topk_groups;
+    if (even) {
+      if (!keep) {
+#pragma unroll
+        for (int i = 0; i < VT; ++i) key[i] = 0u;
+      }
+    } else {
+      const uint32_t kept = __ballot_sync(kAll, keep && lane < p.groups);
 #pragma unroll
       for (int i = 0; i < VT; ++i) {
         const int e = e0 + i;
-        const uint32_t u = i < V && e >= g * per && e < (g + 1) * per ? key[i] : 0u;
-        second = max(second, min(first, u));
-        first = max(first, u);
+        if (i < V && e < p.E && !((kept >> (e / per)) & 1u)) key[i] = 0u;
       }
-      const uint32_t best = __reduce_max_sync(kAll, first);
-      uint32_t sum = best;
-      if (p.group_best == 2 && best) {
-        const int owner = __ffs(__ballot_sync(kAll, first == best)) - 1;
-        const uint32_t next = __reduce_max_sync(kAll, lane == owner ? second : first);
-        if (next) sum = ordered(from_ordered(best) + from_ordered(next));
-      }
-      if (lane == g) mine = sum;
-    }
-    uint32_t kept = 0u;
-    for (int j = 0; j < p.topk_groups; ++j) {
-      const uint32_t best = __reduce_max_sync(kAll, mine);
-      if (!best) break;
-      const int owner = __ffs(__ballot_sync(kAll, mine == best)) - 1;
-      kept |= 1u << owner;
-      if (lane == owner) mine = 0u;
-    }
-#pragma unroll
-    for (int i = 0; i < VT; ++i) {
-      const int e = e0 + i;
-      if (i < V && e < p.E && !((kept >> (e / per)) & 1u)) key[i] = 0u;
     }
   }
 
@@ -114,29 +169,31 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteProblem p) {
     chosen = lane;
     weight = __int_as_float(0x7fffffff);
   } else {
-    for (int j = 0; j < p.k; ++j) {
-      uint32_t first = 0u;
+    uint32_t first = 0u;
 #pragma unroll
-      for (int i = 0; i < VT; ++i) first = max(first, key[i]);
+    for (int i = 0; i < VT; ++i) first = max(first, key[i]);
+    for (int j = 0; j < p.k; ++j) {
       const uint32_t best = __reduce_max_sync(kAll, first);
       if (!best) break;  // no expert left: the other places stay empty
       const int owner = __ffs(__ballot_sync(kAll, first == best)) - 1;
       int at = 0;
       float s = 0.f;
-#pragma unroll
-      for (int i = VT - 1; i >= 0; --i) {
-        if (key[i] == best) {
-          at = i;
-          s = score[i];
-        }
-      }
-      if (lane == owner) {
+      if (lane == owner) {  // its first key of that value goes
+        bool found = false;
+        first = 0u;
 #pragma unroll
         for (int i = 0; i < VT; ++i) {
-          if (i == at) key[i] = 0u;
+          const bool hit = !found && key[i] == best;
+          if (hit) {
+            at = e0 + i;
+            s = score[i];
+            key[i] = 0u;
+          }
+          found |= hit;
+          first = max(first, key[i]);
         }
       }
-      at = __shfl_sync(kAll, e0 + at, owner);
+      at = __shfl_sync(kAll, at, owner);
       s = __shfl_sync(kAll, s, owner);
       if (lane == j) {
         chosen = at;
@@ -157,17 +214,29 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteProblem p) {
   }
 }
 
+template <int DT, int VT>
+cudaError_t launch_route_v(const RouteProblem& p) {
+  const unsigned grid = static_cast<unsigned>((p.T + 3) / 4);
+  constexpr int PER = DT == 1 ? 4 : 8;  // logits of 16 bytes
+  if constexpr (VT % PER == 0) {
+    if (p.E == 32 * VT && p.ld % PER == 0 && aligned(p.logits, 16)) {
+      route_kernel<DT, VT, true><<<grid, 128, 0, p.stream>>>(p);
+      return cudaGetLastError();
+    }
+  }
+  route_kernel<DT, VT, false><<<grid, 128, 0, p.stream>>>(p);
+  return cudaGetLastError();
+}
+
 template <int DT>
 cudaError_t launch_route_dt(const RouteProblem& p) {
-  const unsigned grid = static_cast<unsigned>((p.T + 3) / 4);
   const int V = (p.E + 31) / 32;
-  if (V <= 1) route_kernel<DT, 1><<<grid, 128, 0, p.stream>>>(p);
-  else if (V <= 2) route_kernel<DT, 2><<<grid, 128, 0, p.stream>>>(p);
-  else if (V <= 4) route_kernel<DT, 4><<<grid, 128, 0, p.stream>>>(p);
-  else if (V <= 8) route_kernel<DT, 8><<<grid, 128, 0, p.stream>>>(p);
-  else if (V <= 16) route_kernel<DT, 16><<<grid, 128, 0, p.stream>>>(p);
-  else route_kernel<DT, 32><<<grid, 128, 0, p.stream>>>(p);
-  return cudaGetLastError();
+  if (V <= 1) return launch_route_v<DT, 1>(p);
+  if (V <= 2) return launch_route_v<DT, 2>(p);
+  if (V <= 4) return launch_route_v<DT, 4>(p);
+  if (V <= 8) return launch_route_v<DT, 8>(p);
+  if (V <= 16) return launch_route_v<DT, 16>(p);
+  return launch_route_v<DT, 32>(p);
 }
 
 // ------------------------------------------------------------------------------- dispatch ----
@@ -193,6 +262,7 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_count_kernel(const Disp
   extern __shared__ int cnt[];
   const int64_t R = p.T * p.k, chunk = sort_chunk(R);
   const int64_t i0 = blockIdx.x * chunk, i1 = min(R, i0 + chunk);
+  launch_dependents();
   for (int e = threadIdx.x; e <= p.E; e += kSortThreads) cnt[e] = 0;
   __syncthreads();
   for (int64_t i = i0 + threadIdx.x; i < i1; i += kSortThreads) atomicAdd(cnt + bin_of(__ldg(p.experts + i), p.E), 1);
@@ -205,28 +275,41 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_count_kernel(const Disp
 // the row of that warp's first place of the bin, and the warp hands rows out in flat order.
 __global__ void __launch_bounds__(kSortThreads) dispatch_place_kernel(const DispatchProblem p, const int* hist, int blocks,
                                                                       int* dest) {
-  extern __shared__ int cnt[];  // [kSortWarps][E + 1], then [E + 1] totals
+  extern __shared__ int cnt[];  // [kSortWarps][E + 1], then [E + 1] totals and [E + 1] of earlier blocks
   const int bins = p.E + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int* total = cnt + kSortWarps * bins;
+  int* base = total + bins;
   const int64_t R = p.T * p.k, chunk = sort_chunk(R), part = chunk / kSortWarps;
   const int64_t w0 = blockIdx.x * chunk + warp * part, w1 = min(R, w0 + part);
-  for (int e = threadIdx.x; e < kSortWarps * bins; e += kSortThreads) cnt[e] = 0;
+  for (int e = threadIdx.x; e < (kSortWarps + 2) * bins; e += kSortThreads) cnt[e] = 0;
   __syncthreads();
+  launch_dependents();
   for (int64_t i = w0 + lane; i < w1; i += 32) atomicAdd(cnt + warp * bins + bin_of(__ldg(p.experts + i), p.E), 1);
   __syncthreads();
-  for (int e = threadIdx.x; e < bins; e += kSortThreads) {
+  grid_dependency_wait();  // the counts of all blocks
+  // each warp adds up every kSortWarps-th block's counts, 32 bins at a time
+  for (int e0 = 0; e0 < bins; e0 += 32) {
+    const int e = e0 + lane;
     int before = 0, all = 0;  // this bin's places of earlier blocks, of all blocks
-    for (int b = 0; b < blocks; ++b) {
-      const int c = __ldg(hist + static_cast<int64_t>(b) * bins + e);
-      before += b < static_cast<int>(blockIdx.x) ? c : 0;
-      all += c;
+    if (e < bins) {
+#pragma unroll 4
+      for (int b = warp; b < blocks; b += kSortWarps) {
+        const int c = __ldg(hist + static_cast<int64_t>(b) * bins + e);
+        before += b < static_cast<int>(blockIdx.x) ? c : 0;
+        all += c;
+      }
+      atomicAdd(base + e, before);
+      atomicAdd(total + e, all);
     }
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < bins; e += kSortThreads) {
+    int before = base[e];
     for (int w = 0; w < kSortWarps; ++w) {
       const int c = cnt[w * bins + e];
       cnt[w * bins + e] = before;
       before += c;
     }
-    total[e] = all;
   }
   __syncthreads();
   if (warp == 0) {  // exclusive sum of the totals: the experts' first rows
@@ -254,7 +337,7 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_place_kernel(const Disp
     const unsigned same = __match_any_sync(kAll, bin);
     if (in) {
       const int row = total[bin] + cnt[warp * bins + bin] + __popc(same & ((1u << lane) - 1u));
-      dest[i] = row;
+      dest[i] = bin < p.E ? row : ~row;  // complement: no expert, the row is zeroed
       p.rows[i] = bin < p.E ? row : -1;
     }
     __syncwarp();
@@ -263,36 +346,184 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_place_kernel(const Disp
   }
 }
 
-// Copies a token's row to the rows of its places; a token is read once.
+// Copies a token's row to the rows of its places (zeros where a place has no expert); a token is read
+// once.  Block (t, y): the y-th run of the row's vectors.  HBM-bound by the k rows written.
+constexpr int kRowThreads = 128;
+
 template <typename Vec>
-__global__ void __launch_bounds__(256) dispatch_copy_kernel(const DispatchProblem p, const int* dest) {
-  constexpr int kPer = sizeof(Vec) / 2;
+__device__ __forceinline__ void copy_row(const DispatchProblem& p, int64_t t, const int* dest, int n) {
+  const int c = blockIdx.y * kRowThreads + threadIdx.x;
+  if (c >= n) return;
+  const Vec v = __ldg(reinterpret_cast<const Vec*>(p.x + t * p.ld) + c);
+#pragma unroll 4
+  for (int j = 0; j < p.k; ++j) {
+    const int d = dest[j];
+    // a place without an expert is marked by the complement of its row
+    reinterpret_cast<Vec*>(p.routed + static_cast<int64_t>(d < 0 ? ~d : d) * p.W)[c] = d < 0 ? Vec{} : v;
+  }
+}
+
+template <typename Vec>
+__global__ void __launch_bounds__(kRowThreads) dispatch_copy_kernel(const DispatchProblem p, const int* dest) {
+  grid_dependency_wait();
+  copy_row<Vec>(p, blockIdx.x, dest + static_cast<int64_t>(blockIdx.x) * p.k, p.W / static_cast<int>(sizeof(Vec) / 2));
+}
+
+// Few places: every block finds its token's rows by itself, by counting the places that sort before
+// each of its own (lower bin, or the same bin earlier), and copies at once; the first block also
+// writes the offsets.  One launch, no workspace.  T k compares per place, so only while they are
+// fewer than the latency of two more launches hides.
+constexpr int kFewPlaces = 2048;
+constexpr int kFewK = 32;
+
+template <typename Vec>
+__global__ void __launch_bounds__(kRowThreads) dispatch_few_kernel(const DispatchProblem p) {
+  __shared__ int place[kFewK];
+  extern __shared__ int hist[];  // [E + 1], first block
   const int64_t t = blockIdx.x;
-  const int n = p.W / kPer;
-  const Vec* src = reinterpret_cast<const Vec*>(p.x + t * p.ld);
-  for (int c = threadIdx.x; c < n; c += 256) {
-    const Vec v = __ldg(src + c);
-    for (int j = 0; j < p.k; ++j) {
-      const int64_t i = t * p.k + j;
-      const int id = __ldg(p.experts + i);
-      reinterpret_cast<Vec*>(p.routed + static_cast<int64_t>(__ldg(dest + i)) * p.W)[c] = id >= 0 && id < p.E ? v : Vec{};
+  const int R = static_cast<int>(p.T) * p.k, i0 = static_cast<int>(t) * p.k, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool writes_offsets = blockIdx.x == 0 && blockIdx.y == 0;
+  // a warp takes every fourth place of the token
+  for (int j = warp; j < p.k; j += kRowThreads / 32) {
+    const int mine = bin_of(__ldg(p.experts + i0 + j), p.E);
+    int before = 0;
+    for (int i = lane; i < R; i += 32) {
+      const int b = bin_of(__ldg(p.experts + i), p.E);
+      before += b < mine || (b == mine && i < i0 + j);
+    }
+    before = __reduce_add_sync(kAll, before);
+    if (lane == 0) place[j] = mine < p.E ? before : ~before;
+    if (lane == 0 && blockIdx.y == 0) p.rows[i0 + j] = mine < p.E ? before : -1;
+  }
+  if (writes_offsets) {
+    for (int e = threadIdx.x; e <= p.E; e += kRowThreads) hist[e] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < R; i += kRowThreads) atomicAdd(hist + bin_of(__ldg(p.experts + i), p.E), 1);
+  }
+  __syncthreads();
+  copy_row<Vec>(p, t, place, p.W / static_cast<int>(sizeof(Vec) / 2));
+  if (writes_offsets && warp == 0) {
+    int run = 0;
+    for (int e0 = 0; e0 <= p.E; e0 += 32) {
+      const int e = e0 + lane, c = e <= p.E ? hist[e] : 0;
+      int s = c;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(kAll, s, d);
+        if (lane >= d) s += o;
+      }
+      if (e <= p.E) p.offsets[e] = run + s - c;
+      run += __shfl_sync(kAll, s, 31);
     }
   }
 }
 
 // -------------------------------------------------------------------------------- combine ----
 
-template <bool kBF>
-__global__ void __launch_bounds__(256) combine_any_kernel(const CombineProblem p) {
+// Block (t, y): the y-th run of token t's columns.  A thread owns one vector of eight (kVec) columns
+// or one column and has up to eight rows' loads in flight; sums run in the order of the places.
+// HBM-bound by the rows read.
+template <bool kBF, bool kVec>
+__global__ void __launch_bounds__(kRowThreads) combine_kernel(const CombineProblem p) {
+  constexpr int PER = kVec ? 8 : 1, BATCH = 8;
   const int64_t t = blockIdx.x;
-  for (int c = threadIdx.x; c < p.W; c += 256) {
-    float a = p.base ? elem_to_float<kBF>(p.base[t * p.W + c]) : 0.f;
-    for (int j = 0; j < p.k; ++j) {
-      const int r = __ldg(p.rows + t * p.k + j);
-      if (r >= 0 && r < p.R) a += __ldg(p.weights + t * p.k + j) * elem_to_float<kBF>(__ldg(p.y + static_cast<int64_t>(r) * p.W + c));
+  const int c = (blockIdx.y * kRowThreads + threadIdx.x) * PER;
+  if (c >= p.W) return;
+  float acc[PER];
+  const auto load = [&](const uint16_t* src, uint32_t (&v)[4]) {
+    if constexpr (kVec) *reinterpret_cast<uint4*>(v) = __ldg(reinterpret_cast<const uint4*>(src));
+    else v[0] = __ldg(src);
+  };
+  const auto value = [](const uint32_t (&v)[4], int i) {
+    if constexpr (kVec) {
+      const float2 f = pair_to_float2<kBF>(v[i >> 1]);
+      return i & 1 ? f.y : f.x;
+    } else {
+      return elem_to_float<kBF>(static_cast<uint16_t>(v[0]));
     }
-    p.out[t * p.W + c] = float_to_elem<kBF>(a);
+  };
+#pragma unroll
+  for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+  if (p.base) {
+    uint32_t v[4];
+    if constexpr (kVec) *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(p.base + t * p.W + c);  // out may be base
+    else v[0] = p.base[t * p.W + c];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) acc[i] = value(v, i);
   }
+  for (int j0 = 0; j0 < p.k; j0 += BATCH) {
+    uint32_t v[BATCH][4];
+    float w[BATCH];
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) {
+      w[u] = 0.f;
+      v[u][0] = v[u][1] = v[u][2] = v[u][3] = 0u;
+      if (j0 + u < p.k) {
+        const int r = __ldg(p.rows + t * p.k + j0 + u);
+        if (r >= 0 && r < p.R) {
+          w[u] = __ldg(p.weights + t * p.k + j0 + u);
+          load(p.y + static_cast<int64_t>(r) * p.W + c, v[u]);
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) acc[i] += w[u] * value(v[u], i);
+    }
+  }
+  if constexpr (kVec) {
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = static_cast<uint32_t>(float_to_elem<kBF>(acc[2 * i])) | (static_cast<uint32_t>(float_to_elem<kBF>(acc[2 * i + 1])) << 16);
+    *reinterpret_cast<uint4*>(p.out + t * p.W + c) = *reinterpret_cast<const uint4*>(v);
+  } else {
+    p.out[t * p.W + c] = float_to_elem<kBF>(acc[0]);
+  }
+}
+
+// Column runs of a row; rows of more than 65535 runs are not launched.
+unsigned runs(int64_t vectors) { return static_cast<unsigned>((vectors + kRowThreads - 1) / kRowThreads); }
+
+// A launch that may be set up while the kernel before it on the stream still runs; the kernel waits
+// for that one's results itself.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename Vec>
+cudaError_t run_dispatch(const DispatchProblem& p) {
+  const int64_t R = p.T * p.k, vectors = p.W / static_cast<int>(sizeof(Vec) / 2);
+  const dim3 rows(static_cast<unsigned>(p.T), runs(vectors) ? runs(vectors) : 1u);
+  if (rows.y > 65535u) return cudaErrorInvalidConfiguration;
+  if (R <= kFewPlaces && p.k <= kFewK) {
+    dispatch_few_kernel<Vec><<<rows, kRowThreads, (p.E + 1) * 4, p.stream>>>(p);
+    return cudaGetLastError();
+  }
+  const int bins = p.E + 1, blocks = sort_blocks(R);
+  int* dest = static_cast<int*>(p.workspace);
+  int* hist = dest + R;
+  const int smem = (kSortWarps + 2) * bins * 4;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(dispatch_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  dispatch_count_kernel<<<blocks, kSortThreads, bins * 4, p.stream>>>(p, hist);
+  cudaError_t e = launch_early(dispatch_place_kernel, dim3(blocks), kSortThreads, smem, p.stream, p, hist, blocks, dest);
+  if (e == cudaSuccess) e = launch_early(dispatch_copy_kernel<Vec>, rows, kRowThreads, 0, p.stream, p, dest);
+  return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 }  // namespace
@@ -310,27 +541,21 @@ size_t dispatch_workspace_bytes(int64_t R, int E) {
 }
 
 cudaError_t launch_dispatch(const DispatchProblem& p) {
-  const int64_t R = p.T * p.k;
-  const int bins = p.E + 1, blocks = sort_blocks(R);
-  int* dest = static_cast<int*>(p.workspace);
-  int* hist = dest + R;
-  const int smem = (kSortWarps + 1) * bins * 4;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(dispatch_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
-  dispatch_count_kernel<<<blocks, kSortThreads, bins * 4, p.stream>>>(p, hist);
-  dispatch_place_kernel<<<blocks, kSortThreads, smem, p.stream>>>(p, hist, blocks, dest);
-  if (p.W % 8 == 0 && p.ld % 8 == 0 && aligned(p.x, 16) && aligned(p.routed, 16))
-    dispatch_copy_kernel<uint4><<<static_cast<unsigned>(p.T), 256, 0, p.stream>>>(p, dest);
-  else
-    dispatch_copy_kernel<uint16_t><<<static_cast<unsigned>(p.T), 256, 0, p.stream>>>(p, dest);
-  return cudaGetLastError();
+  if (p.W % 8 == 0 && p.ld % 8 == 0 && aligned(p.x, 16) && aligned(p.routed, 16)) return run_dispatch<uint4>(p);
+  return run_dispatch<uint16_t>(p);
 }
 
 cudaError_t launch_combine(const CombineProblem& p) {
-  if (p.bf16) combine_any_kernel<true><<<static_cast<unsigned>(p.T), 256, 0, p.stream>>>(p);
-  else combine_any_kernel<false><<<static_cast<unsigned>(p.T), 256, 0, p.stream>>>(p);
+  const bool vec = p.W % 8 == 0 && aligned(p.y, 16) && aligned(p.out, 16) && aligned(p.base, 16);
+  const dim3 grid(static_cast<unsigned>(p.T), runs(vec ? p.W / 8 : p.W));
+  if (grid.y > 65535u) return cudaErrorInvalidConfiguration;
+  if (vec) {
+    if (p.bf16) combine_kernel<true, true><<<grid, kRowThreads, 0, p.stream>>>(p);
+    else combine_kernel<false, true><<<grid, kRowThreads, 0, p.stream>>>(p);
+  } else {
+    if (p.bf16) combine_kernel<true, false><<<grid, kRowThreads, 0, p.stream>>>(p);
+    else combine_kernel<false, false><<<grid, kRowThreads, 0, p.stream>>>(p);
+  }
   return cudaGetLastError();
 }
 

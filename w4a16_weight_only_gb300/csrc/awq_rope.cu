@@ -105,6 +105,11 @@ __device__ __forceinline__ int64_t cell_of(const RopeProblem& p, int64_t t) {
   return page * p.kv.page_stride + static_cast<int64_t>(slot - page * p.kv.page_size) * p.kv.token_stride;
 }
 
+template <bool kBF>
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  return static_cast<uint32_t>(float_to_elem<kBF>(lo)) | (static_cast<uint32_t>(float_to_elem<kBF>(hi)) << 16);
+}
+
 // Any size, stride and alignment: one thread per pair or copied element.
 template <bool kBF>
 __global__ void __launch_bounds__(128) rope_any_kernel(const RopeProblem p) {
@@ -139,6 +144,96 @@ __global__ void __launch_bounds__(128) rope_any_kernel(const RopeProblem p) {
   }
 }
 
+// Aligned tensors, rotated part and head size multiples of 16.  A thread owns 16 elements of a head, two
+// 16-byte vectors: eight pairs (the vectors at 8 c and rot / 2 + 8 c, or 16 c and 16 c + 8 when
+// interleaved), or 16 elements behind the rotated part.  It keeps its eight cosines and sines and
+// goes through the heads, kUnroll of them in flight, so a table line is read once per token and the
+// tensors once: HBM-bound for many tokens, a single round trip for few.
+constexpr int kRopeThreads = 128;
+constexpr int kUnroll = 4;
+
+template <bool kBF, bool kInterleaved>
+__global__ void __launch_bounds__(kRopeThreads) rope_vec_kernel(const RopeProblem p, int heads_per_block) {
+  const int chunks = p.D / 16, lanes = kRopeThreads / chunks;  // head lanes of the block
+  const int c = threadIdx.x % chunks, lane = threadIdx.x / chunks;
+  if (lane >= lanes) return;
+  const int64_t t = blockIdx.x;
+  const int heads = p.Hq + p.Hkv * (p.append ? 2 : 1);
+  const int h0 = blockIdx.y * heads_per_block, h1 = min(heads, h0 + heads_per_block);
+  const int64_t cell = cell_of(p, t);
+  const bool turns = 16 * c < p.rot;
+  const int ea = turns && !kInterleaved ? 8 * c : 16 * c, eb = turns && !kInterleaved ? p.rot / 2 + 8 * c : 16 * c + 8;
+  float cs[8], sn[8];
+  if (turns) {
+    const int pos = __ldg(p.positions + t);
+    if (pos >= 0 && pos < p.max_position) {
+      const float* line = p.table + static_cast<int64_t>(pos) * p.rot + 8 * c;
+      *reinterpret_cast<float4*>(cs) = __ldg(reinterpret_cast<const float4*>(line));
+      *reinterpret_cast<float4*>(cs + 4) = __ldg(reinterpret_cast<const float4*>(line + 4));
+      *reinterpret_cast<float4*>(sn) = __ldg(reinterpret_cast<const float4*>(line + p.rot / 2));
+      *reinterpret_cast<float4*>(sn + 4) = __ldg(reinterpret_cast<const float4*>(line + p.rot / 2 + 4));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) cs[i] = sn[i] = __int_as_float(0x7fffffff);
+    }
+  }
+  for (int h = h0 + lane; h < h1; h += kUnroll * lanes) {
+    Row r[kUnroll];
+    uint4 va[kUnroll], vb[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      r[u].dst = nullptr;
+      if (h + u * lanes < h1) r[u] = row_of(p, t, h + u * lanes, cell);
+      if (r[u].dst) {
+        va[u] = *reinterpret_cast<const uint4*>(r[u].src + ea);
+        vb[u] = *reinterpret_cast<const uint4*>(r[u].src + eb);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (!r[u].dst) continue;
+      if (turns && r[u].turn) {
+        uint32_t* a = reinterpret_cast<uint32_t*>(&va[u]);
+        uint32_t* b = reinterpret_cast<uint32_t*>(&vb[u]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 x = ptx::pair_to_float2<kBF>(a[i]), y = ptx::pair_to_float2<kBF>(b[i]);
+          if constexpr (kInterleaved) {  // a[i] is pair i, b[i] pair 4 + i
+            a[i] = pack<kBF>(x.x * cs[i] - x.y * sn[i], x.y * cs[i] + x.x * sn[i]);
+            b[i] = pack<kBF>(y.x * cs[4 + i] - y.y * sn[4 + i], y.y * cs[4 + i] + y.x * sn[4 + i]);
+          } else {  // a[i] and b[i] are the first and second elements of pairs 2 i, 2 i + 1
+            a[i] = pack<kBF>(x.x * cs[2 * i] - y.x * sn[2 * i], x.y * cs[2 * i + 1] - y.y * sn[2 * i + 1]);
+            b[i] = pack<kBF>(y.x * cs[2 * i] + x.x * sn[2 * i], y.y * cs[2 * i + 1] + x.y * sn[2 * i + 1]);
+          }
+        }
+      }
+      *reinterpret_cast<uint4*>(r[u].dst + ea) = va[u];
+      *reinterpret_cast<uint4*>(r[u].dst + eb) = vb[u];
+    }
+  }
+}
+
+bool vectors_fit(const RopeProblem& p) {
+  const int64_t strides = p.q_st | p.q_sh | p.k_st | p.k_sh | p.v_st | p.v_sh | p.qo_st | p.qo_sh |
+                          (p.append ? p.kv.page_stride | p.kv.token_stride | p.kv.head_stride : p.ko_st | p.ko_sh);
+  return p.rot % 16 == 0 && p.D % 16 == 0 && p.D / 16 <= kRopeThreads && strides % 8 == 0 && aligned(p.q, 16) && aligned(p.k, 16) &&
+         aligned(p.v, 16) && aligned(p.q_out, 16) && aligned(p.k_out, 16) && aligned(p.table, 16) && aligned(p.kv.k, 16) &&
+         aligned(p.kv.v, 16);
+}
+
+template <bool kBF, bool kInterleaved>
+cudaError_t launch_vec(const RopeProblem& p) {
+  const int heads = p.Hq + p.Hkv * (p.append ? 2 : 1), lanes = kRopeThreads / (p.D / 16);
+  // few tokens: a token's heads over as many blocks as give each thread one head
+  int per = kUnroll * lanes;
+  if (p.T * ((heads + per - 1) / per) < 304) per = lanes;
+  else per = heads;
+  per = per > (heads + 65534) / 65535 ? per : (heads + 65534) / 65535;
+  rope_vec_kernel<kBF, kInterleaved>
+      <<<dim3(static_cast<unsigned>(p.T), static_cast<unsigned>((heads + per - 1) / per)), kRopeThreads, 0, p.stream>>>(p, per);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_rope_table(const RopeTableProblem& p) {
@@ -148,6 +243,10 @@ cudaError_t launch_rope_table(const RopeTableProblem& p) {
 }
 
 cudaError_t launch_rope(const RopeProblem& p) {
+  if (vectors_fit(p)) {
+    if (p.bf16) return p.interleaved ? launch_vec<true, true>(p) : launch_vec<true, false>(p);
+    return p.interleaved ? launch_vec<false, true>(p) : launch_vec<false, false>(p);
+  }
   const unsigned grid = static_cast<unsigned>(p.T < (1 << 20) ? p.T : (1 << 20));
   if (p.bf16) rope_any_kernel<true><<<grid, 128, 0, p.stream>>>(p);
   else rope_any_kernel<false><<<grid, 128, 0, p.stream>>>(p);
