@@ -41,10 +41,30 @@ struct Stream {
   static_assert(BLOCKS * (SMEM + 1024) <= 228 * 1024, "shared memory");
 };
 
+// n / d for 0 <= n < 2^31 by a multiplication: m = ceil(2^(31 + l) / d), l = ceil(log2 d), is below
+// 2^32, and n m / 2^(31 + l) exceeds n / d by less than 1 / d (Granlund and Montgomery, 1994).
+struct Divider {
+  uint32_t m, shift;
+  static Divider by(uint32_t d) {
+    uint32_t l = 0;
+    while ((uint64_t{1} << l) < d) ++l;
+    return {static_cast<uint32_t>(((uint64_t{1} << (31 + l)) + d - 1) / d), 31 + l};
+  }
+  __device__ __forceinline__ int of(int n) const {
+    return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * m) >> shift);
+  }
+};
+
+struct StreamArgs : AttnArgs {
+  Divider page;  // by the page size
+};
+
+constexpr float kRaise = 8.f;  // log2 of the growth that raises a row's maximum
+
 // Where a warp stands: a unit and a step of it.
 struct Cursor {
   int b;       // sequence, -1: the prefix
-  int unit;    // tile * heads + head
+  int tile, hk;  // row tile, key/value head
   int step, steps;
   int len;
 };
@@ -58,7 +78,7 @@ struct Cursor {
 // rows of an m16n8k16 and 8 query rows its columns, so that the usual 8 heads of a group waste
 // nothing and the accumulators are half those of Q K^T.
 template <bool kBF, int D, int NT>
-__global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_stream_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_stream_kernel(const __grid_constant__ StreamArgs a) {
   using ST = Stream<D>;
   constexpr int PITCH = ST::PITCH, STAGES = ST::STAGES;
   extern __shared__ __align__(16) uint16_t smem[];
@@ -111,7 +131,11 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
   // neighbouring warps of the sequence sit on different SMs' schedulers only by block; order as numbered
   const int64_t w = static_cast<int64_t>(blockIdx.x) * kStreamWarps + warp;
   const int64_t x0 = w * per, x1 = min(total, x0 + per);
-  if (x0 >= x1) return;
+  launch_dependents();
+  if (x0 >= x1) {
+    if (pl.tc) grid_dependency_wait();
+    return;
+  }
 
   // the first step's unit
   Cursor at;
@@ -120,8 +144,10 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
     at.b = -1;
     at.len = prefix_len;
     at.steps = steps_of(prefix_len);
-    at.unit = static_cast<int>(x0 / at.steps);
-    at.step = static_cast<int>(x0 - static_cast<int64_t>(at.unit) * at.steps);
+    const int unit = static_cast<int>(x0 / at.steps);
+    at.step = static_cast<int>(x0 - static_cast<int64_t>(unit) * at.steps);
+    at.tile = unit / heads;
+    at.hk = unit - at.tile * heads;
   } else {
     const int64_t q = (x0 - prefix_total) / per_seq;  // in steps of one unit per sequence
     int lo = 0, hi = ST::COARSE - 1;                  // coarse[lo] <= q < coarse[hi]
@@ -149,20 +175,22 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
       }
       before += __shfl_sync(0xffffffffu, incl, 31);
       b0 += 32;
-      if (b0 >= p.B) return;  // not reached: q lies below the last entry
     }
     at.len = length(at.b);
     at.steps = steps_of(at.len);
     const int64_t rem = x0 - prefix_total - before * per_seq;
-    at.unit = static_cast<int>(rem / at.steps);
-    at.step = static_cast<int>(rem - static_cast<int64_t>(at.unit) * at.steps);
+    const int unit = static_cast<int>(rem / at.steps);
+    at.step = static_cast<int>(rem - static_cast<int64_t>(unit) * at.steps);
+    at.tile = unit / heads;
+    at.hk = unit - at.tile * heads;
   }
   unit_start = x0 - at.step;
   const auto advance = [&](Cursor& c) {  // to the first step of the next unit
     c.step = 0;
-    const int units = heads * (c.b < 0 ? pl.prefix_tiles : pl.private_tiles);
-    if (++c.unit < units) return;
-    c.unit = 0;
+    if (++c.hk < heads) return;
+    c.hk = 0;
+    if (++c.tile < (c.b < 0 ? pl.prefix_tiles : pl.private_tiles)) return;
+    c.tile = 0;
     do {
       ++c.b;
       c.len = length(c.b);
@@ -177,18 +205,19 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
   Cursor ahead = at;
   int64_t to_load = x1 - x0;
   uint32_t loaded = 0;  // steps
-  int page_next = 0;
+  int page_next = 0, token_next = 0;
   const auto fetch_page = [&] {
-    const int key = ahead.step * kStreamKeys + (lane & 15);
+    const int key = ahead.step * kStreamKeys + (lane & 15), slot = a.page.of(key);
     const int* table = ahead.b < 0 ? p.prefix_pages : p.pages + ahead.b * p.pages_ld;
-    page_next = key < ahead.len ? __ldg(table + key / p.kv.page_size) : -1;
+    page_next = key < ahead.len ? __ldg(table + slot) : -1;
+    token_next = key - slot * p.kv.page_size;
   };
   const auto load_step = [&] {
     if (to_load > 0) {
-      const int key = ahead.step * kStreamKeys + (lane & 15), page = page_next;
+      const int page = page_next;
       const bool valid = page >= 0 && page < p.kv.num_pages;
-      const int64_t off = page * p.kv.page_stride + static_cast<int64_t>(key % p.kv.page_size) * p.kv.token_stride +
-                          (ahead.unit % heads) * p.kv.head_stride;
+      const int64_t off = page * p.kv.page_stride + static_cast<int64_t>(token_next) * p.kv.token_stride +
+                          ahead.hk * p.kv.head_stride;
       const uint32_t live = __ballot_sync(0xffffffffu, valid);
       --to_load;
       if (++ahead.step == ahead.steps && to_load > 0) advance(ahead);
@@ -220,7 +249,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
   uint32_t used = 0;  // steps
   for (int64_t x = x0; x < x1;) {
     // one run of a unit
-    const int hk = at.unit % heads, row0 = at.unit / heads * (8 * NT);
+    const int hk = at.hk, row0 = at.tile * (8 * NT);
     const int rows = at.b < 0 ? p.B * pl.own_rows : pl.own_rows, b0 = max(at.b, 0);
     const int end = at.step + static_cast<int>(min(static_cast<int64_t>(at.steps - at.step), x1 - x));
     uint32_t qf[NT][D / 16][2];
@@ -271,28 +300,29 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
         for (int m = 0; m < NT; ++m) mma(s[m][c & 1], kf, qf[m][c][0], qf[m][c][1]);
       }
       const int k0 = step * kStreamKeys + (lane >> 2);
-      uint32_t pf[NT][2];
+      float z[NT][2][2];  // [row][keys lane / 4, + 8]
+      bool raise = false;
 #pragma unroll
-      for (int m = 0; m < NT; ++m) {
-        float z[2][2];  // [row][keys lane / 4, + 8]
+      for (int m = 0; m < NT; ++m)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             const float v = s[m][0][2 * t + h] + s[m][1][2 * t + h];
-            z[h][t] = k0 + 8 * t < limit[m][h] ? v * scale : -INFINITY;
+            z[m][h][t] = k0 + 8 * t < limit[m][h] ? v * scale : -INFINITY;
           }
+          raise |= fmaxf(z[m][h][0], z[m][h][1]) > top[m][h] + kRaise;  // always where no key was seen yet
         }
-        float best[2] = {fmaxf(z[0][0], z[0][1]), fmaxf(z[1][0], z[1][1])};
+      // a row's maximum is raised when a logit exceeds it by 8 (p is up to 256 until then)
+      if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) {
-          best[0] = fmaxf(best[0], __shfl_xor_sync(0xffffffffu, best[0], d));
-          best[1] = fmaxf(best[1], __shfl_xor_sync(0xffffffffu, best[1], d));
-        }
-        if (__any_sync(0xffffffffu, best[0] > top[m][0] || best[1] > top[m][1])) {
+        for (int m = 0; m < NT; ++m)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float now = fmaxf(top[m][h], best[h]);
+            float now = fmaxf(z[m][h][0], z[m][h][1]);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, d));
+            now = fmaxf(now, top[m][h]);
             const float shrink = now == -INFINITY ? 1.f : exp2_approx(top[m][h] - now);
             top[m][h] = now;
             sum[m][h] *= shrink;
@@ -302,17 +332,20 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
               o[m][c][2 + h] *= shrink;
             }
           }
-        }
+      }
+      uint32_t pf[NT][2];
+#pragma unroll
+      for (int m = 0; m < NT; ++m) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const float ref = top[m][h] == -INFINITY ? 0.f : top[m][h];  // a row that has seen no key yet
-          z[h][0] = exp2_approx(z[h][0] - ref);
-          z[h][1] = exp2_approx(z[h][1] - ref);
-          sum[m][h] += z[h][0] + z[h][1];
+          z[m][h][0] = exp2_approx(z[m][h][0] - ref);
+          z[m][h][1] = exp2_approx(z[m][h][1] - ref);
+          sum[m][h] += z[m][h][0] + z[m][h][1];
         }
         // P^T has keys along the lanes' rows; the second product wants them along the registers
-        pf[m][0] = transpose8(pack2<kBF>(z[0][0], z[1][0]));
-        pf[m][1] = transpose8(pack2<kBF>(z[0][1], z[1][1]));
+        pf[m][0] = transpose8(pack2<kBF>(z[m][0][0], z[m][1][0]));
+        pf[m][1] = transpose8(pack2<kBF>(z[m][0][1], z[m][1][1]));
       }
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
@@ -346,7 +379,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
         }
       }
     if (end == at.steps && lane == 0)
-      a.counts[at.b < 0 ? at.unit : (pl.tc ? 0 : pl.prefix_tiles * heads) + at.b * per_seq + at.unit] = part + 1;
+      a.counts[(at.b < 0 ? 0 : pl.prefix_tiles * heads + at.b * per_seq) + at.tile * heads + at.hk] = part + 1;
     x += end - at.step;
     if (x < x1) {
       advance(at);
@@ -354,6 +387,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
     }
   }
   cp_async_wait<0>();
+  if (pl.tc) grid_dependency_wait();  // so that this kernel's end is also the tensor-core kernel's
 }
 
 // Joins a row's parts.  One warp per row; a lane holds the (m, l) of every 32nd part and D / 32
@@ -368,6 +402,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
   if (r >= rows) return;
   const int64_t bi = r / p.Hq;
   const int h = static_cast<int>(r - bi * p.Hq), hk = h / pl.group, b = static_cast<int>(bi / p.n);
+  grid_dependency_wait();  // the parts
   int first = 0, own = 0;  // parts of the prefix, at slots 0 ..; own parts, at slots prefix_parts ..
   if (p.prefix_len > 0) {
     const int64_t stacked = bi * pl.group + h % pl.group;
@@ -476,14 +511,34 @@ Layout layout(const AttentionProblem& p, const Plan& pl) {
   return l;
 }
 
+// The kernel, set up (and where there is room run) while the one before it still runs; it waits for
+// that one's end itself.
+template <typename A>
+cudaError_t launch_early(void (*kernel)(A), unsigned blocks, int threads, size_t smem, cudaStream_t stream, const A& a, bool early) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
 template <bool kBF, int D, int NT>
-cudaError_t run_stream(const AttnArgs& a) {
-  if (a.plan.blocks == 0) return cudaSuccess;
+cudaError_t run_stream(const AttnArgs& attn) {
+  if (attn.plan.blocks == 0) return cudaSuccess;
   constexpr int smem = Stream<D>::SMEM;
-  cudaError_t e = cudaFuncSetAttribute(attn_stream_kernel<kBF, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const auto kernel = attn_stream_kernel<kBF, D, NT>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  attn_stream_kernel<kBF, D, NT><<<a.plan.blocks, kStreamWarps * 32, smem, a.p.stream>>>(a);
-  return cudaGetLastError();
+  StreamArgs a{};
+  static_cast<AttnArgs&>(a) = attn;
+  a.page = Divider::by(static_cast<uint32_t>(attn.p.kv.page_size));
+  return launch_early(kernel, attn.plan.blocks, kStreamWarps * 32, smem, attn.p.stream, a, attn.plan.tc);
 }
 
 template <bool kBF, int D>
@@ -495,8 +550,7 @@ cudaError_t run(const AttnArgs& a) {
   else if constexpr (D <= 128) e = run_stream<kBF, D, 4>(a);
   if (e != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(a.p.B) * a.p.n * a.p.Hq;
-  attn_join_kernel<kBF, D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, a.p.stream>>>(a);
-  return cudaGetLastError();
+  return launch_early(attn_join_kernel<kBF, D>, static_cast<unsigned>((rows + 3) / 4), 128, 0, a.p.stream, a, a.plan.blocks > 0);
 }
 
 template <bool kBF>

@@ -232,6 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  launch_dependents();
 
   // Bounded waits; a role that gives up sets the flag, and the others leave at their next wait.
   // All lanes of a warp wait together and get one answer.
