@@ -64,7 +64,7 @@ constexpr float kRaise = 8.f;  // log2 of the growth that raises a row's maximum
 // Where a warp stands: a unit and a step of it.
 struct Cursor {
   int b;       // sequence, -1: the prefix
-  int tile, hk;  // row tile, key/value head
+  int tile;    // row tile
   int step, steps;
   int len;
 };
@@ -123,14 +123,11 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
     }
     __syncthreads();
   }
-  const int64_t prefix_total = pl.tc ? 0 : static_cast<int64_t>(steps_of(prefix_len)) * heads * pl.prefix_tiles;
-  const int64_t per_seq = static_cast<int64_t>(heads) * pl.private_tiles;  // units of a sequence
-  const int64_t total = prefix_total + (pl.private_parts ? coarse[ST::COARSE - 1] * per_seq : 0);
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * kStreamWarps;
-  const int64_t per = max(static_cast<int64_t>(pl.per_min), (total + warps - 1) / warps);
-  // neighbouring warps of the sequence sit on different SMs' schedulers only by block; order as numbered
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * kStreamWarps + warp;
-  const int64_t x0 = w * per, x1 = min(total, x0 + per);
+  const int64_t prefix_total = pl.tc ? 0 : static_cast<int64_t>(steps_of(prefix_len)) * pl.prefix_tiles;
+  const int64_t total = prefix_total + (pl.private_parts ? coarse[ST::COARSE - 1] * pl.private_tiles : 0);
+  const int64_t per = max(static_cast<int64_t>(pl.per_min), (total + pl.shares - 1) / pl.shares);
+  const int w = blockIdx.x * kStreamWarps + warp, hk = w % heads, share = w / heads;
+  const int64_t x0 = share * per, x1 = share < pl.shares ? min(total, x0 + per) : x0;
   launch_dependents();
   if (x0 >= x1) {
     if (pl.tc) grid_dependency_wait();
@@ -140,55 +137,47 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
   // the first step's unit
   Cursor at;
   int64_t unit_start;  // of the unit's first step, among all
-  if (x0 < prefix_total) {
-    at.b = -1;
-    at.len = prefix_len;
-    at.steps = steps_of(prefix_len);
-    const int unit = static_cast<int>(x0 / at.steps);
-    at.step = static_cast<int>(x0 - static_cast<int64_t>(unit) * at.steps);
-    at.tile = unit / heads;
-    at.hk = unit - at.tile * heads;
-  } else {
-    const int64_t q = (x0 - prefix_total) / per_seq;  // in steps of one unit per sequence
-    int lo = 0, hi = ST::COARSE - 1;                  // coarse[lo] <= q < coarse[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (coarse[mid] <= q) lo = mid;
-      else hi = mid;
-    }
-    int64_t before = coarse[lo];
-    int b0 = lo * gran;
-    while (true) {  // 32 sequences at a time
-      const int n = steps_of(length(b0 + lane));
-      int incl = n;
+  {
+    int64_t rem = x0;
+    if (x0 < prefix_total) {
+      at.b = -1;
+      at.len = prefix_len;
+    } else {
+      const int64_t q = (x0 - prefix_total) / pl.private_tiles;  // in steps of one tile per sequence
+      int lo = 0, hi = ST::COARSE - 1;                           // coarse[lo] <= q < coarse[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (coarse[mid] <= q) lo = mid;
+        else hi = mid;
+      }
+      int64_t before = coarse[lo];
+      for (int b0 = lo * gran;; b0 += 32) {  // 32 sequences at a time; q lies below the last entry
+        const int n = steps_of(length(b0 + lane));
+        int incl = n;
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += o;
+        for (int d = 1; d < 32; d <<= 1) {
+          const int o = __shfl_up_sync(0xffffffffu, incl, d);
+          if (lane >= d) incl += o;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, before + incl > q);
+        if (past) {
+          const int l = __ffs(past) - 1;
+          before += __shfl_sync(0xffffffffu, incl - n, l);
+          at.b = b0 + l;
+          break;
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
       }
-      const unsigned past = __ballot_sync(0xffffffffu, before + incl > q);
-      if (past) {
-        const int l = __ffs(past) - 1;
-        before += __shfl_sync(0xffffffffu, incl - n, l);
-        at.b = b0 + l;
-        break;
-      }
-      before += __shfl_sync(0xffffffffu, incl, 31);
-      b0 += 32;
+      at.len = length(at.b);
+      rem = x0 - prefix_total - before * pl.private_tiles;
     }
-    at.len = length(at.b);
     at.steps = steps_of(at.len);
-    const int64_t rem = x0 - prefix_total - before * per_seq;
-    const int unit = static_cast<int>(rem / at.steps);
-    at.step = static_cast<int>(rem - static_cast<int64_t>(unit) * at.steps);
-    at.tile = unit / heads;
-    at.hk = unit - at.tile * heads;
+    at.tile = static_cast<int>(rem / at.steps);
+    at.step = static_cast<int>(rem - static_cast<int64_t>(at.tile) * at.steps);
   }
   unit_start = x0 - at.step;
   const auto advance = [&](Cursor& c) {  // to the first step of the next unit
     c.step = 0;
-    if (++c.hk < heads) return;
-    c.hk = 0;
     if (++c.tile < (c.b < 0 ? pl.prefix_tiles : pl.private_tiles)) return;
     c.tile = 0;
     do {
@@ -217,7 +206,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
       const int page = page_next;
       const bool valid = page >= 0 && page < p.kv.num_pages;
       const int64_t off = page * p.kv.page_stride + static_cast<int64_t>(token_next) * p.kv.token_stride +
-                          ahead.hk * p.kv.head_stride;
+                          hk * p.kv.head_stride;
       const uint32_t live = __ballot_sync(0xffffffffu, valid);
       --to_load;
       if (++ahead.step == ahead.steps && to_load > 0) advance(ahead);
@@ -249,7 +238,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
   uint32_t used = 0;  // steps
   for (int64_t x = x0; x < x1;) {
     // one run of a unit
-    const int hk = at.hk, row0 = at.tile * (8 * NT);
+    const int row0 = at.tile * (8 * NT);
     const int rows = at.b < 0 ? p.B * pl.own_rows : pl.own_rows, b0 = max(at.b, 0);
     const int end = at.step + static_cast<int>(min(static_cast<int64_t>(at.steps - at.step), x1 - x));
     uint32_t qf[NT][D / 16][2];
@@ -357,8 +346,8 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
       __syncwarp();  // the next load_step overwrites a stage read here
     }
 
-    // the part: slot = this warp's number among those that share the unit
-    const int part = static_cast<int>(w - unit_start / per);
+    // the part: slot = this share's number among those that meet in the unit
+    const int part = static_cast<int>(share - unit_start / per);
 #pragma unroll
     for (int m = 0; m < NT; ++m)
 #pragma unroll
@@ -379,7 +368,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
         }
       }
     if (end == at.steps && lane == 0)
-      a.counts[(at.b < 0 ? 0 : pl.prefix_tiles * heads + at.b * per_seq) + at.tile * heads + at.hk] = part + 1;
+      a.counts[(at.b < 0 ? at.tile : pl.prefix_tiles + static_cast<int64_t>(at.b) * pl.private_tiles + at.tile) * heads + hk] = part + 1;
     x += end - at.step;
     if (x < x1) {
       advance(at);
@@ -482,15 +471,16 @@ Plan make_plan(const AttentionProblem& p, int sms) {
     pl.prefix_tiles = ceil_div(stacked, tile);
   }
   if (p.max_len > 0) pl.private_tiles = ceil_div(pl.own_rows, tile);
-  // most steps that the streaming kernel can have; the lengths, known on the device only, may add up
-  // to less, so shares go down to a quarter of what this many would give each warp
+  // most steps that the streaming kernel can have per head; the lengths, known on the device only, may
+  // add up to less, so shares go down to a quarter of what this many would give each warp
   const int64_t prefix_steps = pl.tc ? 0 : ceil_div(p.prefix_len, kStreamKeys);
   const int64_t own_steps = ceil_div(p.max_len, kStreamKeys);
-  const int64_t total = p.kv.heads * (prefix_steps * pl.prefix_tiles + own_steps * p.B * pl.private_tiles);
-  const int64_t blocks = static_cast<int64_t>(sms) * (p.kv.head_dim <= 128 ? 2 : 1);
-  const int64_t share = (total + blocks * kStreamWarps - 1) / (blocks * kStreamWarps);
-  pl.per_min = static_cast<int>(max(int64_t{2}, min(share / 4, int64_t{1} << 20)));
-  pl.blocks = static_cast<int>(min(blocks, (total + pl.per_min * kStreamWarps - 1) / (pl.per_min * kStreamWarps)));
+  const int64_t total = prefix_steps * pl.prefix_tiles + own_steps * p.B * pl.private_tiles;
+  const int64_t warps = static_cast<int64_t>(sms) * (p.kv.head_dim <= 128 ? 2 : 1) * kStreamWarps;
+  const int64_t shares = max(int64_t{1}, warps / p.kv.heads);
+  pl.per_min = static_cast<int>(max(int64_t{2}, min((total + shares - 1) / shares / 4, int64_t{1} << 20)));
+  pl.shares = static_cast<int>(min(shares, (total + pl.per_min - 1) / pl.per_min));
+  pl.blocks = ceil_div(static_cast<int64_t>(pl.shares) * p.kv.heads, kStreamWarps);
   if (pl.prefix_tiles) pl.prefix_parts = static_cast<int>((prefix_steps - 1) / pl.per_min + 2);
   if (p.max_len > 0) pl.private_parts = static_cast<int>((own_steps - 1) / pl.per_min + 2);
   pl.parts = pl.prefix_parts + pl.private_parts;

@@ -46,10 +46,11 @@ __device__ __forceinline__ void cp_async_wait() {
 // per).
 //
 // Streaming kernel (the sequences' own keys, and the prefix's without tc): units are (sequence, row
-// tile, key/value head), the prefix being a sequence of its own in front; a unit of L keys has
-// ceil(L / kStreamKeys) steps; all steps of all units form one sequence of which warp w takes [w per,
-// (w + 1) per), per = max(per_min, total / warps) being found on the device, where the lengths are.
-// The warp that ends a unit writes the unit's number of parts.
+// tile), the prefix being a sequence of its own in front; a unit of L keys has ceil(L / kStreamKeys)
+// steps; all steps of all units form one sequence of which share i takes [i per, (i + 1) per), per =
+// max(per_min, total / shares) being found on the device, where the lengths are.  Every key/value head
+// has a warp for each share: neighbouring warps read neighbouring heads of the same tokens at the
+// same time.  The warp that ends a unit writes the unit's number of parts.
 struct Plan {
   int group;  // query heads per key/value head
   int own_rows;  // rows of one sequence that share a key/value head
@@ -57,7 +58,7 @@ struct Plan {
   int tc_tiles, tc_steps, tc_per, tc_blocks;
   int tile;                          // rows of a streaming unit
   int prefix_tiles, private_tiles;   // row tiles per key/value head of the streaming units
-  int per_min, blocks;               // streaming kernel
+  int per_min, shares, blocks;       // streaming kernel
   int prefix_parts, private_parts;   // most parts of a row
   int parts;                         // their sum
 };
@@ -81,7 +82,7 @@ struct AttnArgs {
   Plan plan;
   float* part_o;
   float2* part_ml;
-  int* counts;  // parts of each streaming unit: [prefix_tiles][heads], then [B][private_tiles][heads]
+  int* counts;  // parts of each streaming unit, per head: [prefix_tiles][heads], then [B][private_tiles][heads]
   unsigned int* status;
 };
 
