@@ -396,8 +396,8 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
   if (p.prefix_len > 0) {
     const int64_t stacked = bi * pl.group + h % pl.group;
     if (pl.tc) {
-      const int t = hk * pl.tc_tiles + static_cast<int>(stacked / kTcRows);
-      first = tc_last_block(pl, t) - tc_first_block(pl, t) + 1;
+      const int u = tc_unit(pl, hk, static_cast<int>(stacked / kTcRows));
+      first = tc_last_group(pl, u) - tc_first_group(pl, u) + 1;
     } else {
       first = a.counts[stacked / pl.tile * p.kv.heads + hk];
     }
@@ -456,17 +456,20 @@ Plan make_plan(const AttentionProblem& p, int sms) {
   pl.group = p.Hq / p.kv.heads;
   pl.own_rows = p.n * pl.group;
   const int64_t stacked = static_cast<int64_t>(p.B) * pl.own_rows;  // rows that share a prefix key
-  pl.tc = p.prefix_len > 0 && tc_head_dim_supported(p.kv.head_dim) && stacked > 32;
+  // from 33 rows on; its steps are counted in 32 bits
+  pl.tc = p.prefix_len > 0 && tc_head_dim_supported(p.kv.head_dim) && stacked > 32 &&
+          static_cast<int64_t>(p.kv.heads) * ceil_div(stacked, kTcRows) * ceil_div(p.prefix_len, kTcKeys) < (int64_t{1} << 30);
   const int64_t rows = pl.tc || p.prefix_len == 0 ? pl.own_rows : stacked;
   pl.tile = rows <= 8 ? 8 : rows <= 16 || p.kv.head_dim > 128 ? 16 : 32;
   const int tile = pl.tile;
   if (pl.tc) {
     pl.tc_tiles = ceil_div(stacked, kTcRows);
     pl.tc_steps = ceil_div(p.prefix_len, kTcKeys);
-    const int64_t total = static_cast<int64_t>(p.kv.heads) * pl.tc_tiles * pl.tc_steps;
-    pl.tc_per = max(2, ceil_div(total, sms));
-    pl.tc_blocks = ceil_div(total, pl.tc_per);
-    pl.prefix_parts = min((pl.tc_steps - 1) / pl.tc_per + 2, pl.tc_blocks);
+    pl.tc_lanes = pl.tc_tiles <= sms ? pl.tc_tiles : 1;
+    const int total = p.kv.heads * (pl.tc_tiles / pl.tc_lanes) * pl.tc_steps;
+    pl.tc_per = max(2, ceil_div(total, sms / pl.tc_lanes));
+    pl.tc_groups = ceil_div(total, pl.tc_per);
+    pl.prefix_parts = min((pl.tc_steps - 1) / pl.tc_per + 2, pl.tc_groups);
   } else if (p.prefix_len > 0) {
     pl.prefix_tiles = ceil_div(stacked, tile);
   }

@@ -41,9 +41,11 @@ __device__ __forceinline__ void cp_async_wait() {
 // part_o[(r parts + s) D], part_ml[r parts + s]; slots [0, prefix_parts) are the prefix's, the others
 // the sequence's own.
 //
-// Tensor-core kernel (tc, the prefix's keys): tiles of kTcRows rows per key/value head, kTcKeys-key
-// steps per tile; all steps of all tiles form one sequence of which block c takes [c per, (c + 1)
-// per).
+// Tensor-core kernel (tc, the prefix's keys): row tiles of kTcRows rows per key/value head, steps of
+// kTcKeys keys.  The row tiles of a head go side by side, one block each (tc_lanes blocks, a group), so
+// that they read the same keys at the same time and HBM is read once; the steps of all heads form one
+// sequence of which group g takes [g per, (g + 1) per).  (More row tiles than SMs: a group is one block,
+// and the steps of all heads' tiles form the sequence.)
 //
 // Streaming kernel (the sequences' own keys, and the prefix's without tc): units are (sequence, row
 // tile), the prefix being a sequence of its own in front; a unit of L keys has ceil(L / kStreamKeys)
@@ -55,7 +57,7 @@ struct Plan {
   int group;  // query heads per key/value head
   int own_rows;  // rows of one sequence that share a key/value head
   bool tc;
-  int tc_tiles, tc_steps, tc_per, tc_blocks;
+  int tc_tiles, tc_steps, tc_lanes, tc_per, tc_groups;
   int tile;                          // rows of a streaming unit
   int prefix_tiles, private_tiles;   // row tiles per key/value head of the streaming units
   int per_min, shares, blocks;       // streaming kernel
@@ -69,13 +71,10 @@ constexpr int kStreamWarps = 4;
 constexpr int kTcRows = 256;  // two 128-row tensor-core tiles
 constexpr int kTcKeys = 128;
 
-// First and last block of tile t's steps.
-__host__ __device__ inline int tc_first_block(const Plan& pl, int t) {
-  return static_cast<int>(static_cast<int64_t>(t) * pl.tc_steps / pl.tc_per);
-}
-__host__ __device__ inline int tc_last_block(const Plan& pl, int t) {
-  return static_cast<int>((static_cast<int64_t>(t + 1) * pl.tc_steps - 1) / pl.tc_per);
-}
+// Unit (of the sequence of steps) of a head's row tile; first and last group of a unit's steps.
+__host__ __device__ inline int tc_unit(const Plan& pl, int hk, int tile) { return pl.tc_lanes > 1 ? hk : hk * pl.tc_tiles + tile; }
+__host__ __device__ inline int tc_first_group(const Plan& pl, int u) { return u * pl.tc_steps / pl.tc_per; }
+__host__ __device__ inline int tc_last_group(const Plan& pl, int u) { return ((u + 1) * pl.tc_steps - 1) / pl.tc_per; }
 
 struct AttnArgs {
   AttentionProblem p;

@@ -3,9 +3,11 @@
 //
 //   S = Q K^T (128 x 128 fp32 in TMEM),  P = exp2(scale log2(e) S - m),  O += P V (128 x D in TMEM)
 //
-// One block per SM.  All (tile, 128-key step) pairs form one sequence that is cut evenly over the
-// blocks (a tile's keys cut between blocks give one part each; the join kernel adds them), so the
-// SMs finish together whatever the number of tiles.
+// One block per SM.  The row tiles of a head run side by side in a group of blocks, which so read the
+// same keys at the same time (cut one after the other, four tiles read 491 MB of HBM for the 134 MB
+// there are); the 128-key steps of all heads form one sequence that is cut evenly over the groups (a
+// head's keys cut between groups give one part each; the join kernel adds them), so the SMs finish
+// together whatever the number of heads.
 //
 // Warps: 0-3 and 4-7 softmax of the tile's first and second 128 rows, one row per thread (a row's
 // maximum and sum need no shuffles); 8 and 9 load keys and values into a ring of five 128-token slots
@@ -45,8 +47,8 @@ struct Shape {
   static constexpr int Q_OFF = 0;
   static constexpr int RING_OFF = 2 * TILE;
   static constexpr int BAR_OFF = RING_OFF + kSlots * TILE;
-  // full[kSlots], empty[kSlots], q_full[2], s_full[2], p_full[2], pv_done[2], drain
-  static constexpr int NBARS = 2 * kSlots + 9;
+  // full[kSlots], empty[kSlots], q_full[2], s_full[2], p_half[2], p_full[2], pv_done[2], drain
+  static constexpr int NBARS = 2 * kSlots + 11;
   static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;  // TMEM base, abort flag
   static constexpr int SMEM = 1024 + MISC_OFF + 16;
   static_assert(SMEM <= 227 * 1024, "shared memory");
@@ -167,13 +169,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
-// One 32-byte store.
-__device__ __forceinline__ void st_global8(float* p, const float* v) {
-  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]),
-               "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
-               : "memory");
-}
-
 struct TcArgs : AttnArgs {
   CUtensorMap map_k, map_v;  // the cache as [page][head][token][element]
   int box_tokens;
@@ -198,7 +193,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
   uint64_t* empty = full + kSlots;
   uint64_t* q_full = empty + kSlots;
   uint64_t* s_full = q_full + 2;
-  uint64_t* p_full = s_full + 2;
+  uint64_t* p_half = s_full + 2;
+  uint64_t* p_full = p_half + 2;
   uint64_t* pv_done = p_full + 2;
   uint64_t* drain = pv_done + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SH::MISC_OFF);
@@ -216,6 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
     for (int h = 0; h < 2; ++h) {
       mbar_init(&q_full[h], 4);  // the half's softmax warps
       mbar_init(&s_full[h], 1);
+      mbar_init(&p_half[h], 4);
       mbar_init(&p_full[h], 4);
       mbar_init(&pv_done[h], 1);
     }
@@ -253,22 +250,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
   };
 
   // this block's steps, tile by tile
-  const int64_t total = static_cast<int64_t>(p.kv.heads) * pl.tc_tiles * pl.tc_steps;
-  const int64_t s_begin = static_cast<int64_t>(blockIdx.x) * pl.tc_per;
-  const int64_t s_end = min(total, s_begin + pl.tc_per);
+  const int total = p.kv.heads * (pl.tc_tiles / pl.tc_lanes) * pl.tc_steps;
+  const int group = blockIdx.x / pl.tc_lanes, tile_lane = blockIdx.x - group * pl.tc_lanes;
+  const int s_begin = group * pl.tc_per, s_end = min(total, s_begin + pl.tc_per);
   const int stacked = p.B * p.n * pl.group;
   struct Segment {
     int hk, row0, halves, step0, steps, part;
   };
-  const auto segment = [&](int64_t at) {
+  const auto segment = [&](int at) {
     Segment s;
-    const int t = static_cast<int>(at / pl.tc_steps);
-    s.hk = t / pl.tc_tiles;
-    s.row0 = (t - s.hk * pl.tc_tiles) * kTcRows;
+    const int u = at / pl.tc_steps;
+    s.hk = pl.tc_lanes > 1 ? u : u / pl.tc_tiles;
+    s.row0 = (pl.tc_lanes > 1 ? tile_lane : u - s.hk * pl.tc_tiles) * kTcRows;
     s.halves = stacked - s.row0 > 128 ? 2 : 1;
-    s.step0 = static_cast<int>(at - static_cast<int64_t>(t) * pl.tc_steps);
-    s.steps = static_cast<int>(min(static_cast<int64_t>(pl.tc_steps - s.step0), s_end - at));
-    s.part = static_cast<int>(blockIdx.x) - tc_first_block(pl, t);
+    s.step0 = at - u * pl.tc_steps;
+    s.steps = min(pl.tc_steps - s.step0, s_end - at);
+    s.part = group - tc_first_group(pl, u);
     return s;
   };
 
@@ -285,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
       const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
       const float sl = fabsf(p.scale) * kLog2e;
       uint32_t steps_done = 0, segs = 0;
-      for (int64_t at = s_begin; at < s_end;) {
+      for (int at = s_begin; at < s_end;) {
         const Segment sg = segment(at);
         at += sg.steps;
         if (h >= sg.halves) continue;
@@ -322,20 +319,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
           if (!wait(&s_full[h], steps_done & 1u)) return;
           tc_fence_after();
           float s[128];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, s + 32 * c);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_wait_ld32(s + 32 * c);
-          const int left = static_cast<int>(p.prefix_len) - (sg.step0 + j) * kTcKeys;
-          if (left < kTcKeys) {
-#pragma unroll
-            for (int i = 0; i < 128; ++i) s[i] = i < left ? s[i] : -INFINITY;
-          }
           float mx[4] = {m, m, m, m};
+          const int left = static_cast<int>(p.prefix_len) - (sg.step0 + j) * kTcKeys;
+          tmem_ld32(ts, s);
+          tmem_ld32(ts + 32, s + 32);
+          tmem_wait_ld32(s);
+          tmem_wait_ld32(s + 32);
+          tmem_ld32(ts + 64, s + 64);
+          tmem_ld32(ts + 96, s + 96);
 #pragma unroll
-          for (int i = 0; i < 128; i += 8) {
+          for (int c = 0; c < 2; ++c) {
+            if (c) {
+              tmem_wait_ld32(s + 64);
+              tmem_wait_ld32(s + 96);
+            }
+            if (left < 64 * c + 64) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], fmaxf(s[i + 2 * c], s[i + 2 * c + 1]));
+              for (int i = 64 * c; i < 64 * c + 64; ++i) s[i] = i < left ? s[i] : -INFINITY;
+            }
+#pragma unroll
+            for (int i = 64 * c; i < 64 * c + 64; i += 8) {
+#pragma unroll
+              for (int x = 0; x < 4; ++x) mx[x] = fmaxf(mx[x], fmaxf(s[i + 2 * x], s[i + 2 * x + 1]));
+            }
           }
           const float now = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           const bool raise = (now - m) * sl > kRaise || (m == -INFINITY && now > m);
@@ -371,26 +377,39 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
               u[i] = pack2<kBF>(e.x, e.y);
             }
             tmem_st16(ts + 16 * c, u);
+            if (c & 1) {  // the product of the first 64 keys starts while the others' P is made
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(c == 1 ? &p_half[h] : &p_full[h]);
+            }
           }
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[h]);
         }
         if (!wait(&pv_done[h], (steps_done - 1) & 1u)) return;
         tc_fence_after();
         const int64_t out_row = static_cast<int64_t>(bi) * p.Hq + sg.hk * pl.group + g;
         const int64_t slot = out_row * pl.parts + sg.part;
+        // Rows are turned in shared memory, 32 columns at a time, so that a store writes four whole 128-byte
+        // lines (a thread's own row would be 32 partial ones); the warp's share of the query tile is free.
+        float4* turn = reinterpret_cast<float4*>(q_tile + (warp & 3) * 4096);
+        const unsigned rows = __ballot_sync(0xffffffffu, in);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           float o[32];
           tmem_ld32(to + 32 * c, o);
           tmem_wait_ld32(o);
-          if (in) {
+          __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) st_global8(a.part_o + slot * D + 32 * c + i, o + i);
+          for (int i = 0; i < 8; ++i) turn[lane * 8 + (i ^ (lane & 7))] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int k = 4 * i + (lane >> 3), x = lane & 7;  // piece x of row k
+            const int64_t to_slot = __shfl_sync(0xffffffffu, slot, k);
+            if ((rows >> k) & 1u) *reinterpret_cast<float4*>(a.part_o + to_slot * D + 32 * c + 4 * x) = turn[k * 8 + (x ^ (k & 7))];
           }
         }
+        __syncwarp();
         tc_fence_before();
         if (in) a.part_ml[slot] = make_float2(m * sl, (sum0.x + sum0.y) + (sum1.x + sum1.y));
         ++segs;
@@ -413,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
       if (lane == 0) mbar_arrive(&full[i % kSlots]);
     };
     [&] {
-      for (int64_t at = s_begin; at < s_end;) {
+      for (int at = s_begin; at < s_end;) {
         const Segment sg = segment(at);
         at += sg.steps;
         for (int j = 0; j < sg.steps; ++j, item += 2) {
@@ -505,18 +524,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
         }
         __syncwarp();
       };
-      const auto pv = [&](uint32_t h, uint32_t sl, bool accumulate, bool last) {
-        const uint64_t bd = sw128_desc(ring + sl * SH::TILE, SH::PANEL);
+      // the products of the step's first (part 0) or last 64 keys
+      const auto pv = [&](uint32_t h, uint32_t sl, uint32_t part, bool accumulate, bool last) {
+        const uint64_t bd = sw128_desc(ring + sl * SH::TILE + part * 4 * 2048, SH::PANEL);
+        const uint32_t o = tm + kColO + h * 128, pa = tm + kColS + h * 128 + part * 32;
         if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kTcKeys / 16; ++k)
-            mma_ts(tm + kColO + h * 128, tm + kColS + h * 128 + 8 * k, bd + ((k * 2048) >> 4), kPV, accumulate || k > 0);
-          mma_commit(&pv_done[h]);
-          if (last) mma_commit(&empty[sl]);
+          for (int k = 0; k < kTcKeys / 32; ++k) mma_ts(o, pa + 8 * k, bd + ((k * 2048) >> 4), kPV, accumulate || k > 0);
+          if (part) {
+            mma_commit(&pv_done[h]);
+            if (last) mma_commit(&empty[sl]);
+          }
         }
         __syncwarp();
       };
-      for (int64_t at = s_begin; at < s_end;) {
+      for (int at = s_begin; at < s_end;) {
         const Segment sg = segment(at);
         at += sg.steps;
         const bool two = sg.halves == 2;
@@ -533,18 +555,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
           next();
           const uint32_t k = slot, k_phase = phase;
           if (more) next();
-          if (!wait(&full[v], v_phase) || !wait(&p_full[0], done0++ & 1u)) return;
+          if (!wait(&full[v], v_phase) || !wait(&p_half[0], done0 & 1u)) return;
           tc_fence_after();
-          pv(0, v, j > 0, !two);
+          pv(0, v, 0, j > 0, !two);
+          if (!wait(&p_full[0], done0++ & 1u)) return;
+          tc_fence_after();
+          pv(0, v, 1, true, !two);
           if (more) {
             if (!wait(&full[k], k_phase)) return;
             tc_fence_after();
             qk(0, k, !two);
           }
           if (two) {
+            if (!wait(&p_half[1], done1 & 1u)) return;
+            tc_fence_after();
+            pv(1, v, 0, j > 0, true);
             if (!wait(&p_full[1], done1++ & 1u)) return;
             tc_fence_after();
-            pv(1, v, j > 0, true);
+            pv(1, v, 1, true, true);
             if (more) qk(1, k, true);
           }
         }
@@ -593,7 +621,7 @@ cudaError_t run(const AttnArgs& attn) {
   const cudaError_t e =
       cudaFuncSetAttribute(attn_prefix_kernel<kBF, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::SMEM);
   if (e != cudaSuccess) return e;
-  attn_prefix_kernel<kBF, D><<<a.plan.tc_blocks, kThreads, Shape<D>::SMEM, a.p.stream>>>(a);
+  attn_prefix_kernel<kBF, D><<<a.plan.tc_groups * a.plan.tc_lanes, kThreads, Shape<D>::SMEM, a.p.stream>>>(a);
   return cudaGetLastError();
 }
 
