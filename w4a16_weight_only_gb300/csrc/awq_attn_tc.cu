@@ -10,7 +10,7 @@
 // together whatever the number of heads.
 //
 // Warps: 0-3 and 4-7 softmax of the tile's first and second 128 rows, one row per thread (a row's
-// maximum and sum need no shuffles); 8 and 9 load keys and values into a ring of five 128-token slots
+// maximum and sum need no shuffles); 8 and 9 load keys and values into a ring of four 128-token slots
 // (TMA boxes of whole runs of a page's tokens; cp.async where pages are odd and where the prefix
 // ends); 10 issues the MMAs.  While one half's softmax runs, the tensor core works for the other half:
 // PV(a), QK(a) of the next step, PV(b), QK(b).  P, rounded to the element type, overwrites the S it
@@ -30,7 +30,9 @@ using namespace ptx;
 using namespace attn;
 
 constexpr int kThreads = 384;
-constexpr int kSlots = 5;  // ring of key / value tiles
+// Registers per thread at launch; the softmax warpgroups take 160, the third one 88: 2 x 160 + 88 = 3 x 136.
+constexpr int kRegs = 136;
+constexpr int kSlots = 4;  // ring of key / value tiles
 constexpr uint64_t kWaitLimitNs = 200ull * 1000 * 1000;
 constexpr unsigned int kStatusAttnTimeout = 0x8u;
 constexpr float kRaise = 8.f;  // log2 of the growth that raises a row's maximum
@@ -185,7 +187,7 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
 }
 
 template <bool kBF, int D>
-__global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_constant__ TcArgs a) {
+__global__ void __maxnreg__(kRegs) attn_prefix_kernel(const __grid_constant__ TcArgs a) {
   using SH = Shape<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -271,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
 
   if (warp < 8) {
     // ------------------------------------------------------------------ softmax ----
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
     [&] {
       const int h = warp >> 2;
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -416,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
       }
     }();
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");  // one instruction for the four warps
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");  // one instruction for the four warps
   }
   if (warp == 8 || warp == 9) {
     // ------------------------------------------------------------------- loads ----
