@@ -36,7 +36,7 @@ __device__ __forceinline__ float reciprocal(float x) {  // good to the last bit 
 
 // One warp per token.  Lane l holds experts [l V, l V + V), V = ceil(E / 32) <= VT, so that the
 // lowest lane and the lowest register of the equal keys is the lowest expert.  kVec: V == VT and rows
-// allow 16-byte loads.  Bound by instructions (about 600 per token at 256 experts, 8 of them chosen);
+// allow 16-byte loads.  Bound by instructions;
 // every maximum over the warp is one redux on the keys as ordered integers.
 template <int DT, int VT, bool kVec>
 __global__ void __launch_bounds__(128) route_kernel(const RouteProblem p) {
@@ -71,12 +71,13 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteProblem p) {
   }
 
   // scores; an expert whose logit is -inf is out
+  float top = -INFINITY, inv = 0.f;
+  const auto score_of = [&](float v) { return p.sigmoid ? reciprocal(1.f + expf(-v)) : expf(v - top) * inv; };
   float score[VT];
   if (p.sigmoid) {
 #pragma unroll
     for (int i = 0; i < VT; ++i) score[i] = reciprocal(1.f + expf(-x[i]));
   } else {
-    float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < VT; ++i) top = fmaxf(top, x[i]);
     top = from_ordered(__reduce_max_sync(kAll, ordered(top)));
@@ -88,7 +89,7 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteProblem p) {
     }
 #pragma unroll
     for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
-    const float inv = __fdiv_rn(1.f, sum);
+    inv = __fdiv_rn(1.f, sum);
 #pragma unroll
     for (int i = 0; i < VT; ++i) score[i] *= inv;
   }
@@ -169,37 +170,78 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteProblem p) {
     chosen = lane;
     weight = __int_as_float(0x7fffffff);
   } else {
-    uint32_t first = 0u;
+    if constexpr (VT <= 8) {
+      // Each lane sorts its keys once (a rank by comparing pairs, then a sorting network), so that a
+      // place costs the maximum over the lanes' first keys and one shift: 290 instructions for 8 of 256
+      // experts, 520 when every place searches the lane's keys.
+      uint32_t order = 0u;  // the lane's registers by falling key, four bits each
+      int rank[VT];
 #pragma unroll
-    for (int i = 0; i < VT; ++i) first = max(first, key[i]);
-    for (int j = 0; j < p.k; ++j) {
-      const uint32_t best = __reduce_max_sync(kAll, first);
-      if (!best) break;  // no expert left: the other places stay empty
-      const int owner = __ffs(__ballot_sync(kAll, first == best)) - 1;
-      int at = 0;
-      float s = 0.f;
-      if (lane == owner) {  // its first key of that value goes
-        bool found = false;
-        first = 0u;
+      for (int i = 0; i < VT; ++i) rank[i] = 0;
 #pragma unroll
-        for (int i = 0; i < VT; ++i) {
-          const bool hit = !found && key[i] == best;
-          if (hit) {
-            at = e0 + i;
-            s = score[i];
-            key[i] = 0u;
-          }
-          found |= hit;
-          first = max(first, key[i]);
+      for (int i = 0; i < VT; ++i)
+#pragma unroll
+        for (int j = i + 1; j < VT; ++j) {
+          const bool later = key[j] > key[i];  // equal keys: the lower register first
+          rank[i] += later;
+          rank[j] += !later;
         }
+#pragma unroll
+      for (int i = 0; i < VT; ++i) order |= static_cast<uint32_t>(i) << (4 * rank[i]);
+#pragma unroll
+      for (int n = 1; n < VT; n <<= 1)  // odd-even merge sort (Batcher), falling
+#pragma unroll
+        for (int d = n; d; d >>= 1)
+#pragma unroll
+          for (int i = d % n; i + d < VT; i += 2 * d)
+#pragma unroll
+            for (int j = 0; j < d; ++j)
+              if (i + j + d < VT && (i + j) / (2 * n) == (i + j + d) / (2 * n)) {
+                const uint32_t hi = max(key[i + j], key[i + j + d]);
+                key[i + j + d] = min(key[i + j], key[i + j + d]);
+                key[i + j] = hi;
+              }
+      for (int j = 0; j < p.k; ++j) {
+        const uint32_t best = __reduce_max_sync(kAll, key[0]);
+        if (!best) break;  // no expert left: the other places stay empty
+        const int owner = __ffs(__ballot_sync(kAll, key[0] == best)) - 1;
+        const int at = __shfl_sync(kAll, e0 + static_cast<int>(order & 15u), owner);
+        if (lane == owner) {
+          order >>= 4;
+#pragma unroll
+          for (int i = 0; i + 1 < VT; ++i) key[i] = key[i + 1];
+          key[VT - 1] = 0u;
+        }
+        if (lane == j) chosen = at;
       }
-      at = __shfl_sync(kAll, at, owner);
-      s = __shfl_sync(kAll, s, owner);
-      if (lane == j) {
-        chosen = at;
-        weight = s;
+    } else {
+      uint32_t first = 0u;
+#pragma unroll
+      for (int i = 0; i < VT; ++i) first = max(first, key[i]);
+      for (int j = 0; j < p.k; ++j) {
+        const uint32_t best = __reduce_max_sync(kAll, first);
+        if (!best) break;
+        const int owner = __ffs(__ballot_sync(kAll, first == best)) - 1;
+        int at = 0;
+        if (lane == owner) {  // its first key of that value goes
+          bool found = false;
+          first = 0u;
+#pragma unroll
+          for (int i = 0; i < VT; ++i) {
+            const bool hit = !found && key[i] == best;
+            if (hit) {
+              at = e0 + i;
+              key[i] = 0u;
+            }
+            found |= hit;
+            first = max(first, key[i]);
+          }
+        }
+        at = __shfl_sync(kAll, at, owner);
+        if (lane == j) chosen = at;
       }
     }
+    if (chosen >= 0) weight = score_of(load_logit<DT>(p.logits, row + chosen));
     if (p.renormalize) {
       float sum = weight;
 #pragma unroll
