@@ -8,6 +8,7 @@ import math
 
 import torch
 
+from . import _binding
 from ._binding import (AWQ_OK, DTYPE_BF16, DTYPE_F16, DTYPE_F32, AwqError, PagedKV, _cuda_index, _need, last_error,
                        load_library)
 
@@ -18,24 +19,52 @@ _GRANULE = 1 << 20
 _scratch = {}
 
 
+# The calls below run once per layer and token, so they are written for few interpreter steps: one
+# expression tests what a correct call satisfies, and only if it is false are the arguments looked at
+# one by one for the message (17 and 24 us of host time for awq_rope_append and awq_attention_shared;
+# 19 and 28 with a helper call per tensor).
+_half_dtypes = (torch.float16, torch.bfloat16)
+_i32, _f32 = torch.int32, torch.float32
+
+
+def _current(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+# the same without building a Stream object (1.1 us), where this PyTorch has it
+_current = getattr(torch._C, "_cuda_getCurrentRawStream", _current)
+
+
 def _handle(stream, device):
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return _current(device)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+def _library():
+    return _binding._lib or load_library()
+
+
 def scratch(device, handle, nbytes):
-    """A uint8 workspace of at least ``nbytes`` that this module's calls on (device, stream) share:
+    """(address, bytes, tensor) of a workspace of at least ``nbytes`` that this module's calls on (device,
+    stream) share:
     calls on one stream never overlap, and no call reads what an earlier one left.  It grows by
     allocation (at least doubling) and a smaller one is kept, since a captured CUDA graph may hold its
     address; make a stream's largest call once before capturing."""
     kept = _scratch.get((device, handle))
     if kept is None:
         kept = _scratch[(device, handle)] = []
-    if not kept or kept[-1].numel() < nbytes:
-        size = max(nbytes, 2 * kept[-1].numel() if kept else 0)
-        kept.append(torch.empty(((size + _GRANULE - 1) // _GRANULE * _GRANULE,), dtype=torch.uint8, device=device))
+    if not kept or kept[-1][1] < nbytes:
+        size = (max(nbytes, 2 * kept[-1][1] if kept else 0) + _GRANULE - 1) // _GRANULE * _GRANULE
+        t = torch.empty((size,), dtype=torch.uint8, device=device)
+        kept.append((t.data_ptr(), size, t))
     return kept[-1]
+
+
+def _given(workspace, device, name):
+    if workspace.dtype is not torch.uint8 or workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {name}'s device")
+    return workspace.data_ptr(), workspace.numel(), workspace
 
 
 def _half(t, name):
@@ -58,18 +87,20 @@ def _heads(t, name, dt, shape, device):
 
 
 def _cache(k_cache, v_cache, dt, heads, dim, device):
-    if k_cache.dim() != 4:
-        raise ValueError("k_cache must be [pages, page_size, heads, head_dim]")
-    shape = k_cache.shape
-    if (heads is not None and shape[2] != heads) or shape[3] != dim:
-        raise ValueError(f"k_cache must have {heads if heads is not None else 'some'} heads of {dim} elements, "
-                         f"got shape {tuple(shape)}")
-    _heads(k_cache, "k_cache", dt, shape, device)
-    _heads(v_cache, "v_cache", dt, shape, device)
-    s = k_cache.stride()
-    if v_cache.stride() != s:
-        raise ValueError("k_cache and v_cache must have the same strides")
-    return PagedKV(k_cache.data_ptr(), v_cache.data_ptr(), shape[0], shape[1], shape[2], shape[3], s[0], s[1], s[2])
+    shape, s = k_cache.shape, k_cache.stride()
+    if not (len(shape) == 4 and (heads is None or shape[2] == heads) and shape[3] == dim and k_cache.dtype is dt and
+            v_cache.dtype is dt and v_cache.shape == shape and v_cache.stride() == s and k_cache.get_device() == device and
+            v_cache.get_device() == device and s[3] == 1):
+        if len(shape) != 4:
+            raise ValueError("k_cache must be [pages, page_size, heads, head_dim]")
+        if (heads is not None and shape[2] != heads) or shape[3] != dim:
+            raise ValueError(f"k_cache must have {heads if heads is not None else 'some'} heads of {dim} elements, "
+                             f"got shape {tuple(shape)}")
+        _heads(k_cache, "k_cache", dt, shape, device)
+        _heads(v_cache, "v_cache", dt, shape, device)
+        if v_cache.stride() != s:
+            raise ValueError("k_cache and v_cache must have the same strides")
+    return PagedKV(k_cache.data_ptr(), v_cache.data_ptr(), *shape, s[0], s[1], s[2])
 
 
 def _ok(status):
@@ -100,23 +131,27 @@ def awq_rope_table(max_position, rotary_dim, base=10000.0, scaling="none", facto
 
 
 def _rope_inputs(q, k, positions, table):
-    dt, dev = _half(q, "q"), _cuda_index(q, "q")
-    if q.dim() != 3 or k.dim() != 3:
-        raise ValueError("q and k must be [tokens, heads, head_dim]")
-    T, Hq, D = q.shape
-    Hkv = k.shape[1]
-    _heads(q, "q", dt, (T, Hq, D), dev)
-    _heads(k, "k", dt, (T, Hkv, D), dev)
-    _need(positions, "positions", torch.int32, (T,), dev)
-    if table.dim() != 2:
-        raise ValueError("table must be [max_position, rotary_dim]")
-    _need(table, "table", torch.float32, table.shape, dev)
-    return dt, dev, T, Hq, Hkv, D
+    dt, dev = q.dtype, q.get_device()
+    qs, ks, ts = q.shape, k.shape, table.shape
+    if not (dt in _half_dtypes and dev >= 0 and len(qs) == 3 and len(ks) == 3 and len(ts) == 2 and k.dtype is dt and
+            ks[0] == qs[0] and ks[2] == qs[2] and k.get_device() == dev and positions.dtype is _i32 and
+            positions.shape == qs[:1] and positions.is_contiguous() and positions.get_device() == dev and
+            table.dtype is _f32 and table.is_contiguous() and table.get_device() == dev and
+            (qs[2] <= 1 or (q.stride(2) == 1 and k.stride(2) == 1))):
+        _half(q, "q")
+        dev = _cuda_index(q, "q")
+        if len(qs) != 3 or len(ks) != 3:
+            raise ValueError("q and k must be [tokens, heads, head_dim]")
+        if len(ts) != 2:
+            raise ValueError("table must be [max_position, rotary_dim]")
+        _heads(q, "q", dt, qs, dev)
+        _heads(k, "k", dt, (qs[0], ks[1], qs[2]), dev)
+        _need(positions, "positions", _i32, (qs[0],), dev)
+        _need(table, "table", _f32, ts, dev)
+    return dt, dev, qs, ks[1], ts
 
 
 def _dense_or_same(out, t, name, dt, dev):
-    if out is None:
-        return torch.empty(t.shape, dtype=dt, device=t.device)
     if out.data_ptr() == t.data_ptr() and out.stride() == t.stride() and out.shape == t.shape and out.dtype is dt:
         return out  # in place
     _need(out, name, dt, t.shape, dev)
@@ -128,13 +163,14 @@ def awq_rope(q, k, positions, table, interleaved=False, q_out=None, k_out=None, 
     or bf16; heads contiguous, other strides free) by the angles of positions int32 [T] and copies the
     rest.  Pairs are (i, i + rotary_dim / 2), or (2 i, 2 i + 1) with interleaved=True.  Returns
     (q_out, k_out), dense, or written in place where q_out is q (k_out is k)."""
-    dt, dev, T, Hq, Hkv, D = _rope_inputs(q, k, positions, table)
-    q_out = _dense_or_same(q_out, q, "q_out", dt, dev)
-    k_out = _dense_or_same(k_out, k, "k_out", dt, dev)
-    qs, ks = q.stride(), k.stride()
-    _ok(load_library().awq_rope(q.data_ptr(), k.data_ptr(), positions.data_ptr(), table.data_ptr(), T, Hq, Hkv, D,
-                                table.shape[1], table.shape[0], qs[0], qs[1], ks[0], ks[1], q_out.data_ptr(),
-                                k_out.data_ptr(), 1 if interleaved else 0, _DTYPES[dt], _handle(stream, dev)))
+    dt, dev, (T, Hq, D), Hkv, (last, rot) = _rope_inputs(q, k, positions, table)
+    q_out = torch.empty((T, Hq, D), dtype=dt, device=dev) if q_out is None else _dense_or_same(q_out, q, "q_out", dt, dev)
+    k_out = torch.empty((T, Hkv, D), dtype=dt, device=dev) if k_out is None else _dense_or_same(k_out, k, "k_out", dt, dev)
+    st = _library().awq_rope(q.data_ptr(), k.data_ptr(), positions.data_ptr(), table.data_ptr(), T, Hq, Hkv, D, rot, last,
+                             q.stride(0), q.stride(1), k.stride(0), k.stride(1), q_out.data_ptr(), k_out.data_ptr(),
+                             1 if interleaved else 0, _DTYPES[dt], _handle(stream, dev))
+    if st != AWQ_OK:
+        raise AwqError(st, last_error())
     return q_out, k_out
 
 
@@ -143,16 +179,19 @@ def awq_rope_append(q, k, v, positions, table, k_cache, v_cache, slots, interlea
     and v_cache [pages, page_size, Hkv, D], any equal strides with contiguous heads) at slots int32
     [T]: slot s is token s % page_size of page s // page_size, and a slot outside the cache (-1) keeps
     nothing.  Returns the rotated queries."""
-    dt, dev, T, Hq, Hkv, D = _rope_inputs(q, k, positions, table)
-    _heads(v, "v", dt, (T, Hkv, D), dev)
-    _need(slots, "slots", torch.int32, (T,), dev)
+    dt, dev, (T, Hq, D), Hkv, (last, rot) = _rope_inputs(q, k, positions, table)
+    if not (v.dtype is dt and v.shape == k.shape and v.get_device() == dev and (D <= 1 or v.stride(2) == 1) and
+            slots.dtype is _i32 and slots.shape == (T,) and slots.is_contiguous() and slots.get_device() == dev):
+        _heads(v, "v", dt, (T, Hkv, D), dev)
+        _need(slots, "slots", _i32, (T,), dev)
     cache = _cache(k_cache, v_cache, dt, Hkv, D, dev)
-    q_out = _dense_or_same(q_out, q, "q_out", dt, dev)
-    qs, ks, vs = q.stride(), k.stride(), v.stride()
-    _ok(load_library().awq_rope_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), positions.data_ptr(), table.data_ptr(), T,
-                                       Hq, Hkv, D, table.shape[1], table.shape[0], qs[0], qs[1], ks[0], ks[1], vs[0], vs[1],
-                                       q_out.data_ptr(), ctypes.byref(cache), slots.data_ptr(), 1 if interleaved else 0,
-                                       _DTYPES[dt], _handle(stream, dev)))
+    q_out = torch.empty((T, Hq, D), dtype=dt, device=dev) if q_out is None else _dense_or_same(q_out, q, "q_out", dt, dev)
+    st = _library().awq_rope_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), positions.data_ptr(), table.data_ptr(), T, Hq,
+                                    Hkv, D, rot, last, q.stride(0), q.stride(1), k.stride(0), k.stride(1), v.stride(0),
+                                    v.stride(1), q_out.data_ptr(), cache, slots.data_ptr(), 1 if interleaved else 0,
+                                    _DTYPES[dt], _handle(stream, dev))
+    if st != AWQ_OK:
+        raise AwqError(st, last_error())
     return q_out
 
 
@@ -167,42 +206,56 @@ def awq_attention_shared(q, k_cache, v_cache, prefix_pages, prefix_len, pages, l
     default W * page_size) are host integers.  scale defaults to 1 / sqrt(D).  Returns q's shape, dense.
     workspace: a uint8 device tensor of awq_attention_shared_workspace_size bytes (default: this
     module's for the stream)."""
-    lib = load_library()
-    dt, dev = _half(q, "q"), _cuda_index(q, "q")
-    if q.dim() == 3:
-        B, Hq, D = q.shape
-        n, sb, sn, sh = 1, q.stride(0), 0, q.stride(1)
-    elif q.dim() == 4:
-        B, n, Hq, D = q.shape
-        sb, sn, sh = q.stride(0), q.stride(1), q.stride(2)
+    dt, dev, qs = q.dtype, q.get_device(), q.shape
+    if len(qs) == 4:
+        B, n, Hq, D = qs
+        sb, sn, sh, one = q.stride()
+    elif len(qs) == 3:
+        B, Hq, D = qs
+        n, sn = 1, 0
+        sb, sh, one = q.stride()
     else:
         raise ValueError("q must be [B, n, heads, head_dim] or [B, heads, head_dim]")
-    _heads(q, "q", dt, q.shape, dev)
+    ps = pages.shape
+    if not (dt in _half_dtypes and dev >= 0 and one == 1 and len(ps) == 2 and ps[0] == B and pages.dtype is _i32 and
+            pages.get_device() == dev and (ps[1] <= 1 or pages.stride(1) == 1) and prefix_pages.dtype is _i32 and
+            prefix_pages.dim() == 1 and prefix_pages.is_contiguous() and prefix_pages.get_device() == dev and
+            lens.dtype is _i32 and lens.shape == (B,) and lens.is_contiguous() and lens.get_device() == dev):
+        _half(q, "q")
+        dev = _cuda_index(q, "q")
+        _heads(q, "q", dt, qs, dev)
+        if len(ps) != 2 or pages.dtype is not _i32 or ps[0] != B:
+            raise ValueError(f"pages must be an int32 [{B}, W] table, got {pages.dtype} {tuple(ps)}")
+        if B:
+            _heads(pages, "pages", _i32, ps, dev)
+        if prefix_pages.dim() != 1:
+            raise ValueError("prefix_pages must have one dimension")
+        _need(prefix_pages, "prefix_pages", _i32, prefix_pages.shape, dev)
+        _need(lens, "lens", _i32, (B,), dev)
     cache = _cache(k_cache, v_cache, dt, None, D, dev)
-    page = cache.page_size
-    if prefix_pages.dim() != 1 or (page > 0 and prefix_pages.shape[0] * page < prefix_len):
+    page, heads = k_cache.shape[1:3]
+    if page > 0 and prefix_pages.shape[0] * page < prefix_len:
         raise ValueError(f"prefix_pages must hold the pages of {prefix_len} tokens")
-    _need(prefix_pages, "prefix_pages", torch.int32, prefix_pages.shape, dev)
-    if pages.dim() != 2 or pages.dtype is not torch.int32 or pages.shape[0] != B:
-        raise ValueError(f"pages must be an int32 [{B}, W] table, got {pages.dtype} {tuple(pages.shape)}")
-    _heads(pages, "pages", torch.int32, pages.shape, dev)
-    _need(lens, "lens", torch.int32, (B,), dev)
     if max_len is None:
-        max_len = pages.shape[1] * page
+        max_len = ps[1] * page
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = torch.empty(q.shape, dtype=dt, device=q.device)
+        out = torch.empty(qs, dtype=dt, device=dev)
     else:
-        _need(out, "out", dt, q.shape, dev)
-    handle = _handle(stream, dev)
+        _need(out, "out", dt, qs, dev)
+    handle, lib = _handle(stream, dev), _library()
+    need = ctypes.c_size_t(0)
     if workspace is None:
-        workspace = scratch(dev, handle, awq_attention_shared_workspace_size(B, n, Hq, cache.heads, D, prefix_len, max_len))
-    elif workspace.dtype is not torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
-    _ok(lib.awq_attention_shared(q.data_ptr(), B, n, Hq, sb, sn, sh, ctypes.byref(cache), prefix_pages.data_ptr(), prefix_len,
-                                 pages.data_ptr(), pages.shape[1], pages.stride(0), lens.data_ptr(), max_len, scale,
-                                 out.data_ptr(), _DTYPES[dt], workspace.data_ptr(), workspace.numel(), handle))
+        _ok(lib.awq_attention_shared_workspace_size(B, n, Hq, heads, D, prefix_len, max_len, need))
+        ws = scratch(dev, handle, need.value)
+    else:
+        ws = _given(workspace, dev, "q")
+    st = lib.awq_attention_shared(q.data_ptr(), B, n, Hq, sb, sn, sh, cache, prefix_pages.data_ptr(), prefix_len,
+                                  pages.data_ptr(), ps[1], pages.stride(0), lens.data_ptr(), max_len, scale, out.data_ptr(),
+                                  _DTYPES[dt], ws[0], ws[1], handle)
+    if st != AWQ_OK:
+        raise AwqError(st, last_error())
     return out
 
 
@@ -220,28 +273,32 @@ def awq_moe_route(logits, topk, scoring="softmax", bias=None, groups=1, topk_gro
     topk_groups best of ``groups`` groups (a group's score: the sum of its group_best best keys), the
     scores divided by their sum if renormalize, times scale.  Equal keys go to the lower index.  Returns
     (weights fp32 [T, topk], experts int32 [T, topk]), or fills ``out``, a tuple of those two."""
-    if logits.dtype not in _DTYPES:
-        raise TypeError(f"logits must be float16, bfloat16 or float32, got {logits.dtype}")
-    if logits.dim() != 2:
-        raise ValueError("logits must be [tokens, experts]")
-    if scoring not in ("softmax", "sigmoid"):
-        raise ValueError(f"scoring must be 'softmax' or 'sigmoid', got {scoring!r}")
-    dev = _cuda_index(logits, "logits")
-    T, E = logits.shape
-    _heads(logits, "logits", logits.dtype, (T, E), dev)
+    dt, dev, shape = logits.dtype, logits.get_device(), logits.shape
+    if not (dt in _DTYPES and len(shape) == 2 and dev >= 0 and (logits.stride(1) == 1 or shape[1] <= 1) and
+            scoring in ("softmax", "sigmoid")):
+        if dt not in _DTYPES:
+            raise TypeError(f"logits must be float16, bfloat16 or float32, got {dt}")
+        if len(shape) != 2:
+            raise ValueError("logits must be [tokens, experts]")
+        if scoring not in ("softmax", "sigmoid"):
+            raise ValueError(f"scoring must be 'softmax' or 'sigmoid', got {scoring!r}")
+        _heads(logits, "logits", dt, shape, _cuda_index(logits, "logits"))
+    T, E = shape
     if bias is not None:
-        _need(bias, "bias", torch.float32, (E,), dev)
+        _need(bias, "bias", _f32, (E,), dev)
     if out is None:
-        weights = torch.empty((T, topk), dtype=torch.float32, device=logits.device)
-        experts = torch.empty((T, topk), dtype=torch.int32, device=logits.device)
+        weights = torch.empty((T, topk), dtype=_f32, device=dev)
+        experts = torch.empty((T, topk), dtype=_i32, device=dev)
     else:
         weights, experts = out
-        _need(weights, "weights", torch.float32, (T, topk), dev)
-        _need(experts, "experts", torch.int32, (T, topk), dev)
-    _ok(load_library().awq_moe_route(logits.data_ptr(), T, E, logits.stride(0), _DTYPES[logits.dtype], topk,
-                                     1 if scoring == "sigmoid" else 0, None if bias is None else bias.data_ptr(), groups,
-                                     topk_groups, group_best, 1 if renormalize else 0, scale, weights.data_ptr(),
-                                     experts.data_ptr(), _handle(stream, dev)))
+        _need(weights, "weights", _f32, (T, topk), dev)
+        _need(experts, "experts", _i32, (T, topk), dev)
+    st = _library().awq_moe_route(logits.data_ptr(), T, E, logits.stride(0), _DTYPES[dt], topk,
+                                  1 if scoring == "sigmoid" else 0, None if bias is None else bias.data_ptr(), groups,
+                                  topk_groups, group_best, 1 if renormalize else 0, scale, weights.data_ptr(),
+                                  experts.data_ptr(), _handle(stream, dev))
+    if st != AWQ_OK:
+        raise AwqError(st, last_error())
     return weights, experts
 
 
@@ -252,30 +309,37 @@ def awq_moe_dispatch(x, experts, num_experts, out=None, stream=None, workspace=N
     ``out``, a tuple of those three.  A place whose id lies outside [0, num_experts) gets row -1; the
     rows of routed behind offsets[-1] are zero.  workspace: a uint8 device tensor of
     awq_moe_dispatch_workspace_size bytes (default: this module's for the stream)."""
-    lib = load_library()
-    dt, dev = _half(x, "x"), _cuda_index(x, "x")
-    if x.dim() != 2 or experts.dim() != 2:
-        raise ValueError("x must be [tokens, width], experts [tokens, k]")
-    T, W = x.shape
-    k = experts.shape[1]
-    _heads(x, "x", dt, (T, W), dev)
-    _need(experts, "experts", torch.int32, (T, k), dev)
+    dt, dev, xs, es = x.dtype, x.get_device(), x.shape, experts.shape
+    if not (dt in _half_dtypes and dev >= 0 and len(xs) == 2 and len(es) == 2 and es[0] == xs[0] and
+            (x.stride(1) == 1 or xs[1] <= 1) and experts.dtype is _i32 and experts.is_contiguous() and
+            experts.get_device() == dev):
+        _half(x, "x")
+        if len(xs) != 2 or len(es) != 2:
+            raise ValueError("x must be [tokens, width], experts [tokens, k]")
+        dev = _cuda_index(x, "x")
+        _heads(x, "x", dt, xs, dev)
+        _need(experts, "experts", _i32, (xs[0], es[1]), dev)
+    (T, W), k = xs, es[1]
     if out is None:
-        routed = torch.empty((T * k, W), dtype=dt, device=x.device)
-        offsets = torch.empty((num_experts + 1,), dtype=torch.int32, device=x.device)
-        rows = torch.empty((T, k), dtype=torch.int32, device=x.device)
+        routed = torch.empty((T * k, W), dtype=dt, device=dev)
+        offsets = torch.empty((num_experts + 1,), dtype=_i32, device=dev)
+        rows = torch.empty((T, k), dtype=_i32, device=dev)
     else:
         routed, offsets, rows = out
         _need(routed, "routed", dt, (T * k, W), dev)
-        _need(offsets, "offsets", torch.int32, (num_experts + 1,), dev)
-        _need(rows, "rows", torch.int32, (T, k), dev)
-    handle = _handle(stream, dev)
+        _need(offsets, "offsets", _i32, (num_experts + 1,), dev)
+        _need(rows, "rows", _i32, (T, k), dev)
+    handle, lib = _handle(stream, dev), _library()
     if workspace is None:
-        workspace = scratch(dev, handle, awq_moe_dispatch_workspace_size(T, k, num_experts))
-    elif workspace.dtype is not torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous uint8 tensor on x's device")
-    _ok(lib.awq_moe_dispatch(x.data_ptr(), T, W, x.stride(0), experts.data_ptr(), k, num_experts, routed.data_ptr(),
-                             offsets.data_ptr(), rows.data_ptr(), workspace.data_ptr(), workspace.numel(), handle))
+        need = ctypes.c_size_t(0)
+        _ok(lib.awq_moe_dispatch_workspace_size(T, k, num_experts, need))
+        ws = scratch(dev, handle, need.value)
+    else:
+        ws = _given(workspace, dev, "x")
+    st = lib.awq_moe_dispatch(x.data_ptr(), T, W, x.stride(0), experts.data_ptr(), k, num_experts, routed.data_ptr(),
+                              offsets.data_ptr(), rows.data_ptr(), ws[0], ws[1], handle)
+    if st != AWQ_OK:
+        raise AwqError(st, last_error())
     return routed, offsets, rows
 
 
@@ -290,21 +354,27 @@ def awq_moe_combine(y, weights, rows, base=None, out=None, stream=None):
     """out[t] = base[t] + sum_j weights[t, j] * y[rows[t, j]], in fp32 in the order of the places: y [R,
     W] fp16 or bf16, weights fp32 [T, k], rows int32 [T, k] (outside [0, R): left out), base [T, W] or
     None.  Returns [T, W]; out may be base."""
-    dt, dev = _half(y, "y"), _cuda_index(y, "y")
-    if y.dim() != 2 or rows.dim() != 2:
-        raise ValueError("y must be [rows, width], rows [tokens, k]")
-    R, W = y.shape
-    T, k = rows.shape
-    _need(y, "y", dt, (R, W), dev)
-    _need(weights, "weights", torch.float32, (T, k), dev)
-    _need(rows, "rows", torch.int32, (T, k), dev)
+    dt, dev, ys, rs = y.dtype, y.get_device(), y.shape, rows.shape
+    if not (dt in _half_dtypes and dev >= 0 and len(ys) == 2 and len(rs) == 2 and y.is_contiguous() and rows.dtype is _i32 and
+            rows.is_contiguous() and rows.get_device() == dev and weights.dtype is _f32 and weights.shape == rs and
+            weights.is_contiguous() and weights.get_device() == dev):
+        _half(y, "y")
+        if len(ys) != 2 or len(rs) != 2:
+            raise ValueError("y must be [rows, width], rows [tokens, k]")
+        dev = _cuda_index(y, "y")
+        _need(y, "y", dt, ys, dev)
+        _need(weights, "weights", _f32, rs, dev)
+        _need(rows, "rows", _i32, rs, dev)
+    (R, W), (T, k) = ys, rs
     if base is not None:
         _need(base, "base", dt, (T, W), dev)
     if out is None:
-        out = torch.empty((T, W), dtype=dt, device=y.device)
+        out = torch.empty((T, W), dtype=dt, device=dev)
     else:
         _need(out, "out", dt, (T, W), dev)
-    _ok(load_library().awq_moe_combine(y.data_ptr(), R, W, weights.data_ptr(), rows.data_ptr(), T, k,
-                                       None if base is None else base.data_ptr(), out.data_ptr(), _DTYPES[dt],
-                                       _handle(stream, dev)))
+    st = _library().awq_moe_combine(y.data_ptr(), R, W, weights.data_ptr(), rows.data_ptr(), T, k,
+                                    None if base is None else base.data_ptr(), out.data_ptr(), _DTYPES[dt],
+                                    _handle(stream, dev))
+    if st != AWQ_OK:
+        raise AwqError(st, last_error())
     return out

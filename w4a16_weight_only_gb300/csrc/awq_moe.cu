@@ -172,8 +172,8 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteProblem p) {
   } else {
     if constexpr (VT <= 8) {
       // Each lane sorts its keys once (a rank by comparing pairs, then a sorting network), so that a
-      // place costs the maximum over the lanes' first keys and one shift: 290 instructions for 8 of 256
-      // experts, 520 when every place searches the lane's keys.
+      // place costs the maximum over the lanes' first keys and one shift (16381 tokens, 8 of 256 experts
+      // in 8 groups: 18.5 us; 23.1 us when every place searches the lane's keys).
       uint32_t order = 0u;  // the lane's registers by falling key, four bits each
       int rank[VT];
 #pragma unroll
