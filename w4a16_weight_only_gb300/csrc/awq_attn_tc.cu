@@ -540,6 +540,12 @@ __global__ void __maxnreg__(kRegs) attn_prefix_kernel(const __grid_constant__ Tc
         }
         __syncwarp();
       };
+      // Three waits at the price of one (some 120 cycles each, even if they pass at once; issuing an MMA
+      // takes as long as executing one, so they are lost to the tensor core).
+      const auto wait3 = [&](uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, uint64_t* c, uint32_t pc) {
+        const bool x = mbar_try_wait(a, pa), y = mbar_try_wait(b, pb), z = mbar_try_wait(c, pc);
+        return __all_sync(0xffffffffu, x && y && z) || (wait(a, pa) && wait(b, pb) && wait(c, pc));
+      };
       for (int at = s_begin; at < s_end;) {
         const Segment sg = segment(at);
         at += sg.steps;
@@ -555,19 +561,15 @@ __global__ void __maxnreg__(kRegs) attn_prefix_kernel(const __grid_constant__ Tc
           const bool more = j + 1 < sg.steps;
           const uint32_t v = slot, v_phase = phase;
           next();
-          const uint32_t k = slot, k_phase = phase;
+          const uint32_t k = more ? slot : v, k_phase = more ? phase : v_phase;
           if (more) next();
-          if (!wait(&full[v], v_phase) || !wait(&p_half[0], done0 & 1u)) return;
+          if (!wait3(&full[v], v_phase, &full[k], k_phase, &p_half[0], done0 & 1u)) return;
           tc_fence_after();
           pv(0, v, 0, j > 0, !two);
           if (!wait(&p_full[0], done0++ & 1u)) return;
           tc_fence_after();
           pv(0, v, 1, true, !two);
-          if (more) {
-            if (!wait(&full[k], k_phase)) return;
-            tc_fence_after();
-            qk(0, k, !two);
-          }
+          if (more) qk(0, k, !two);
           if (two) {
             if (!wait(&p_half[1], done1 & 1u)) return;
             tc_fence_after();
