@@ -409,44 +409,64 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
   }
   const int parts = first + own, skip = pl.prefix_parts - first;
   const float2* ml = a.part_ml + r * pl.parts;
-  const float* src = a.part_o + r * pl.parts * D;
-  constexpr int N = D / 32, BATCH = 8;
-  float acc[N] = {}, l = 0.f, all = -INFINITY;
+  constexpr int V = D % 128 == 0 ? 4 : D % 64 == 0 ? 2 : 1, N = D / 32 / V, BATCH = 8;  // elements of a load, loads of a row
+  const float* src = a.part_o + r * pl.parts * D + lane * V;
+  float acc[N][V] = {}, l = 0.f, all = -INFINITY;
   for (int s0 = 0; s0 < parts; s0 += 32) {
-    const int s = s0 + lane;
+    const int s = s0 + lane, n = min(32, parts - s0);
     const float2 mine = s < parts ? ml[s < first ? s : s + skip] : make_float2(-INFINITY, 0.f);
+    float v[BATCH][N][V];
+    const auto load = [&](int i0) {  // a batch of parts; past the last one it is read again, with weight 0
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const int t = s0 + min(i0 + i, n - 1);
+        const float* from = src + static_cast<int64_t>(t < first ? t : t + skip) * D;
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+          if constexpr (V == 4) *reinterpret_cast<float4*>(v[i][c]) = *reinterpret_cast<const float4*>(from + c * 128);
+          else if constexpr (V == 2) *reinterpret_cast<float2*>(v[i][c]) = *reinterpret_cast<const float2*>(from + c * 64);
+          else v[i][c][0] = from[c * 32];
+        }
+      }
+    };
+    load(0);
     float best = mine.x;
 #pragma unroll
     for (int d = 16; d; d >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, d));
     const float now = fmaxf(all, best), ref = now == -INFINITY ? 0.f : now;
     const float shrink = exp2_approx(all - ref), f = exp2_approx(mine.x - ref);  // 0 past the last part
     all = now;
-    l = l * shrink + mine.y * f;  // this lane's share
+    l = l * shrink + mine.y * f;  // this lane's parts
 #pragma unroll
-    for (int c = 0; c < N; ++c) acc[c] *= shrink;
-    const int n = min(32, parts - s0);
+    for (int c = 0; c < N; ++c)
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[c][e] *= shrink;
     for (int i0 = 0; i0 < n; i0 += BATCH) {
-      float v[BATCH][N];
+      if (i0) load(i0);
 #pragma unroll
       for (int i = 0; i < BATCH; ++i) {
-        const int t = s0 + min(i0 + i, n - 1);
-        const float* from = src + static_cast<int64_t>(t < first ? t : t + skip) * D + lane;
+        const float g = __shfl_sync(0xffffffffu, f, i0 + i);
+        if (i0 + i < n) {
 #pragma unroll
-        for (int c = 0; c < N; ++c) v[i][c] = from[c * 32];
-      }
+          for (int c = 0; c < N; ++c)
 #pragma unroll
-      for (int i = 0; i < BATCH; ++i) {
-        const float g = i0 + i < n ? __shfl_sync(0xffffffffu, f, i0 + i) : 0.f;
-#pragma unroll
-        for (int c = 0; c < N; ++c) acc[c] = i0 + i < n ? acc[c] + v[i][c] * g : acc[c];
+            for (int e = 0; e < V; ++e) acc[c][e] += v[i][c][e] * g;
+        }
       }
     }
   }
 #pragma unroll
   for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
   const float inv = l > 0.f ? 1.f / l : l;  // a row that sees no key is zero; NaN stays
+  uint16_t* out = p.out + r * D + lane * V;
 #pragma unroll
-  for (int c = 0; c < N; ++c) p.out[r * D + c * 32 + lane] = float_to_elem<kBF>(acc[c] * inv);
+  for (int c = 0; c < N; ++c) {
+    if constexpr (V == 4)
+      *reinterpret_cast<uint2*>(out + c * 128) =
+          make_uint2(pack2<kBF>(acc[c][0] * inv, acc[c][1] * inv), pack2<kBF>(acc[c][2] * inv, acc[c][3] * inv));
+    else if constexpr (V == 2) *reinterpret_cast<uint32_t*>(out + c * 64) = pack2<kBF>(acc[c][0] * inv, acc[c][1] * inv);
+    else out[c * 32] = float_to_elem<kBF>(acc[c][0] * inv);
+  }
 }
 
 int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
@@ -505,7 +525,9 @@ Layout layout(const AttentionProblem& p, const Plan& pl) {
 }
 
 // The kernel, set up (and where there is room run) while the one before it still runs; it waits for
-// that one's end itself.
+// that one's end itself.  Behind the tensor-core kernel (67 against 75 us for 64 sequences over 8197
+// keys, 200 against 208 for 128 over 32768); without it the launch attribute's host time is more than
+// what is saved (30.3 against 27.7 us a call for 3 over 1000).
 template <typename A>
 cudaError_t launch_early(void (*kernel)(A), unsigned blocks, int threads, size_t smem, cudaStream_t stream, const A& a, bool early) {
   cudaLaunchAttribute attr[1];
@@ -543,7 +565,7 @@ cudaError_t run(const AttnArgs& a) {
   else if constexpr (D <= 128) e = run_stream<kBF, D, 4>(a);
   if (e != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(a.p.B) * a.p.n * a.p.Hq;
-  return launch_early(attn_join_kernel<kBF, D>, static_cast<unsigned>((rows + 3) / 4), 128, 0, a.p.stream, a, a.plan.blocks > 0);
+  return launch_early(attn_join_kernel<kBF, D>, static_cast<unsigned>((rows + 3) / 4), 128, 0, a.p.stream, a, a.plan.tc && a.plan.blocks > 0);
 }
 
 template <bool kBF>
