@@ -504,6 +504,15 @@ __global__ void __maxnreg__(kRegs) attn_prefix_kernel(const __grid_constant__ Tc
     }();
     cp_async_wait<0>();
     if (pending != ~0u) hand_over(pending);
+    if (*abort_flag) {  // no copy may outlive the block: wait, a bounded time, for the last of each slot
+      static_assert(kSlots % 2 == 0, "a warp's copies alternate between kSlots / 2 slots");
+      const uint64_t t0 = globaltimer_ns();
+      for (uint32_t d = 2; d <= kSlots && item >= d; d += 2) {
+        const uint32_t i = item - d;
+        while (!mbar_try_wait(&full[i % kSlots], (i / kSlots) & 1u) && globaltimer_ns() - t0 < kWaitLimitNs) {
+        }
+      }
+    }
   } else if (warp == 10) {
     // -------------------------------------------------------------------- MMAs ----
     // The whole warp runs the loop and one elected lane issues: every operand is the same in all
