@@ -56,7 +56,7 @@ struct Divider {
 };
 
 struct StreamArgs : AttnArgs {
-  Divider page;  // by the page size
+  Divider page, group, n;  // by the page size, the heads of a group, the new tokens of a sequence
 };
 
 constexpr float kRaise = 8.f;  // log2 of the growth that raises a row's maximum
@@ -146,7 +146,8 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
       at.b = -1;
       at.len = prefix_len;
     } else {
-      const int64_t q = (x0 - prefix_total) / pl.private_tiles;  // in steps of one tile per sequence
+      const int64_t own = x0 - prefix_total;
+      const int64_t q = pl.private_tiles == 1 ? own : own / pl.private_tiles;  // in steps of one tile per sequence
       int lo = 0, hi = ST::COARSE - 1;                           // coarse[lo] <= q < coarse[hi]
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
       rem = x0 - prefix_total - before * pl.private_tiles;
     }
     at.steps = steps_of(at.len);
-    at.tile = static_cast<int>(rem / at.steps);
+    at.tile = rem < at.steps ? 0 : static_cast<int>(rem / at.steps);
     at.step = static_cast<int>(rem - static_cast<int64_t>(at.tile) * at.steps);
   }
   unit_start = x0 - at.step;
@@ -248,17 +249,19 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
     int limit[NT][2];  // keys that the lane's two rows of each column tile see
 #pragma unroll
     for (int m = 0; m < NT; ++m) {
-      const int r = row0 + m * 8 + (lane >> 2);
-      const int g = r % pl.group, bi = r / pl.group;  // bi: query token within the rows' sequences
-      const uint16_t* src = p.q + (b0 + bi / p.n) * p.q_sb + (bi % p.n) * p.q_sn + (hk * pl.group + g) * p.q_sh + (lane & 3) * 2;
+      const int r = row0 + m * 8 + (lane >> 2), bi = a.group.of(r), g = r - bi * pl.group;  // bi: query token within the rows' sequences
+      const int s = a.n.of(bi);
+      const uint16_t* src = p.q + (b0 + s) * p.q_sb + (bi - s * p.n) * p.q_sn + (hk * pl.group + g) * p.q_sh + (lane & 3) * 2;
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
         qf[m][c][0] = r < rows ? __ldg(reinterpret_cast<const uint32_t*>(src + c * 16)) : 0u;
         qf[m][c][1] = r < rows ? __ldg(reinterpret_cast<const uint32_t*>(src + c * 16 + 8)) : 0u;
       }
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        limit[m][h] = at.b < 0 ? at.len : min(at.len, at.len - p.n + 1 + (row0 + m * 8 + (lane & 3) * 2 + h) / pl.group % p.n);
+      for (int h = 0; h < 2; ++h) {  // an own unit's query token is its row's: b0 + 0
+        const int i = a.group.of(row0 + m * 8 + (lane & 3) * 2 + h);
+        limit[m][h] = at.b < 0 ? at.len : min(at.len, at.len - p.n + 1 + i);
+      }
     }
     float o[NT][D / 16][4];
     float top[NT][2], sum[NT][2];
@@ -350,7 +353,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
     }
 
     // the part: slot = this share's number among those that meet in the unit
-    const int part = static_cast<int>(share - unit_start / per);
+    const int part = unit_start < x0 ? static_cast<int>(share - unit_start / per) : 0;
 #pragma unroll
     for (int m = 0; m < NT; ++m)
 #pragma unroll
@@ -360,7 +363,8 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
         for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
         const int r = row0 + m * 8 + (lane & 3) * 2 + h;
         if (r >= rows) continue;
-        const int64_t out_row = (static_cast<int64_t>(b0) * p.n + r / pl.group) * p.Hq + hk * pl.group + r % pl.group;
+        const int bi = a.group.of(r);
+        const int64_t out_row = (static_cast<int64_t>(b0) * p.n + bi) * p.Hq + hk * pl.group + (r - bi * pl.group);
         const int64_t slot = out_row * pl.parts + (at.b < 0 ? 0 : pl.prefix_parts) + part;
         if (lane < 4) a.part_ml[slot] = make_float2(top[m][h], l);
         float* dst = a.part_o + slot * D + (lane >> 2);
@@ -383,37 +387,35 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
 }
 
 // Joins a row's parts.  One warp per row; a lane holds the (m, l) of every 32nd part and D / 32
-// elements of the sums, and the parts' elements are read eight parts at a time.
-template <bool kBF, int D>
+// elements of the sums, and the parts' elements are read BATCH parts at a time.
+template <bool kBF, int D, int BATCH>
 __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
   const AttentionProblem& p = a.p;
   const Plan& pl = a.plan;
   const int lane = threadIdx.x & 31;
-  const int64_t rows = static_cast<int64_t>(p.B) * p.n * p.Hq;
-  const int64_t r = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int rows = p.B * p.n * p.Hq, r = blockIdx.x * 4 + (threadIdx.x >> 5);  // below 2^31
   if (r >= rows) return;
-  const int64_t bi = r / p.Hq;
-  const int h = static_cast<int>(r - bi * p.Hq), hk = h / pl.group, b = static_cast<int>(bi / p.n);
+  const int bi = r / p.Hq, h = r - bi * p.Hq, hk = h / pl.group, b = bi / p.n;
   grid_dependency_wait();  // the parts
   int first = 0, own = 0;  // parts of the prefix, at slots 0 ..; own parts, at slots prefix_parts ..
   if (p.prefix_len > 0) {
-    const int64_t stacked = bi * pl.group + h % pl.group;
+    const int stacked = bi * pl.group + h - hk * pl.group;
     if (pl.tc) {
-      const int u = tc_unit(pl, hk, static_cast<int>(stacked / kTcRows));
+      const int u = tc_unit(pl, hk, stacked / kTcRows);
       first = tc_last_group(pl, u) - tc_first_group(pl, u) + 1;
     } else {
       first = a.counts[stacked / pl.tile * p.kv.heads + hk];
     }
   }
   if (pl.private_parts && __ldg(p.lens + b) > 0) {
-    const int own_row = static_cast<int>(bi - static_cast<int64_t>(b) * p.n) * pl.group + h % pl.group;
+    const int own_row = (bi - b * p.n) * pl.group + h - hk * pl.group;
     own = a.counts[pl.prefix_tiles * p.kv.heads +
                    (static_cast<int64_t>(b) * pl.private_tiles + own_row / pl.tile) * p.kv.heads + hk];
   }
   const int parts = first + own, skip = pl.prefix_parts - first;
-  const float2* ml = a.part_ml + r * pl.parts;
-  constexpr int V = D % 128 == 0 ? 4 : D % 64 == 0 ? 2 : 1, N = D / 32 / V, BATCH = 8;  // elements of a load, loads of a row
-  const float* src = a.part_o + r * pl.parts * D + lane * V;
+  const float2* ml = a.part_ml + static_cast<int64_t>(r) * pl.parts;
+  constexpr int V = D % 128 == 0 ? 4 : D % 64 == 0 ? 2 : 1, N = D / 32 / V;  // elements of a load, loads of a row
+  const float* src = a.part_o + static_cast<int64_t>(r) * pl.parts * D + lane * V;
   float acc[N][V] = {}, l = 0.f, all = -INFINITY;
   for (int s0 = 0; s0 < parts; s0 += 32) {
     const int s = s0 + lane, n = min(32, parts - s0);
@@ -461,7 +463,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
 #pragma unroll
   for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
   const float inv = l > 0.f ? 1.f / l : l;  // a row that sees no key is zero; NaN stays
-  uint16_t* out = p.out + r * D + lane * V;
+  uint16_t* out = p.out + static_cast<int64_t>(r) * D + lane * V;
 #pragma unroll
   for (int c = 0; c < N; ++c) {
     if constexpr (V == 4)
@@ -556,6 +558,8 @@ cudaError_t run_stream(const AttnArgs& attn) {
   StreamArgs a{};
   static_cast<AttnArgs&>(a) = attn;
   a.page = Divider::by(static_cast<uint32_t>(attn.p.kv.page_size));
+  a.group = Divider::by(static_cast<uint32_t>(attn.plan.group));
+  a.n = Divider::by(static_cast<uint32_t>(attn.p.n));
   return launch_early(kernel, attn.plan.blocks, kStreamWarps * 32, smem, attn.p.stream, a, attn.plan.tc);
 }
 
@@ -568,7 +572,10 @@ cudaError_t run(const AttnArgs& a) {
   else if constexpr (D <= 128) e = run_stream<kBF, D, 4>(a);
   if (e != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(a.p.B) * a.p.n * a.p.Hq;
-  return launch_early(attn_join_kernel<kBF, D>, static_cast<unsigned>((rows + 3) / 4), 128, 0, a.p.stream, a, a.plan.tc && a.plan.blocks > 0);
+  // few rows: more parts in flight per row (96 rows of 34 parts 5.1 us, 6.1 with eight); many: more rows
+  // (8192 rows 10.4 us, 12.1 with sixteen)
+  const auto join = D <= 128 && rows <= 2048 ? attn_join_kernel<kBF, D, 16> : attn_join_kernel<kBF, D, 8>;
+  return launch_early(join, static_cast<unsigned>((rows + 3) / 4), 128, 0, a.p.stream, a, a.plan.tc && a.plan.blocks > 0);
 }
 
 template <bool kBF>
