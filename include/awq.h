@@ -532,13 +532,14 @@ awq_status_t awq_rope_append(const void* q, const void* k, const void* v, const 
  *   pages int32 [B, W] (row stride pages_stride), lens int32 [B]: each sequence's own pages and its
  *   number of own tokens; max_len >= every lens[b] (a longer one is cut to max_len), max_len <=
  *   W * page_size.  prefix_len, max_len are host values: the plan depends on them.
- * What the cache holds past a length is never used (it may be NaN).  A page outside [0, num_pages)
- * gives unspecified values for its sequence.  A row that sees no key is zero.  B, n or Hq 0:
- * AWQ_OK, no launch.
+ * A row uses only the keys that it sees: what the cache holds past a length, or a newer token's value,
+ * may be infinite or NaN.  A page outside [0, num_pages) gives unspecified values for its sequence.
+ * A row that sees no key is zero.  B, n or Hq 0: AWQ_OK, no launch.
  *   workspace: awq_attention_shared_workspace_size bytes (partial sums; same host values), 256-byte
  *   aligned; any content.  Calls that overlap in time need workspaces of their own.
  * Repeated calls give the same bits.  Requirements: q, the cache's tensors and out 16-byte aligned,
- * q's and the cache's strides multiples of 8; sizes below 2^31.
+ * q's and the cache's strides multiples of 8; prefix_len and max_len <= 2^31 - 256, other sizes below
+ * 2^31.
  */
 awq_status_t awq_attention_shared_workspace_size(int64_t B, int64_t n, int64_t Hq, int64_t heads,
                                                  int64_t D, int64_t prefix_len, int64_t max_len,

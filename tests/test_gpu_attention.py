@@ -216,6 +216,48 @@ def test_values_of_infinity_and_nan_reach_only_their_rows(awq):
     assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+@pytest.mark.parametrize("B,n,hq,hkv,D,prefix,lens,page", [
+    (3, 4, 8, 1, 128, 0, [4, 21, 70], 16),
+    (2, 2, 2, 1, 64, 100, [2, 16], 7),          # 4 rows a sequence, the prefix streamed
+    (2, 3, 40, 2, 96, 150, [17, 3], 16),        # 60 rows a sequence, the prefix on the tensor cores
+    (1, 20, 4, 4, 256, 19, [40], 16),
+])
+def test_values_of_newer_tokens_reach_only_rows_that_see_them(awq, B, n, hq, hkv, D, prefix, lens, page, value):
+    for dtype in ("fp16", "bf16"):
+        d = make(B, n, hq, hkv, D, prefix, lens, page, dtype, seed=13)
+        finite = awq.awq_attention_shared(**d)
+        e = dict(d, v_cache=d["v_cache"].clone())
+        for b in range(B):  # the two newest tokens' values
+            for j in (lens[b] - 1, lens[b] - 2):
+                e["v_cache"][int(d["pages"][b, j // page]), j % page] = value
+        got = awq.awq_attention_shared(**e)
+        assert not got[:, n - 2:].isfinite().any()
+        got[:, n - 2:] = finite[:, n - 2:]
+        check(got, d, dtype)
+
+
+def test_scale_of_zero_and_below(awq):
+    for scale in (0.0, -0.05):
+        for B in (3, 40):  # the prefix streamed, and on the tensor cores
+            d = make(B, 1, 8, 2, 128, 300, [10] * B, 16, "fp16", seed=14)
+            check(awq.awq_attention_shared(**d, scale=scale), d, "fp16", scale)
+
+
+def test_keys_of_small_weight(awq):
+    # every 16th key has the largest logit and a value of zero; the others, e^-13 of its weight (below
+    # fp16's full precision), make the result
+    for B in (2, 40):
+        d = make(B, 1, 4, 1, 64, 608, [96] * B, 16, "fp16", seed=15)
+        d["q"].zero_()
+        d["q"][..., 0] = 1.0
+        d["k_cache"][..., 0] = -13.0
+        d["v_cache"].abs_().mul_(1000.0)
+        d["k_cache"][:, 0, :, 0] = 0.0
+        d["v_cache"][:, 0] = 0.0
+        check(awq.awq_attention_shared(**d, scale=1.0), d, "fp16", 1.0)
+
+
 def test_cache_offsets_past_32_bits(awq):
     d = make(2, 1, 4, 1, 256, 40, [33, 20], 16, "fp16", seed=9)
     want = awq.awq_attention_shared(**d)

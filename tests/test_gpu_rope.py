@@ -176,6 +176,8 @@ def test_refusals(awq):
         awq.awq_rope(q, k, pos, awq.awq_rope_table(16, 128))  # more than the head holds
     with pytest.raises(ValueError):
         awq.awq_rope_table(16, 64, scaling="other")
+    with pytest.raises(ValueError):  # neither in place nor apart from its input
+        awq.awq_rope(q, k, pos, table, q_out=q.as_strided((4, 2, 64), (128, 64, 1)))
     cache = torch.empty((2, 4, 1, 64), dtype=torch.float16, device="cuda")
     with pytest.raises(ValueError):
         awq.awq_rope_append(q, k, v, pos, table, cache, cache.transpose(0, 1).contiguous().transpose(0, 1), pos)

@@ -77,6 +77,7 @@ def test_attention(lib):
     assert attention(lib) == DEVICE and attention(lib, B_=0, q=None, out=None) == 0
     assert attention(lib, Hq=3) == INVALID and attention(lib, prefix=-1) == INVALID and attention(lib, max_len=33) == INVALID
     assert attention(lib, kv=cache(head_dim=80)) == SHAPE and attention(lib, prefix=1 << 31) == SHAPE
+    assert attention(lib, prefix=(1 << 31) - 255) == SHAPE
     assert attention(lib, q=None) == INVALID and attention(lib, pp=None) == INVALID and attention(lib, lens=None) == INVALID
     assert attention(lib, prefix=0, pp=None) == DEVICE
     assert attention(lib, max_len=0, pages=None, lens=None) == DEVICE

@@ -50,7 +50,8 @@ def scratch(device, handle, nbytes):
     stream) share:
     calls on one stream never overlap, and no call reads what an earlier one left.  It grows by
     allocation (at least doubling) and a smaller one is kept, since a captured CUDA graph may hold its
-    address; make a stream's largest call once before capturing."""
+    address; make a stream's largest call once before capturing.  A graph keeps the workspace of the
+    stream that captured it: replayed beside other calls of that stream, it needs a workspace of its own."""
     kept = _scratch.get((device, handle))
     if kept is None:
         kept = _scratch[(device, handle)] = []
@@ -154,6 +155,8 @@ def _rope_inputs(q, k, positions, table):
 def _dense_or_same(out, t, name, dt, dev):
     if out.data_ptr() == t.data_ptr() and out.stride() == t.stride() and out.shape == t.shape and out.dtype is dt:
         return out  # in place
+    if out.numel() and out.data_ptr() == t.data_ptr():
+        raise ValueError(f"{name} starts where its input does but has other strides")
     _need(out, name, dt, t.shape, dev)
     return out
 

@@ -732,6 +732,8 @@ awq_status_t rope(awq::RopeProblem* p, int64_t T, int64_t Hq, int64_t Hkv, int64
   return ok();
 }
 
+constexpr int64_t kAttentionLimit = (int64_t{1} << 31) - 256;  // keys: the end of a step stays below 2^31
+
 // Shape rules of awq_attention_shared and its workspace; fills the host-side sizes of p.
 awq_status_t attention_shape(int64_t B, int64_t n, int64_t Hq, int64_t heads, int64_t D, int64_t prefix_len,
                              int64_t max_len, awq::AttentionProblem* p) {
@@ -742,9 +744,9 @@ awq_status_t attention_shape(int64_t B, int64_t n, int64_t Hq, int64_t heads, in
                 (long long)Hq, (long long)heads);
   if (!awq::attention_head_dim_supported(D))
     return fail(AWQ_ERR_UNSUPPORTED_SHAPE, "head_dim must be 64, 96, 128 or 256 (got %lld)", (long long)D);
-  if (Hq > 65536 || B > kDimLimit || n > kDimLimit || prefix_len > kDimLimit || max_len > kDimLimit || B * n > kDimLimit ||
+  if (Hq > 65536 || B > kDimLimit || n > kDimLimit || prefix_len > kAttentionLimit || max_len > kAttentionLimit || B * n > kDimLimit ||
       B * n * Hq > kDimLimit)
-    return fail(AWQ_ERR_UNSUPPORTED_SHAPE, "B * n * Hq, prefix_len and max_len must be below 2^31, Hq <= 65536");
+    return fail(AWQ_ERR_UNSUPPORTED_SHAPE, "B * n * Hq must be below 2^31, prefix_len and max_len <= 2^31 - 256, Hq <= 65536");
   p->B = static_cast<int>(B);
   p->n = static_cast<int>(n);
   p->Hq = static_cast<int>(Hq);

@@ -59,7 +59,13 @@ struct StreamArgs : AttnArgs {
   Divider page, group, n;  // by the page size, the heads of a group, the new tokens of a sequence
 };
 
-constexpr float kRaise = 8.f;  // log2 of the growth that raises a row's maximum
+// Whether one of two elements is infinite or NaN (all bits of its exponent set).
+template <bool kBF>
+__device__ __forceinline__ bool any_not_finite(uint32_t pair) {
+  constexpr uint32_t lo = kBF ? 0x7f80u : 0x7c00u, hi = lo << 16;
+  return (pair & lo) == lo || (pair & hi) == hi;
+}
+
 
 // Where a warp stands: a unit and a step of it.
 struct Cursor {
@@ -91,7 +97,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
   int64_t* coarse = reinterpret_cast<int64_t*>(reinterpret_cast<uint8_t*>(smem) + ST::RING);
   const int heads = p.kv.heads, max_len = static_cast<int>(p.max_len), prefix_len = static_cast<int>(p.prefix_len);
   const auto length = [&](int b) { return b < p.B ? min(max(__ldg(p.lens + b), 0), max_len) : 0; };
-  const auto steps_of = [](int len) { return (len + kStreamKeys - 1) / kStreamKeys; };
+  const auto steps_of = [](int len) { return len / kStreamKeys + (len % kStreamKeys != 0); };
 
   // coarse[g]: steps (of one unit each) of the sequences before g * gran; its last entry: of all
   const int gran = (p.B + ST::COARSE - 2) / (ST::COARSE - 1);
@@ -246,6 +252,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
     const int rows = at.b < 0 ? p.B * pl.own_rows : pl.own_rows, b0 = max(at.b, 0);
     const int end = at.step + static_cast<int>(min(static_cast<int64_t>(at.steps - at.step), x1 - x));
     uint32_t qf[NT][D / 16][2];
+    const bool causal = at.b >= 0 && p.n > 1;
     int limit[NT][2];  // keys that the lane's two rows of each column tile see
 #pragma unroll
     for (int m = 0; m < NT; ++m) {
@@ -308,7 +315,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
           }
           raise |= fmaxf(z[m][h][0], z[m][h][1]) > top[m][h] + kRaise;  // always where no key was seen yet
         }
-      // a row's maximum is raised when a logit exceeds it by 8 (p is up to 256 until then)
+      // a row's maximum is raised when a logit exceeds it by kRaise
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
         for (int m = 0; m < NT; ++m)
@@ -333,7 +340,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
       for (int m = 0; m < NT; ++m) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float ref = top[m][h] == -INFINITY ? 0.f : top[m][h];  // a row that has seen no key yet
+          const float ref = top[m][h] == -INFINITY ? 0.f : top[m][h] - kLift;  // a row that has seen no key yet: 0
           z[m][h][0] = exp2_approx(z[m][h][0] - ref);
           z[m][h][1] = exp2_approx(z[m][h][1] - ref);
           sum[m][h] += z[m][h][0] + z[m][h][1];
@@ -341,6 +348,39 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
         // P^T has keys along the lanes' rows; the second product wants them along the registers
         pf[m][0] = transpose8(pack2<kBF>(z[m][0][0], z[m][1][0]));
         pf[m][1] = transpose8(pack2<kBF>(z[m][0][1], z[m][1][1]));
+      }
+      // A key that some of the rows do not see (new tokens among themselves) has p = 0 there, and 0 times
+      // a value that is not finite would be NaN: with such a value among them, the step's products are
+      // made one by one.
+      bool odd = false;
+      if (causal && (step + 1) * kStreamKeys > at.len - p.n + 1) {
+#pragma unroll 1
+        for (int i = lane; i < kStreamKeys * CH; i += 32) {
+          const uint4 v = *reinterpret_cast<const uint4*>(st + (kStreamKeys + i / CH) * PITCH + i % CH * 8);
+          odd |= any_not_finite<kBF>(v.x) | any_not_finite<kBF>(v.y) | any_not_finite<kBF>(v.z) | any_not_finite<kBF>(v.w);
+        }
+        odd = __any_sync(0xffffffffu, odd);
+      }
+      if (odd) {
+#pragma unroll 1
+        for (int k = 0; k < kStreamKeys; ++k) {
+          const uint16_t* v = st + (kStreamKeys + k) * PITCH + (lane >> 2);
+#pragma unroll
+          for (int m = 0; m < NT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float w = __shfl_sync(0xffffffffu, k < 8 ? z[m][h][0] : z[m][h][1], (k & 7) * 4 + (lane & 3));
+              if (step * kStreamKeys + k < limit[m][h]) {
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) {
+                  o[m][c][h] += w * elem_to_float<kBF>(v[c * 16]);
+                  o[m][c][2 + h] += w * elem_to_float<kBF>(v[c * 16 + 8]);
+                }
+              }
+            }
+        }
+        __syncwarp();
+        continue;
       }
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
@@ -366,7 +406,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
         const int bi = a.group.of(r);
         const int64_t out_row = (static_cast<int64_t>(b0) * p.n + bi) * p.Hq + hk * pl.group + (r - bi * pl.group);
         const int64_t slot = out_row * pl.parts + (at.b < 0 ? 0 : pl.prefix_parts) + part;
-        if (lane < 4) a.part_ml[slot] = make_float2(top[m][h], l);
+        if (lane < 4) a.part_ml[slot] = make_float2(top[m][h] - kLift, l);
         float* dst = a.part_o + slot * D + (lane >> 2);
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {

@@ -9,6 +9,12 @@ namespace attn {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// A probability is kept as p = 2^(z - m + kLift), z the logit (base 2) and m the row's running maximum,
+// raised only when a logit exceeds it by kRaise.  Largest p: 2^15, in fp16's range; fp16 numbers with
+// their full 11 bits reach down to 2^-21 of the maximum (2^-14 without the lift).  The sum l and the
+// sums of values carry the same factor; a part's maximum is written as m - kLift.
+constexpr float kRaise = 8.f, kLift = 7.f;
+
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

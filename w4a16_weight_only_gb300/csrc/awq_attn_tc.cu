@@ -22,9 +22,9 @@
 // core's share of a step being 2050) and by the issue of the MMAs, each of which takes its thread about
 // as long as it runs.
 //
-// The running maximum m of a row is raised only when it is exceeded by more than 2^8: until then P
-// holds values up to 256 and nothing is rescaled (O and the sum l use the same m, so the result is
-// unchanged; P keeps its relative accuracy).  A raise waits for the row's last PV and rescales O in
+// The running maximum m of a row is raised only when it is exceeded by more than 2^kRaise: until then
+// nothing is rescaled (O and the sum l use the same m, so the result is unchanged; P keeps its relative
+// accuracy).  A raise waits for the row's last PV and rescales O in
 // TMEM.
 #include "awq_attn.cuh"
 
@@ -40,7 +40,6 @@ constexpr int kRegs = 136;
 constexpr int kSlots = 4;  // ring of key / value tiles
 constexpr uint64_t kWaitLimitNs = 200ull * 1000 * 1000;
 constexpr unsigned int kStatusAttnTimeout = 0x8u;
-constexpr float kRaise = 8.f;  // log2 of the growth that raises a row's maximum
 constexpr uint32_t kTmemCols = 512;
 
 // TMEM columns: S / P of the two halves, then O of the two halves.
@@ -287,7 +286,8 @@ __global__ void __maxnreg__(kRegs) attn_prefix_kernel(const __grid_constant__ Tc
       const int row = (warp & 3) * 32 + lane;  // of the half
       // a negative scale goes to the query's sign bits, so that the largest S is the largest logit
       const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
-      const float sl = fabsf(p.scale) * kLog2e;
+      // a scale of zero: the smallest factor, under which every finite logit is zero, but -inf stays
+      const float sl = p.scale == 0.f ? 0x1p-126f : fabsf(p.scale) * kLog2e;
       uint32_t steps_done = 0, segs = 0;
       for (int at = s_begin; at < s_end;) {
         const Segment sg = segment(at);
@@ -370,7 +370,7 @@ __global__ void __maxnreg__(kRegs) attn_prefix_kernel(const __grid_constant__ Tc
               }
             }
           }
-          const float ref = m == -INFINITY ? 0.f : -m * sl;
+          const float ref = m == -INFINITY ? 0.f : kLift - m * sl;
           const float2 sl2 = make_float2(sl, sl), ref2 = make_float2(ref, ref);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -418,7 +418,7 @@ __global__ void __maxnreg__(kRegs) attn_prefix_kernel(const __grid_constant__ Tc
         }
         __syncwarp();
         tc_fence_before();
-        if (in) a.part_ml[slot] = make_float2(m * sl, (sum0.x + sum0.y) + (sum1.x + sum1.y));
+        if (in) a.part_ml[slot] = make_float2(m * sl - kLift, (sum0.x + sum0.y) + (sum1.x + sum1.y));
         ++segs;
       }
     }();
