@@ -29,15 +29,19 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   return r;
 }
 
-template <int D>
+template <int D, bool kTma>
 struct Stream {
-  static constexpr int PITCH = D + 8;  // elements: eight rows of a fragment fall into different banks
-  static constexpr int STEP = 2 * kStreamKeys * PITCH;                // keys, then values
-  static constexpr int STAGES = D <= 64 ? 5 : D <= 96 ? 4 : 3;        // steps in flight per warp
+  // a step in shared memory: rows of PITCH elements, so that eight rows of a fragment fall into different
+  // banks; or (kTma) panels of 64 elements, 16 rows of 128 bytes in the 128-byte swizzle
+  static constexpr int PITCH = D + 8, PANELS = (D + 63) / 64;
+  static constexpr int HALF = kStreamKeys * (kTma ? PANELS * 64 : PITCH);  // elements of the keys or values
+  static constexpr int STEP = 2 * HALF;                               // keys, then values
+  static constexpr int STAGES = D <= 64 ? 5 : D <= 96 && !kTma ? 4 : 3;       // steps in flight per warp
   static constexpr int BLOCKS = D <= 128 ? 2 : 1;                     // blocks per SM
   static constexpr int COARSE = 256;                                  // entries of the table of lengths
   static constexpr int RING = kStreamWarps * STAGES * STEP * 2;
-  static constexpr int SMEM = RING + COARSE * 8 + 16;
+  static constexpr int BARS_OFF = RING + COARSE * 8;                  // full[kStreamWarps][STAGES]
+  static constexpr int SMEM = BARS_OFF + kStreamWarps * STAGES * 8 + 16 + (kTma ? 1024 : 0);
   static_assert(BLOCKS * (SMEM + 1024) <= 228 * 1024, "shared memory");
 };
 
@@ -56,6 +60,7 @@ struct Divider {
 };
 
 struct StreamArgs : AttnArgs {
+  CUtensorMap map_k, map_v;  // kTma
   Divider page, group, n;  // by the page size, the heads of a group, the new tokens of a sequence
 };
 
@@ -86,18 +91,23 @@ struct Cursor {
 // The products are taken transposed, S^T = K Q^T and O^T += V^T P^T: keys (then elements) fill the 16
 // rows of an m16n8k16 and 8 query rows its columns, so that the usual 8 heads of a group waste
 // nothing and the accumulators are half those of Q K^T.
-template <bool kBF, int D, int NT>
-__global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_stream_kernel(const __grid_constant__ StreamArgs a) {
-  using ST = Stream<D>;
-  constexpr int PITCH = ST::PITCH, STAGES = ST::STAGES;
-  extern __shared__ __align__(16) uint16_t smem[];
+template <bool kBF, int D, int NT, bool kTma>
+__global__ void __launch_bounds__(kStreamWarps * 32, Stream<D, kTma>::BLOCKS) attn_stream_kernel(const __grid_constant__ StreamArgs a) {
+  using ST = Stream<D, kTma>;
+  constexpr int STAGES = ST::STAGES;
+  extern __shared__ __align__(16) uint16_t smem_raw[];
+  uint16_t* smem = kTma ? smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u) / 2 : smem_raw;
+  // bytes from a step's keys or values to 16-byte chunk c of row k
+  const auto at_chunk = [](int k, int c) {
+    return kTma ? (c >> 3) * (kStreamKeys * 128) + k * 128 + (((c & 7) ^ (k & 7)) << 4) : k * (ST::PITCH * 2) + c * 16;
+  };
   const AttentionProblem& p = a.p;
   const Plan& pl = a.plan;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int64_t* coarse = reinterpret_cast<int64_t*>(reinterpret_cast<uint8_t*>(smem) + ST::RING);
-  const int heads = p.kv.heads, max_len = static_cast<int>(p.max_len), prefix_len = static_cast<int>(p.prefix_len);
-  const auto length = [&](int b) { return b < p.B ? min(max(__ldg(p.lens + b), 0), max_len) : 0; };
-  const auto steps_of = [](int len) { return len / kStreamKeys + (len % kStreamKeys != 0); };
+  const int heads = p.kv.heads, prefix_len = static_cast<int>(p.prefix_len);
+  const auto length = [&](int b) { return b < p.B ? own_length(p, b) : 0; };
+  const auto steps_of = [](int len) { return stream_steps(len); };
 
   // coarse[g]: steps (of one unit each) of the sequences before g * gran; its last entry: of all
   const int gran = (p.B + ST::COARSE - 2) / (ST::COARSE - 1);
@@ -134,12 +144,18 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
   }
   const int64_t prefix_total = pl.tc ? 0 : static_cast<int64_t>(steps_of(prefix_len)) * pl.prefix_tiles;
   const int64_t total = prefix_total + (pl.private_parts ? coarse[ST::COARSE - 1] * pl.private_tiles : 0);
-  const int64_t per = max(static_cast<int64_t>(pl.per_min), (total + pl.shares - 1) / pl.shares);
+  int shares = pl.shares;
+  if (pl.tc) {  // one wave of blocks on the SMs that the tensor-core kernel leaves
+    const int tc_per = tc_steps_per_group(pl, heads, total), tc_total = heads * (pl.tc_tiles / pl.tc_lanes) * pl.tc_steps;
+    const int left = pl.sms - (tc_total + tc_per - 1) / tc_per * pl.tc_lanes;
+    if (left > 0) shares = max(1, min(shares, left * (ST::BLOCKS * kStreamWarps) / heads));
+  }
+  const int64_t per = max(static_cast<int64_t>(pl.per_min), (total + shares - 1) / shares);
   const int w = blockIdx.x * kStreamWarps + warp, hk = w % heads, share = w / heads;
-  const int64_t x0 = share * per, x1 = share < pl.shares ? min(total, x0 + per) : x0;
+  const int64_t x0 = share * per, x1 = share < shares ? min(total, x0 + per) : x0;
   launch_dependents();
   if (x0 >= x1) {
-    if (pl.tc) grid_dependency_wait();
+    if (pl.tc && blockIdx.x == gridDim.x - 1) grid_dependency_wait();
     return;
   }
 
@@ -201,18 +217,43 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
   // key l of the next step to load starts; its page was read a step earlier.
   constexpr int CH = D / 8;  // 16-byte chunks of a row
   uint16_t* ring = smem + warp * STAGES * ST::STEP;
+  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(smem) + ST::BARS_OFF) + warp * STAGES;
+  if constexpr (kTma) {
+    if (lane == 0) {
+      for (int s = 0; s < STAGES; ++s) mbar_init(&full[s], 1);
+      fence_mbar_init();
+    }
+    __syncwarp();
+  }
   Cursor ahead = at;
   int64_t to_load = x1 - x0;
   uint32_t loaded = 0;  // steps
   int page_next = 0, token_next = 0;
   const auto fetch_page = [&] {
-    const int key = ahead.step * kStreamKeys + (lane & 15), slot = a.page.of(key);
+    const int key = ahead.step * kStreamKeys + (kTma ? 0 : lane & 15), slot = a.page.of(key);
     const int* table = ahead.b < 0 ? p.prefix_pages : p.pages + ahead.b * p.pages_ld;
     page_next = key < ahead.len ? __ldg(table + slot) : -1;
     token_next = key - slot * p.kv.page_size;
   };
   const auto load_step = [&] {
-    if (to_load > 0) {
+    if (kTma && to_load > 0) {  // a step lies in one page
+      const int page = page_next, token = token_next;
+      --to_load;
+      if (++ahead.step == ahead.steps && to_load > 0) advance(ahead);
+      if (to_load > 0) fetch_page();
+      if (lane == 0) {
+        uint64_t* bar = &full[loaded % STAGES];
+        uint16_t* dst = ring + loaded % STAGES * ST::STEP;
+        mbar_arrive_expect_tx(bar, ST::STEP * 2);
+#pragma unroll
+        for (int n = 0; n < ST::PANELS; ++n) {  // a page outside the cache: zeros
+          tma_load_4d(dst + n * kStreamKeys * 64, &a.map_k, bar, 64 * n, token, hk, page);
+          tma_load_4d(dst + ST::HALF + n * kStreamKeys * 64, &a.map_v, bar, 64 * n, token, hk, page);
+        }
+      }
+      __syncwarp();
+      ++loaded;
+    } else if (to_load > 0) {
       const int page = page_next;
       const bool valid = page >= 0 && page < p.kv.num_pages;
       const int64_t off = page * p.kv.page_stride + static_cast<int64_t>(token_next) * p.kv.token_stride +
@@ -228,12 +269,12 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
         const int64_t o = __shfl_sync(0xffffffffu, off, k);
         const bool in = (live >> k) & 1u;
         const int64_t from = in ? o + c * 8 : 0;
-        cp_async16(dk + (k * PITCH + c * 8) * 2, p.kv.k + from, in);
-        cp_async16(dk + ((kStreamKeys + k) * PITCH + c * 8) * 2, p.kv.v + from, in);
+        cp_async16(dk + at_chunk(k, c), p.kv.k + from, in);
+        cp_async16(dk + ST::HALF * 2 + at_chunk(k, c), p.kv.v + from, in);
       }
       ++loaded;
     }
-    cp_async_commit();
+    if constexpr (!kTma) cp_async_commit();
   };
   fetch_page();
 #pragma unroll
@@ -245,8 +286,19 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
     else mma16816(d, x[0], x[1], x[2], x[3], b0, b1);
   };
 
+  // Step `used` has arrived.  A bounded wait: one that gives up sets the status word, and the warp leaves
+  // once its copies in flight have landed (waiting for each a bounded time too).
+  const auto arrived = [&](uint32_t used) -> bool {
+    const auto there = [&] { return __all_sync(0xffffffffu, mbar_try_wait(&full[used % STAGES], (used / STAGES) & 1u)) != 0; };
+    if (there()) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (!there())
+      if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > kWaitLimitNs)) return false;
+    return true;
+  };
   uint32_t used = 0;  // steps
-  for (int64_t x = x0; x < x1;) {
+  bool gave_up = false;
+  for (int64_t x = x0; x < x1 && !gave_up;) {
     // one run of a unit
     const int row0 = at.tile * (8 * NT);
     const int rows = at.b < 0 ? p.B * pl.own_rows : pl.own_rows, b0 = max(at.b, 0);
@@ -282,13 +334,23 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
 
     for (int step = at.step; step < end; ++step, ++used) {
       load_step();
-      cp_async_wait<STAGES - 1>();
+      uint16_t* st = ring + used % STAGES * ST::STEP;
+      const uint32_t ks = smem_u32(st), vs = ks + ST::HALF * 2;
+      if constexpr (kTma) {
+        if (!arrived(used)) {
+          gave_up = true;
+          break;
+        }
+        const int live = at.len - step * kStreamKeys;  // what follows the last key may be anything: values to zero
+        if (live < kStreamKeys) {
+          for (int i = live * CH + lane; i < kStreamKeys * CH; i += 32)
+            *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(st + ST::HALF) + at_chunk(i / CH, i % CH)) = make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();  // before the copy that overwrites them
+        }
+      } else {
+        cp_async_wait<STAGES - 1>();
+      }
       __syncwarp();
-      const uint16_t* st = ring + used % STAGES * ST::STEP;
-      const uint32_t frag = (lane & 15) * PITCH + (lane >> 4) * 8;
-      const uint32_t ks = smem_u32(st) + frag * 2;
-      // values: rows are keys, so the transposed tile's first 8 columns are keys 0-7
-      const uint32_t vs = smem_u32(st + kStreamKeys * PITCH) + (((lane & 7) + (lane >> 4) * 8) * PITCH + ((lane >> 3) & 1) * 8) * 2;
       float s[NT][2][4];  // two chains
 #pragma unroll
       for (int m = 0; m < NT; ++m)
@@ -297,7 +359,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
         uint32_t kf[4];  // (keys 0-7, low), (keys 8-15, low), (keys 0-7, high), (keys 8-15, high)
-        ldmatrix_x4(kf, ks + c * 32);
+        ldmatrix_x4(kf, ks + at_chunk(lane & 15, 2 * c + (lane >> 4)));
 #pragma unroll
         for (int m = 0; m < NT; ++m) mma(s[m][c & 1], kf, qf[m][c][0], qf[m][c][1]);
       }
@@ -356,7 +418,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
       if (causal && (step + 1) * kStreamKeys > at.len - p.n + 1) {
 #pragma unroll 1
         for (int i = lane; i < kStreamKeys * CH; i += 32) {
-          const uint4 v = *reinterpret_cast<const uint4*>(st + (kStreamKeys + i / CH) * PITCH + i % CH * 8);
+          const uint4 v = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(st + ST::HALF) + at_chunk(i / CH, i % CH));
           odd |= any_not_finite<kBF>(v.x) | any_not_finite<kBF>(v.y) | any_not_finite<kBF>(v.z) | any_not_finite<kBF>(v.w);
         }
         odd = __any_sync(0xffffffffu, odd);
@@ -364,7 +426,10 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
       if (odd) {
 #pragma unroll 1
         for (int k = 0; k < kStreamKeys; ++k) {
-          const uint16_t* v = st + (kStreamKeys + k) * PITCH + (lane >> 2);
+          const auto value = [&](int c) {  // element c 8 + lane / 4 of the key
+            return elem_to_float<kBF>(*reinterpret_cast<const uint16_t*>(reinterpret_cast<const uint8_t*>(st + ST::HALF) +
+                                                                         at_chunk(k, c) + (lane >> 2) * 2));
+          };
 #pragma unroll
           for (int m = 0; m < NT; ++m)
 #pragma unroll
@@ -373,8 +438,8 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
               if (step * kStreamKeys + k < limit[m][h]) {
 #pragma unroll
                 for (int c = 0; c < D / 16; ++c) {
-                  o[m][c][h] += w * elem_to_float<kBF>(v[c * 16]);
-                  o[m][c][2 + h] += w * elem_to_float<kBF>(v[c * 16 + 8]);
+                  o[m][c][h] += w * value(2 * c);
+                  o[m][c][2 + h] += w * value(2 * c + 1);
                 }
               }
             }
@@ -385,13 +450,15 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
         uint32_t vf[4];  // (elements 0-7, keys 0-7), (8-15, 0-7), (0-7, 8-15), (8-15, 8-15)
-        ldmatrix_x4_trans(vf, vs + c * 32);
+        // rows are keys, so the transposed tile's first 8 columns are keys 0-7
+        ldmatrix_x4_trans(vf, vs + at_chunk((lane & 7) + (lane >> 4) * 8, 2 * c + ((lane >> 3) & 1)));
 #pragma unroll
         for (int m = 0; m < NT; ++m) mma(o[m][c], vf, pf[m][0], pf[m][1]);
       }
       __syncwarp();  // the next load_step overwrites a stage read here
     }
 
+    if (gave_up) break;
     // the part: slot = this share's number among those that meet in the unit
     const int part = unit_start < x0 ? static_cast<int>(share - unit_start / per) : 0;
 #pragma unroll
@@ -422,8 +489,13 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D>::BLOCKS) attn_str
       unit_start = x;
     }
   }
-  cp_async_wait<0>();
-  if (pl.tc) grid_dependency_wait();  // so that this kernel's end is also the tensor-core kernel's
+  if constexpr (!kTma) cp_async_wait<0>();
+  if (kTma && gave_up) {
+    if (lane == 0) atomicOr(a.status, kStatusAttnTimeout);
+    for (; used < loaded; ++used) arrived(used);
+  }
+  // One block waits, so that this kernel's end is also the tensor-core kernel's; the others make room.
+  if (pl.tc && blockIdx.x == gridDim.x - 1) grid_dependency_wait();
 }
 
 // Joins a row's parts.  One warp per row; a lane holds the (m, l) of every 32nd part and D / 32
@@ -441,8 +513,8 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
   if (p.prefix_len > 0) {
     const int stacked = bi * pl.group + h - hk * pl.group;
     if (pl.tc) {
-      const int u = tc_unit(pl, hk, stacked / kTcRows);
-      first = tc_last_group(pl, u) - tc_first_group(pl, u) + 1;
+      const int u = tc_unit(pl, hk, stacked / kTcRows), per = *a.tc_per;
+      first = tc_last_group(pl, u, per) - tc_first_group(pl, u, per) + 1;
     } else {
       first = a.counts[stacked / pl.tile * p.kv.heads + hk];
     }
@@ -518,6 +590,7 @@ int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
 Plan make_plan(const AttentionProblem& p, int sms) {
   Plan pl{};
+  pl.sms = sms;
   pl.group = p.Hq / p.kv.heads;
   pl.own_rows = p.n * pl.group;
   const int64_t stacked = static_cast<int64_t>(p.B) * pl.own_rows;  // rows that share a prefix key
@@ -556,7 +629,7 @@ Plan make_plan(const AttentionProblem& p, int sms) {
 }
 
 struct Layout {
-  size_t ml, counts, bytes;  // offsets; part_o first
+  size_t ml, per, counts, bytes;  // offsets; part_o first
 };
 
 Layout layout(const AttentionProblem& p, const Plan& pl) {
@@ -564,7 +637,8 @@ Layout layout(const AttentionProblem& p, const Plan& pl) {
   const size_t units = (static_cast<size_t>(pl.prefix_tiles) + static_cast<size_t>(p.B) * pl.private_tiles) * p.kv.heads;
   Layout l;
   l.ml = slots * p.kv.head_dim * 4;
-  l.counts = l.ml + slots * 8;
+  l.per = l.ml + slots * 8;
+  l.counts = l.per + 4;
   l.bytes = l.counts + units * 4;
   return l;
 }
@@ -588,19 +662,27 @@ cudaError_t launch_early(void (*kernel)(A), unsigned blocks, int threads, size_t
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-template <bool kBF, int D, int NT>
-cudaError_t run_stream(const AttnArgs& attn) {
-  if (attn.plan.blocks == 0) return cudaSuccess;
-  constexpr int smem = Stream<D>::SMEM;
-  const auto kernel = attn_stream_kernel<kBF, D, NT>;
+template <bool kBF, int D, int NT, bool kTma>
+cudaError_t launch_stream(const AttnArgs& attn, StreamArgs& a) {
+  constexpr int smem = Stream<D, kTma>::SMEM;
+  const auto kernel = attn_stream_kernel<kBF, D, NT, kTma>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  StreamArgs a{};
   static_cast<AttnArgs&>(a) = attn;
   a.page = Divider::by(static_cast<uint32_t>(attn.p.kv.page_size));
   a.group = Divider::by(static_cast<uint32_t>(attn.plan.group));
   a.n = Divider::by(static_cast<uint32_t>(attn.p.n));
   return launch_early(kernel, attn.plan.blocks, kStreamWarps * 32, smem, attn.p.stream, a, attn.plan.tc);
+}
+
+template <bool kBF, int D, int NT>
+cudaError_t run_stream(const AttnArgs& attn) {
+  if (attn.plan.blocks == 0) return cudaSuccess;
+  StreamArgs a{};
+  if (attn.p.kv.page_size % kStreamKeys == 0 && make_cache_map(&a.map_k, attn.p.kv.k, attn.p, kStreamKeys) &&
+      make_cache_map(&a.map_v, attn.p.kv.v, attn.p, kStreamKeys))
+    return launch_stream<kBF, D, NT, true>(attn, a);
+  return launch_stream<kBF, D, NT, false>(attn, a);
 }
 
 template <bool kBF, int D>
@@ -638,14 +720,13 @@ cudaError_t launch_attention(const AttentionProblem& p, int sms) {
   AttnArgs a{};
   a.p = p;
   a.plan = make_plan(p, sms);
-  if (a.plan.tc) {
-    const cudaError_t e = status_word_ptr(&a.status);
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t e = status_word_ptr(&a.status);
+  if (e != cudaSuccess) return e;
   const Layout l = layout(p, a.plan);
   uint8_t* ws = static_cast<uint8_t*>(p.workspace);
   a.part_o = reinterpret_cast<float*>(ws);
   a.part_ml = reinterpret_cast<float2*>(ws + l.ml);
+  a.tc_per = reinterpret_cast<int*>(ws + l.per);
   a.counts = reinterpret_cast<int*>(ws + l.counts);
   return p.bf16 ? run_dim<true>(a) : run_dim<false>(a);
 }

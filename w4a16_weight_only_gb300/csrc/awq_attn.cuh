@@ -43,6 +43,19 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Copies a 64-element wide box of tokens.
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(ptx::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(ptx::smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+
+// Bounded waits give up after this long, set the bit in the status word and leave.
+constexpr uint64_t kWaitLimitNs = 200ull * 1000 * 1000;
+constexpr unsigned int kStatusAttnTimeout = 0x8u;
+
 // How a call is cut.  Row r = (b n + i) Hq + h of the output; part s of row r is at
 // part_o[(r parts + s) D], part_ml[r parts + s]; slots [0, prefix_parts) are the prefix's, the others
 // the sequence's own.
@@ -50,7 +63,7 @@ __device__ __forceinline__ void cp_async_wait() {
 // Tensor-core kernel (tc, the prefix's keys): row tiles of kTcRows rows per key/value head, steps of
 // kTcKeys keys.  The row tiles of a head go side by side, one block each (tc_lanes blocks, a group), so
 // that they read the same keys at the same time and HBM is read once; the steps of all heads form one
-// sequence of which group g takes [g per, (g + 1) per).  (More row tiles than SMs: a group is one block,
+// sequence of which group g takes [g per, (g + 1) per), per being found on the device.  (More row tiles than SMs: a group is one block,
 // and the steps of all heads' tiles form the sequence.)
 //
 // Streaming kernel (the sequences' own keys, and the prefix's without tc): units are (sequence, row
@@ -63,7 +76,9 @@ struct Plan {
   int group;  // query heads per key/value head
   int own_rows;  // rows of one sequence that share a key/value head
   bool tc;
-  int tc_tiles, tc_steps, tc_lanes, tc_per, tc_groups;
+  int sms;
+  int tc_tiles, tc_steps, tc_lanes;
+  int tc_per, tc_groups;             // least steps of a group, most groups
   int tile;                          // rows of a streaming unit
   int prefix_tiles, private_tiles;   // row tiles per key/value head of the streaming units
   int per_min, shares, blocks;       // streaming kernel
@@ -77,20 +92,48 @@ constexpr int kStreamWarps = 4;
 constexpr int kTcRows = 256;  // two 128-row tensor-core tiles
 constexpr int kTcKeys = 128;
 
-// Unit (of the sequence of steps) of a head's row tile; first and last group of a unit's steps.
+// Unit (of the sequence of steps) of a head's row tile; first and last group of a unit's steps, of which a
+// group takes `per`.
 __host__ __device__ inline int tc_unit(const Plan& pl, int hk, int tile) { return pl.tc_lanes > 1 ? hk : hk * pl.tc_tiles + tile; }
-__host__ __device__ inline int tc_first_group(const Plan& pl, int u) { return u * pl.tc_steps / pl.tc_per; }
-__host__ __device__ inline int tc_last_group(const Plan& pl, int u) { return ((u + 1) * pl.tc_steps - 1) / pl.tc_per; }
+__host__ __device__ inline int tc_first_group(const Plan& pl, int u, int per) { return u * pl.tc_steps / per; }
+__host__ __device__ inline int tc_last_group(const Plan& pl, int u, int per) { return ((u + 1) * pl.tc_steps - 1) / per; }
+
+// The two kernels of a call with tc run side by side, the tensor-core kernel on as many SMs as its share of
+// the work, the streaming kernel on the others.  The lengths decide, so the device does: a block's step of
+// the one takes some 1.66 us of an SM, a step of a head of the other 0.11 us (heads of 128; fewer elements,
+// less of both).  Blocks of the tensor-core kernel beyond its share leave at once.  128 sequences of 1024
+// own keys over 32768 shared ones, 8 heads: 100 SMs and 52, 149 us for both and the join; one after the
+// other on all SMs 192 us; 64 of 512 over 8197: 50 and 67 us.
+constexpr int64_t kTcStepNs = 1660, kStreamStepNs = 108;
+
+// Steps that a group of the tensor-core kernel takes when each head has `own` steps of the sequences' own keys.
+__device__ inline int tc_steps_per_group(const Plan& pl, int heads, int64_t own) {
+  const int total = heads * (pl.tc_tiles / pl.tc_lanes) * pl.tc_steps;
+  const int64_t tc = total * (pl.tc_lanes * kTcStepNs);
+  const int64_t rest = min(own, int64_t{1} << 30) * heads * kStreamStepNs;
+  const int64_t sms = pl.sms * tc / (tc + rest);
+  const int groups = max(1, min(pl.tc_groups, static_cast<int>((sms + pl.tc_lanes / 2) / pl.tc_lanes)));
+  return max(pl.tc_per, (total + groups - 1) / groups);
+}
 
 struct AttnArgs {
   AttentionProblem p;
   Plan plan;
   float* part_o;
   float2* part_ml;
+  int* tc_per;  // steps of a tensor-core group
   int* counts;  // parts of each streaming unit, per head: [prefix_tiles][heads], then [B][private_tiles][heads]
   unsigned int* status;
 };
 
+__device__ __forceinline__ int own_length(const AttentionProblem& p, int b) {
+  return min(max(__ldg(p.lens + b), 0), static_cast<int>(p.max_len));
+}
+__device__ __forceinline__ int stream_steps(int len) { return len / kStreamKeys + (len % kStreamKeys != 0); }
+
+// The keys or values of the cache as [page][head][token][element] for boxes of 64 elements of `box`
+// tokens, 128-byte swizzle.  False: the strides do not allow it.
+bool make_cache_map(CUtensorMap* map, const void* base, const AttentionProblem& p, int box);
 bool tc_head_dim_supported(int D);
 cudaError_t launch_prefix_tc(const AttnArgs& a);
 

@@ -38,8 +38,6 @@ constexpr int kThreads = 384;
 // Registers per thread at launch; the softmax warpgroups take 160, the third one 88: 2 x 160 + 88 = 3 x 136.
 constexpr int kRegs = 136;
 constexpr int kSlots = 4;  // ring of key / value tiles
-constexpr uint64_t kWaitLimitNs = 200ull * 1000 * 1000;
-constexpr unsigned int kStatusAttnTimeout = 0x8u;
 constexpr uint32_t kTmemCols = 512;
 
 // TMEM columns: S / P of the two halves, then O of the two halves.
@@ -176,19 +174,10 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 
 struct TcArgs : AttnArgs {
-  CUtensorMap map_k, map_v;  // the cache as [page][head][token][element]
+  CUtensorMap map_k, map_v;  // make_cache_map
   int box_tokens;
   bool tma;
 };
-
-// Copies a 64-element wide box of tokens.
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z, int w) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
-      : "memory");
-}
 
 template <bool kBF, int D>
 __global__ void __maxnreg__(kRegs) attn_prefix_kernel(const __grid_constant__ TcArgs a) {
@@ -210,6 +199,16 @@ __global__ void __maxnreg__(kRegs) attn_prefix_kernel(const __grid_constant__ Tc
   const Plan& pl = a.plan;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  launch_dependents();
+  __shared__ int64_t own_steps[kThreads / 32];
+  {
+    int64_t own = 0;  // steps of the sequences' own keys
+    if (pl.private_parts)
+      for (int b = threadIdx.x; b < p.B; b += kThreads) own += stream_steps(own_length(p, b));
+#pragma unroll
+    for (int d = 16; d; d >>= 1) own += __shfl_xor_sync(0xffffffffu, own, d);
+    if (lane == 0) own_steps[warp] = own;
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&full[i], 1);
@@ -235,7 +234,11 @@ __global__ void __maxnreg__(kRegs) attn_prefix_kernel(const __grid_constant__ Tc
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  launch_dependents();
+  int64_t own = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) own += own_steps[w];
+  const int per = tc_steps_per_group(pl, p.kv.heads, own * pl.private_tiles);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.tc_per = per;
 
   // Bounded waits; a role that gives up sets the flag, and the others leave at their next wait.
   // All lanes of a warp wait together and get one answer.
@@ -258,7 +261,7 @@ __global__ void __maxnreg__(kRegs) attn_prefix_kernel(const __grid_constant__ Tc
   // this block's steps, tile by tile
   const int total = p.kv.heads * (pl.tc_tiles / pl.tc_lanes) * pl.tc_steps;
   const int group = blockIdx.x / pl.tc_lanes, tile_lane = blockIdx.x - group * pl.tc_lanes;
-  const int s_begin = group * pl.tc_per, s_end = min(total, s_begin + pl.tc_per);
+  const int s_begin = group * per, s_end = min(total, s_begin + per);  // none for a group beyond the last
   const int stacked = p.B * p.n * pl.group;
   struct Segment {
     int hk, row0, halves, step0, steps, part;
@@ -271,7 +274,7 @@ __global__ void __maxnreg__(kRegs) attn_prefix_kernel(const __grid_constant__ Tc
     s.halves = stacked - s.row0 > 128 ? 2 : 1;
     s.step0 = at - u * pl.tc_steps;
     s.steps = min(pl.tc_steps - s.step0, s_end - at);
-    s.part = group - tc_first_group(pl, u);
+    s.part = group - tc_first_group(pl, u, per);
     return s;
   };
 
@@ -611,16 +614,6 @@ __global__ void __maxnreg__(kRegs) attn_prefix_kernel(const __grid_constant__ Tc
   }
 }
 
-bool make_map(CUtensorMap* map, const void* base, const AttentionProblem& p, int box) {
-  const uint64_t dims[4] = {static_cast<uint64_t>(p.kv.head_dim), static_cast<uint64_t>(p.kv.page_size),
-                            static_cast<uint64_t>(p.kv.heads), static_cast<uint64_t>(p.kv.num_pages)};
-  const uint64_t strides[3] = {static_cast<uint64_t>(p.kv.token_stride) * 2, static_cast<uint64_t>(p.kv.head_stride) * 2,
-                               static_cast<uint64_t>(p.kv.page_stride) * 2};
-  const uint32_t boxes[4] = {64, static_cast<uint32_t>(box), 1, 1};
-  return make_tmap_4d(map, p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, dims, strides,
-                      boxes, CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
 // Tokens of a TMA box: a step is whole boxes and no box crosses a page; 0: the pages do not allow it
 // (a box's rows must start at a multiple of 8, where the swizzle pattern repeats).
 int box_tokens(int page_size) {
@@ -634,7 +627,7 @@ cudaError_t run(const AttnArgs& attn) {
   static_cast<AttnArgs&>(a) = attn;
   a.box_tokens = box_tokens(attn.p.kv.page_size);
   a.tma = a.box_tokens > 0 && attn.p.prefix_len >= kTcKeys &&
-          make_map(&a.map_k, attn.p.kv.k, attn.p, a.box_tokens) && make_map(&a.map_v, attn.p.kv.v, attn.p, a.box_tokens);
+          make_cache_map(&a.map_k, attn.p.kv.k, attn.p, a.box_tokens) && make_cache_map(&a.map_v, attn.p.kv.v, attn.p, a.box_tokens);
   if (!a.tma) a.box_tokens = kTcKeys;
   const cudaError_t e =
       cudaFuncSetAttribute(attn_prefix_kernel<kBF, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::SMEM);
@@ -644,6 +637,16 @@ cudaError_t run(const AttnArgs& attn) {
 }
 
 }  // namespace
+
+bool attn::make_cache_map(CUtensorMap* map, const void* base, const AttentionProblem& p, int box) {
+  const uint64_t dims[4] = {static_cast<uint64_t>(p.kv.head_dim), static_cast<uint64_t>(p.kv.page_size),
+                            static_cast<uint64_t>(p.kv.heads), static_cast<uint64_t>(p.kv.num_pages)};
+  const uint64_t strides[3] = {static_cast<uint64_t>(p.kv.token_stride) * 2, static_cast<uint64_t>(p.kv.head_stride) * 2,
+                               static_cast<uint64_t>(p.kv.page_stride) * 2};
+  const uint32_t boxes[4] = {64, static_cast<uint32_t>(box), 1, 1};
+  return make_tmap_4d(map, p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, dims, strides,
+                      boxes, CU_TENSOR_MAP_SWIZZLE_128B);
+}
 
 bool attn::tc_head_dim_supported(int D) { return D == 64 || D == 96 || D == 128; }
 
