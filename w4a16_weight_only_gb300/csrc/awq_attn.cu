@@ -145,9 +145,8 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D, kTma>::BLOCKS) at
   const int64_t prefix_total = pl.tc ? 0 : static_cast<int64_t>(steps_of(prefix_len)) * pl.prefix_tiles;
   const int64_t total = prefix_total + (pl.private_parts ? coarse[ST::COARSE - 1] * pl.private_tiles : 0);
   int shares = pl.shares;
-  if (pl.tc) {  // one wave of blocks on the SMs that the tensor-core kernel leaves
-    const int tc_per = tc_steps_per_group(pl, heads, total), tc_total = heads * (pl.tc_tiles / pl.tc_lanes) * pl.tc_steps;
-    const int left = pl.sms - (tc_total + tc_per - 1) / tc_per * pl.tc_lanes;
+  if (pl.tc) {
+    const int left = split_sms(pl, heads, total, static_cast<int64_t>(p.B) * pl.private_tiles).left;
     if (left > 0) shares = max(1, min(shares, left * (ST::BLOCKS * kStreamWarps) / heads));
   }
   const int64_t per = max(static_cast<int64_t>(pl.per_min), (total + shares - 1) / shares);

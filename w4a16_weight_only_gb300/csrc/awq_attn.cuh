@@ -99,21 +99,36 @@ __host__ __device__ inline int tc_first_group(const Plan& pl, int u, int per) { 
 __host__ __device__ inline int tc_last_group(const Plan& pl, int u, int per) { return ((u + 1) * pl.tc_steps - 1) / per; }
 
 // The two kernels of a call with tc run side by side, the tensor-core kernel on as many SMs as its share of
-// the work, the streaming kernel on the others.  The lengths decide, so the device does: a block's step of
-// the one takes some 1.66 us of an SM, a step of a head of the other 0.11 us (heads of 128; fewer elements,
-// less of both).  Blocks of the tensor-core kernel beyond its share leave at once.  128 sequences of 1024
-// own keys over 32768 shared ones, 8 heads: 100 SMs and 52, 149 us for both and the join; one after the
-// other on all SMs 192 us; 64 of 512 over 8197: 50 and 67 us.
-constexpr int64_t kTcStepNs = 1660, kStreamStepNs = 108;
+// the work, the streaming kernel on the others.  The lengths decide, so the device does.  A block's step of
+// the one takes some 1.66 us of an SM and its start and end as long as three more, a step of a head of the
+// other 0.11 us and a unit's start and end as long as two (heads of 128; fewer elements, less of both).  A
+// streaming kernel that would get fewer than a twelfth of the SMs comes after, on all.  Blocks of the tensor-core kernel beyond its
+// share leave at once; the streaming kernel's blocks are one wave on the SMs left, or, where whole groups
+// leave it much less than its share, as many as all SMs hold.  128 sequences of 1024 own keys over 32768
+// shared ones, 8 heads: 100 SMs and 52, SIDE us with the join; one after the other on all SMs 192 us; 64 of
+// 512 over 8197: SIDE2 and 67 us.
+constexpr int64_t kTcStepNs = 1660, kTcFixedSteps = 3, kStreamStepNs = 108, kStreamFixedSteps = 2;
 
-// Steps that a group of the tensor-core kernel takes when each head has `own` steps of the sequences' own keys.
-__device__ inline int tc_steps_per_group(const Plan& pl, int heads, int64_t own) {
+constexpr int kLeastShare = 12;
+
+struct Split {
+  int per;    // steps that a group of the tensor-core kernel takes
+  int left;   // SMs on which the streaming kernel's blocks are one wave; 0: all
+};
+
+// `own`: steps of the sequences' own keys, per head; `units`: sequences times their row tiles.
+__device__ inline Split split_sms(const Plan& pl, int heads, int64_t own, int64_t units) {
   const int total = heads * (pl.tc_tiles / pl.tc_lanes) * pl.tc_steps;
-  const int64_t tc = total * (pl.tc_lanes * kTcStepNs);
-  const int64_t rest = min(own, int64_t{1} << 30) * heads * kStreamStepNs;
-  const int64_t sms = pl.sms * tc / (tc + rest);
-  const int groups = max(1, min(pl.tc_groups, static_cast<int>((sms + pl.tc_lanes / 2) / pl.tc_lanes)));
-  return max(pl.tc_per, (total + groups - 1) / groups);
+  const int64_t tc = (total + kTcFixedSteps * pl.tc_groups) * (pl.tc_lanes * kTcStepNs);
+  const int64_t rest = min(own + kStreamFixedSteps * units, int64_t{1} << 32) * heads * kStreamStepNs;
+  int share = static_cast<int>(pl.sms * tc / (tc + rest));  // SMs
+  if ((pl.sms - share) * kLeastShare < pl.sms) share = pl.sms;
+  const int groups = max(1, min(pl.tc_groups, (share + pl.tc_lanes / 2) / pl.tc_lanes));
+  Split s;
+  s.per = max(pl.tc_per, (total + groups - 1) / groups);
+  s.left = pl.sms - (total + s.per - 1) / s.per * pl.tc_lanes;
+  if (share == pl.sms || 4 * s.left < 3 * (pl.sms - share)) s.left = 0;
+  return s;
 }
 
 struct AttnArgs {

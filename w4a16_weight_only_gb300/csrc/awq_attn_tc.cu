@@ -237,7 +237,7 @@ __global__ void __maxnreg__(kRegs) attn_prefix_kernel(const __grid_constant__ Tc
   int64_t own = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) own += own_steps[w];
-  const int per = tc_steps_per_group(pl, p.kv.heads, own * pl.private_tiles);
+  const int per = split_sms(pl, p.kv.heads, own * pl.private_tiles, static_cast<int64_t>(p.B) * pl.private_tiles).per;
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.tc_per = per;
 
   // Bounded waits; a role that gives up sets the flag, and the others leave at their next wait.
