@@ -115,6 +115,7 @@ def test_attention(awq, case, dtype):
     (75, 2, 32, 8, 128, 4097, 100, 32),
     (130, 1, 16, 16, 96, 3000, 33, 24),    # pages that no TMA box divides
     (64, 1, 64, 8, 128, 5000, 50, 128),
+    (48, 1, 8, 2, 128, 300, 3000, 16),     # own keys outweigh the prefix: most SMs stream
 ])
 def test_many_rows(awq, B, n, hq, hkv, D, prefix, private, page, dtype):
     g = torch.Generator(device="cuda").manual_seed(B)

@@ -80,13 +80,14 @@ struct Cursor {
   int len;
 };
 
-// Each warp works alone: it copies its own keys and values (cp.async into a ring, zero-filled past
-// the sequence's end: what lies there may be anything), keeps its own (m, l, o), and writes a part
-// when its unit or its share ends.  Its copies run ahead across units, so the memory system is busy
-// from the first step to the last; 2 blocks of 4 warps per SM keep about 140 KB per SM in flight.
-// HBM-bound: 128 sequences of 1024 own keys on average, 8 heads of 128, 537 MB in 95 us (5.6 TB/s); 64
-// of 512, 134 MB in 33 us, of which some 6 us are the reads of lengths, pages and queries before the
-// first key arrives.
+// Each warp works alone: it copies its own keys and values into a ring, keeps its own (m, l, o), and writes
+// a part when its unit or its share ends.  Pages of whole steps come by TMA, boxes of 16 tokens of 64
+// elements (kTma); other pages by cp.async, whole rows by all lanes (128 sequences as below: 192 and 199 us a
+// call, the kernels one after the other).  What follows a sequence's end may be anything: it is zero-filled.
+// The copies run ahead across units, so the memory system is busy from the first step to the last; 2 blocks
+// of 4 warps per SM keep about 130 KB per SM in flight.  HBM-bound on all SMs: 128 sequences of 1024 own keys
+// on average, 8 heads of 128, 537 MB in 90 us (5.9 TB/s).  On 40 SMs alone 151 us (3.6 TB/s), of which the
+// copies are 110: so it shares the SMs with the tensor-core kernel (split_sms).
 //
 // The products are taken transposed, S^T = K Q^T and O^T += V^T P^T: keys (then elements) fill the 16
 // rows of an m16n8k16 and 8 query rows its columns, so that the usual 8 heads of a group waste
@@ -642,10 +643,9 @@ Layout layout(const AttentionProblem& p, const Plan& pl) {
   return l;
 }
 
-// The kernel, set up (and where there is room run) while the one before it still runs; it waits for
-// that one's end itself.  Behind the tensor-core kernel (67 against 75 us for 64 sequences over 8197
-// keys, 200 against 208 for 128 over 32768); without it the launch attribute's host time is more than
-// what is saved (30.3 against 27.7 us a call for 3 over 1000).
+// The kernel, set up and where there is room run while the one before it still runs; it waits for that
+// one's end itself.  Behind the tensor-core kernel: the streaming kernel runs beside it.  Without it the
+// launch attribute's host time is more than what is saved (30.3 against 27.7 us a call for 3 over 1000).
 template <typename A>
 cudaError_t launch_early(void (*kernel)(A), unsigned blocks, int threads, size_t smem, cudaStream_t stream, const A& a, bool early) {
   cudaLaunchAttribute attr[1];

@@ -63,8 +63,8 @@ constexpr unsigned int kStatusAttnTimeout = 0x8u;
 // Tensor-core kernel (tc, the prefix's keys): row tiles of kTcRows rows per key/value head, steps of
 // kTcKeys keys.  The row tiles of a head go side by side, one block each (tc_lanes blocks, a group), so
 // that they read the same keys at the same time and HBM is read once; the steps of all heads form one
-// sequence of which group g takes [g per, (g + 1) per), per being found on the device.  (More row tiles than SMs: a group is one block,
-// and the steps of all heads' tiles form the sequence.)
+// sequence of which group g takes [g per, (g + 1) per), per being found on the device.  (More row tiles
+// than SMs: a group is one block, and the steps of all heads' tiles form the sequence.)
 //
 // Streaming kernel (the sequences' own keys, and the prefix's without tc): units are (sequence, row
 // tile), the prefix being a sequence of its own in front; a unit of L keys has ceil(L / kStreamKeys)
@@ -102,11 +102,12 @@ __host__ __device__ inline int tc_last_group(const Plan& pl, int u, int per) { r
 // the work, the streaming kernel on the others.  The lengths decide, so the device does.  A block's step of
 // the one takes some 1.66 us of an SM and its start and end as long as three more, a step of a head of the
 // other 0.11 us and a unit's start and end as long as two (heads of 128; fewer elements, less of both).  A
-// streaming kernel that would get fewer than a twelfth of the SMs comes after, on all.  Blocks of the tensor-core kernel beyond its
+// streaming kernel that would get fewer than a twelfth of the SMs comes after, on all (128 sequences of
+// up to 64 own keys over 32768: 109 us, 131 with 4 SMs).  Blocks of the tensor-core kernel beyond its
 // share leave at once; the streaming kernel's blocks are one wave on the SMs left, or, where whole groups
 // leave it much less than its share, as many as all SMs hold.  128 sequences of 1024 own keys over 32768
-// shared ones, 8 heads: 100 SMs and 52, SIDE us with the join; one after the other on all SMs 192 us; 64 of
-// 512 over 8197: SIDE2 and 67 us.
+// shared ones, 8 heads: some 100 SMs and 50, 149 us a call with the join; one after the other on all SMs 188
+// us; 64 of 512 over 8192: 52 and 61 us.
 constexpr int64_t kTcStepNs = 1660, kTcFixedSteps = 3, kStreamStepNs = 108, kStreamFixedSteps = 2;
 
 constexpr int kLeastShare = 12;

@@ -17,7 +17,8 @@
 // came from and is the MMA's A operand in TMEM; MMAs of one thread run in the order of issue, so the
 // next QK into S starts after the PV that reads P.
 //
-// 128 sequences of 64 / 8 heads over 32768 keys of 128, bf16: 137 GFLOP in 92 us, 1.49 PFLOP/s.  Bound
+// 128 sequences of 64 / 8 heads over 32768 keys of 128, bf16: 137 GFLOP in 92 us on all SMs, 1.49 PFLOP/s;
+// 138 us on 100 SMs beside the streaming kernel, the same per SM.  Bound
 // by the chain softmax - PV - QK of a half (about 1500 + 500 + 600 cycles of a step's 2900, the tensor
 // core's share of a step being 2050) and by the issue of the MMAs, each of which takes its thread about
 // as long as it runs.
