@@ -96,6 +96,13 @@ constexpr int kTcKeys = 128;
 // group takes `per`.
 __host__ __device__ inline int tc_unit(const Plan& pl, int hk, int tile) { return pl.tc_lanes > 1 ? hk : hk * pl.tc_tiles + tile; }
 __host__ __device__ inline int tc_first_group(const Plan& pl, int u, int per) { return u * pl.tc_steps / per; }
+// First of the steps of a group, `total` for a group beyond the last.  Blocks are launched for the least
+// steps a group can have; where the split leaves few groups, `per` is up to total (below 2^30) and the
+// product passes 32 bits for the groups beyond the last.
+__host__ __device__ inline int tc_first_step(int group, int per, int total) {
+  const int64_t first = static_cast<int64_t>(group) * per;
+  return first < total ? static_cast<int>(first) : total;
+}
 __host__ __device__ inline int tc_last_group(const Plan& pl, int u, int per) { return ((u + 1) * pl.tc_steps - 1) / per; }
 
 // The two kernels of a call with tc run side by side, the tensor-core kernel on as many SMs as its share of

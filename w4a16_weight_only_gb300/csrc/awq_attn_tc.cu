@@ -262,7 +262,7 @@ __global__ void __maxnreg__(kRegs) attn_prefix_kernel(const __grid_constant__ Tc
   // this block's steps, tile by tile
   const int total = p.kv.heads * (pl.tc_tiles / pl.tc_lanes) * pl.tc_steps;
   const int group = blockIdx.x / pl.tc_lanes, tile_lane = blockIdx.x - group * pl.tc_lanes;
-  const int s_begin = group * per, s_end = min(total, s_begin + per);  // none for a group beyond the last
+  const int s_begin = tc_first_step(group, per, total), s_end = min(total, s_begin + per);  // none for a group beyond the last
   const int stacked = p.B * p.n * pl.group;
   struct Segment {
     int hk, row0, halves, step0, steps, part;
