@@ -51,3 +51,18 @@ void test() {
     check(covered == (most < total ? most : total), "steps of all groups", covered);
   }
 }""")
+
+
+def test_the_join_stays_within_a_rows_slots(run):
+    # what an old workspace holds in place of a number of parts: an fp32 sum, a negative one, NaN, noise
+    run(r"""
+void test() {
+  const int found[] = {0, 1, 5, 6, 7, 1 << 20, 0x4f3a1200, 0x7fffffff, -1, -7, static_cast<int>(0x80000000u),
+                       static_cast<int>(0xc1200000u), 0x7fc00000};
+  for (int most : {0, 1, 6, 4096})
+    for (int count : found) {
+      const int got = parts_within(count, most);
+      check(got >= 0 && got <= most, "parts", got);
+      if (count >= 0 && count <= most) check(got == count, "parts that were written", got);
+    }
+}""")

@@ -518,11 +518,13 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
     } else {
       first = a.counts[stacked / pl.tile * p.kv.heads + hk];
     }
+    first = parts_within(first, pl.prefix_parts);
   }
   if (pl.private_parts && __ldg(p.lens + b) > 0) {
     const int own_row = (bi - b * p.n) * pl.group + h - hk * pl.group;
-    own = a.counts[pl.prefix_tiles * p.kv.heads +
-                   (static_cast<int64_t>(b) * pl.private_tiles + own_row / pl.tile) * p.kv.heads + hk];
+    own = parts_within(a.counts[pl.prefix_tiles * p.kv.heads +
+                                (static_cast<int64_t>(b) * pl.private_tiles + own_row / pl.tile) * p.kv.heads + hk],
+                       pl.private_parts);
   }
   const int parts = first + own, skip = pl.prefix_parts - first;
   const float2* ml = a.part_ml + static_cast<int64_t>(r) * pl.parts;

@@ -139,6 +139,10 @@ __device__ inline Split split_sms(const Plan& pl, int heads, int64_t own, int64_
   return s;
 }
 
+// A number of parts as the join uses it.  A streaming warp that gave up a wait has written none, and the
+// workspace may hold anything: whatever stands there, the join stays within the row's slots.
+__host__ __device__ inline int parts_within(int count, int most) { return count < 0 ? 0 : count < most ? count : most; }
+
 struct AttnArgs {
   AttentionProblem p;
   Plan plan;
