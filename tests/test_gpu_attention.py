@@ -342,3 +342,39 @@ def test_empty(awq):
     d = make(2, 1, 4, 2, 64, 40, [33, 20], 16, "fp16")
     d.update(q=d["q"][:0], pages=d["pages"][:0], lens=d["lens"][:0])
     assert awq.awq_attention_shared(**d).shape == (0, 1, 4, 64)
+
+
+# B, n, hq, hkv, D, prefix, lens, page, workspace's content; every call has streaming warps that wait, the last
+# two blocks of the prefix kernel with several steps as well
+GIVE_UPS = [
+    (2, 1, 8, 2, 128, 300, [40, 33], 16),
+    (3, 1, 4, 2, 64, 0, [200, 1, 90], 16),
+    (2, 20, 4, 4, 256, 64, [40, 64], 32),
+    (40, 1, 8, 1, 128, 128 * 900, [20] * 40, 64),
+    (70, 2, 8, 1, 64, 128 * 640 + 5, [50] * 70, 128),
+]
+
+
+@pytest.mark.parametrize("word", [0x4f3a1200, 0x7fffffff, -1, -(1 << 31)])
+@pytest.mark.parametrize("case", range(len(GIVE_UPS)))
+def test_waits_that_give_up_are_reported(awq, case, word):
+    # nothing arrives in time: an error status, whatever the workspace held, and the next call is right
+    B, n, hq, hkv, D, prefix, lens, page = GIVE_UPS[case]
+    g = torch.Generator(device="cuda").manual_seed(case)
+    shared, per = -(-prefix // page), -(-max(lens) // page)
+    order = torch.randperm(shared + B * per, generator=g, device="cuda", dtype=torch.int32)
+    k, v = (torch.randn((order.numel(), page, hkv, D), generator=g, device="cuda").half() for _ in range(2))
+    d = dict(q=torch.randn((B, n, hq, D), generator=g, device="cuda").half(), k_cache=k, v_cache=v, prefix_pages=order[:shared],
+             prefix_len=prefix, pages=order[shared:].view(B, per), lens=torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    want = awq.awq_attention_shared(**d)
+    size = awq.awq_attention_shared_workspace_size(B, n, hq, hkv, D, prefix, per * page)
+    workspace = torch.full((-(-size // 4),), word, dtype=torch.int32, device="cuda").view(torch.uint8)
+    awq.device_status()
+    awq.selftest_attention_give_up(True)
+    try:
+        awq.awq_attention_shared(**d, workspace=workspace)
+    finally:
+        awq.selftest_attention_give_up(False)
+    with pytest.raises(awq.AwqError, match="bounded wait"):
+        awq.device_status()
+    assert torch.equal(awq.awq_attention_shared(**d, workspace=workspace), want)

@@ -10,7 +10,7 @@ from ._binding import (AwqError, AwqLinear, PATHS, awq_dequant, awq_dequant_w8, 
                        awq_gemm_w8, awq_quantize_rtn,
                        device_status,
                        last_error, load_library, runtime_available, select_path,
-                       selftest_wait_timeout)
+                       selftest_attention_give_up, selftest_wait_timeout)
 from ._layer import (awq_attention_shared, awq_attention_shared_workspace_size, awq_moe_combine, awq_moe_dispatch,
                      awq_moe_dispatch_workspace_size, awq_moe_route, awq_rope, awq_rope_append, awq_rope_table)
 
@@ -20,7 +20,8 @@ __all__ = ["AwqError", "AwqLinear", "PATHS", "awq_dequant", "awq_dequant_w8", "a
            "awq_gemm_w8", "awq_quantize_rtn",
            "device_status",
            "last_error",
-           "load_library", "runtime_available", "select_path", "selftest_wait_timeout",
+           "load_library", "runtime_available", "select_path", "selftest_attention_give_up",
+           "selftest_wait_timeout",
            "awq_rope_table", "awq_rope", "awq_rope_append", "awq_attention_shared",
            "awq_attention_shared_workspace_size", "awq_moe_route", "awq_moe_dispatch",
            "awq_moe_dispatch_workspace_size", "awq_moe_combine"]

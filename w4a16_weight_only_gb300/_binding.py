@@ -44,6 +44,7 @@ SIGNATURES = {
     "awq_gemm_select_path_ex": (_i32, [_i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32]),
     "awq_device_status": (_i32, [_vp]),
     "awq_selftest_wait_timeout": (_i32, [ctypes.c_uint64, _vp]),
+    "awq_selftest_attention_give_up": (_i32, [_i32]),
     "awq_quantize_rtn": (_i32, [_vp, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp]),
     "awq_gemm_bf16": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp]),
     "awq_gemm_bf16_ex": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _i32, _vp]),
@@ -458,6 +459,11 @@ def device_status(stream=None):
 def selftest_wait_timeout(limit_ns=2_000_000, stream=None):
     """Launch the bounded-wait self test (awq.h); the next device_status() raises AwqError."""
     _check(load_library().awq_selftest_wait_timeout(int(limit_ns), _stream(stream)))
+
+
+def selftest_attention_give_up(on):
+    """Let this thread's awq_attention_shared calls give up their kernels' waits (awq.h), or wait again."""
+    _check(load_library().awq_selftest_attention_give_up(1 if on else 0))
 
 
 def awq_repack_size(K, N, group_size=128, bits=4) -> int:

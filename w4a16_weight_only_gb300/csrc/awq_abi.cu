@@ -12,6 +12,7 @@
 namespace {
 
 thread_local std::string g_err;
+thread_local bool g_attention_gives_up = false;  // awq_selftest_attention_give_up
 
 awq_status_t fail(awq_status_t st, const char* fmt, ...) {
   char buf[512];
@@ -664,6 +665,11 @@ awq_status_t awq_selftest_wait_timeout(uint64_t limit_ns, awq_stream_t stream) {
   return ok();
 }
 
+awq_status_t awq_selftest_attention_give_up(int on) {
+  g_attention_gives_up = on != 0;
+  return ok();
+}
+
 // ------------------------------------------------ operators between a layer's linears ----
 
 namespace {
@@ -903,6 +909,7 @@ awq_status_t awq_attention_shared(const void* q, int64_t B, int64_t n, int64_t H
   p.scale = scale;
   p.out = static_cast<uint16_t*>(out);
   p.bf16 = dtype == AWQ_DTYPE_BF16;
+  p.give_up = g_attention_gives_up;
   p.workspace = workspace;
   p.stream = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = awq::launch_attention(p, sms);

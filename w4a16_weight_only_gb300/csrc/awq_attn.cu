@@ -287,14 +287,17 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D, kTma>::BLOCKS) at
   };
 
   // Step `used` has arrived.  A bounded wait: one that gives up sets the status word, and the warp leaves
-  // once its copies in flight have landed (waiting for each a bounded time too).
+  // once its copies in flight have landed (waiting for each a bounded time too).  The clock is read before
+  // the test that decides, so that a pause between the two (a context switch) gives nothing up.
   const auto arrived = [&](uint32_t used) -> bool {
     const auto there = [&] { return __all_sync(0xffffffffu, mbar_try_wait(&full[used % STAGES], (used / STAGES) & 1u)) != 0; };
     if (there()) return true;
     const uint64_t t0 = globaltimer_ns();
-    while (!there())
-      if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > kWaitLimitNs)) return false;
-    return true;
+    while (true) {
+      const bool late = __any_sync(0xffffffffu, globaltimer_ns() - t0 > kWaitLimitNs);
+      if (there()) return true;
+      if (late) return false;
+    }
   };
   uint32_t used = 0;  // steps
   bool gave_up = false;
@@ -337,7 +340,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, Stream<D, kTma>::BLOCKS) at
       uint16_t* st = ring + used % STAGES * ST::STEP;
       const uint32_t ks = smem_u32(st), vs = ks + ST::HALF * 2;
       if constexpr (kTma) {
-        if (!arrived(used)) {
+        if (p.give_up || !arrived(used)) {
           gave_up = true;
           break;
         }

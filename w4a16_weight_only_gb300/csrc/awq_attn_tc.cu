@@ -242,20 +242,23 @@ __global__ void __maxnreg__(kRegs) attn_prefix_kernel(const __grid_constant__ Tc
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.tc_per = per;
 
   // Bounded waits; a role that gives up sets the flag, and the others leave at their next wait.
-  // All lanes of a warp wait together and get one answer.
-  const auto gave_up = [&](uint64_t t0) -> bool {
-    if (*abort_flag) return true;
-    if (globaltimer_ns() - t0 <= kWaitLimitNs) return false;
+  // All lanes of a warp wait together and get one answer.  The clock is read before the test that
+  // decides, so that a pause between the two (a context switch) gives nothing up.
+  const auto give_up = [&] {
     atomicOr(a.status, kStatusAttnTimeout);
     *abort_flag = 1u;
-    return true;
   };
   const auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     const uint64_t t0 = globaltimer_ns();
     while (true) {
+      const bool late = globaltimer_ns() - t0 > kWaitLimitNs;
       if (__all_sync(0xffffffffu, mbar_try_wait_hint(bar, parity, AWQ_MBAR_SUSPEND_HINT_NS))) return true;
-      if (__any_sync(0xffffffffu, gave_up(t0))) return false;
+      if (__any_sync(0xffffffffu, *abort_flag != 0u)) return false;
+      if (__any_sync(0xffffffffu, late)) {
+        give_up();
+        return false;
+      }
     }
   };
 
@@ -448,7 +451,10 @@ __global__ void __maxnreg__(kRegs) attn_prefix_kernel(const __grid_constant__ Tc
         at += sg.steps;
         for (int j = 0; j < sg.steps; ++j, item += 2) {
           const int key0 = (sg.step0 + j) * kTcKeys;
-          if (item >= kSlots && !wait(&empty[item % kSlots], (item / kSlots - 1) & 1u)) return;
+          if (item >= kSlots) {
+            if (p.give_up) return give_up();
+            if (!wait(&empty[item % kSlots], (item / kSlots - 1) & 1u)) return;
+          }
           uint8_t* tile = smem + SH::RING_OFF + (item % kSlots) * SH::TILE;
           if (a.tma && key0 + kTcKeys <= p.prefix_len) {
             // whole step: one box of 64 elements per panel and run of tokens within a page
@@ -508,13 +514,13 @@ __global__ void __maxnreg__(kRegs) attn_prefix_kernel(const __grid_constant__ Tc
     }();
     cp_async_wait<0>();
     if (pending != ~0u) hand_over(pending);
-    if (*abort_flag) {  // no copy may outlive the block: wait, a bounded time, for the last of each slot
-      static_assert(kSlots % 2 == 0, "a warp's copies alternate between kSlots / 2 slots");
-      const uint64_t t0 = globaltimer_ns();
-      for (uint32_t d = 2; d <= kSlots && item >= d; d += 2) {
-        const uint32_t i = item - d;
-        while (!mbar_try_wait(&full[i % kSlots], (i / kSlots) & 1u) && globaltimer_ns() - t0 < kWaitLimitNs) {
-        }
+    // No copy may outlive the block, and another role may give up after this one has issued its last: wait, a
+    // bounded time, for the last of each slot (in a run to the end the products have waited for them anyway).
+    static_assert(kSlots % 2 == 0, "a warp's copies alternate between kSlots / 2 slots");
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t d = 2; d <= kSlots && item >= d; d += 2) {
+      const uint32_t i = item - d;
+      while (!mbar_try_wait(&full[i % kSlots], (i / kSlots) & 1u) && globaltimer_ns() - t0 < kWaitLimitNs) {
       }
     }
   } else if (warp == 10) {

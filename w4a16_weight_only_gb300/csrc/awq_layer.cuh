@@ -101,6 +101,7 @@ struct AttentionProblem {
   float scale;
   uint16_t* out;  // [B, n, Hq, D]
   bool bf16;
+  bool give_up;  // self test: the kernels' bounded waits give up at once
   void* workspace;
   cudaStream_t stream;
 };
