@@ -133,6 +133,35 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _current(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+# the same without building a Stream object (1.1 us), where this PyTorch has it
+_current = getattr(torch._C, "_cuda_getCurrentRawStream", _current)
+
+
+def _allocating_for(handle, device):
+    """Context in which PyTorch allocates for the stream of this handle."""
+    return torch.cuda.stream(torch.cuda.ExternalStream(handle, device=device) if handle
+                             else torch.cuda.default_stream(device))
+
+
+def _empty(shape, dtype, device, stream=None):
+    """torch.empty for what a call on ``stream`` (an object, a handle, or None: the current one) writes.
+    PyTorch hands a freed block to the next allocation on its stream at once, so memory that another
+    stream writes has to come from that stream's blocks; the current one is recorded as a user too, since
+    the caller may read the tensor and drop it there."""
+    if stream is not None:
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        if handle != _current(device):
+            with _allocating_for(handle, device):
+                t = torch.empty(shape, dtype=dtype, device=device)
+            t.record_stream(torch.cuda.current_stream(device))
+            return t
+    return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _cuda_index(t, name):
     d = t.get_device()
     if d < 0:
@@ -185,7 +214,7 @@ def awq_gemm(x, qweight, qzeros, scales, bias=None, group_size=128, out=None, pa
     if bias is not None:
         _need(bias, "bias", dt, (N,), dev)
     if out is None:
-        out = torch.empty((M, N), dtype=dt, device=dev)
+        out = _empty((M, N), dt, dev, stream)
     else:
         _need(out, "out", dt, (M, N), dev)
     st = lib.awq_gemm_any(_ptr(x2), _ptr(qweight), _ptr(qzeros), _ptr(scales), _ptr(bias),
@@ -274,7 +303,7 @@ class AwqLinear:
             raise ValueError(f"x must be a contiguous [..., {K}] tensor, got {tuple(shape)}")
         M = x.numel() // K
         if out is None:
-            out = torch.empty(shape[:-1] + (N,), dtype=dt, device=x.device)
+            out = _empty(shape[:-1] + (N,), dt, self.device, stream)
         elif (out.dtype is not dt or out.get_device() != self.device or out.shape[-1] != N
               or out.numel() != M * N or not out.is_contiguous()):
             raise ValueError(f"out must be a contiguous {dt} [..., {N}] tensor of {M} rows "
@@ -322,7 +351,7 @@ def awq_gemm_w8(x, qweight, qzeros, scales, bias=None, group_size=128, out=None,
     if bias is not None:
         _need(bias, "bias", torch.float16, (N,), dev)
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float16, device=dev)
+        out = _empty((M, N), torch.float16, dev, stream)
     else:
         _need(out, "out", torch.float16, (M, N), dev)
     st = lib.awq_gemm_any(_ptr(x2), _ptr(qweight), _ptr(qzeros), _ptr(scales), _ptr(bias),
@@ -344,7 +373,7 @@ def awq_dequant_w8(qweight, qzeros, scales, group_size=128, out_dtype=torch.floa
     _need(scales, "scales", torch.float16, (ng, N), dev)
     if out_dtype not in (torch.float16, torch.float32):
         raise TypeError("out_dtype must be torch.float16 or torch.float32")
-    out = torch.empty((K, N), dtype=out_dtype, device=dev)
+    out = _empty((K, N), out_dtype, dev, stream)
     st = lib.awq_dequant_w8(_ptr(qweight), _ptr(qzeros), _ptr(scales), K, N, group_size, _ptr(out),
                             DTYPE_F32 if out_dtype == torch.float32 else DTYPE_F16, _stream(stream))
     _check(st)
@@ -371,7 +400,7 @@ def awq_gemm_grouped(x, qweight, qzeros, scales, offsets, bias=None, group_size=
     if bias is not None:
         _need(bias, "bias", torch.float16, (E, N), dev)
     if out is None:
-        out = torch.empty((R, N), dtype=torch.float16, device=dev)
+        out = _empty((R, N), torch.float16, dev, stream)
     else:
         _need(out, "out", torch.float16, (R, N), dev)
     st = lib.awq_gemm_grouped(_ptr(x), _ptr(qweight), _ptr(qzeros), _ptr(scales), _ptr(bias),
@@ -399,7 +428,7 @@ def awq_dequant(qweight, qzeros, scales, group_size=128, out_dtype=torch.float16
     if out_dtype not in (half, torch.float32):
         raise TypeError(f"out_dtype must be {half} or torch.float32")
     if out is None:
-        out = torch.empty((K, N), dtype=out_dtype, device=dev)
+        out = _empty((K, N), out_dtype, dev, stream)
     else:
         _need(out, "out", out_dtype, (K, N), dev)
     if bf:
@@ -425,9 +454,9 @@ def awq_quantize_rtn(w, group_size=128, sym=False, out=None, stream=None):
     _need(w, "w", torch.float16, (N, K), dev)
     ng = _groups(K, group_size)
     if out is None:
-        qweight = torch.empty((K, N // 8), dtype=torch.int32, device=dev)
-        qzeros = torch.empty((ng, N // 8), dtype=torch.int32, device=dev)
-        scales = torch.empty((ng, N), dtype=torch.float16, device=dev)
+        qweight = _empty((K, N // 8), torch.int32, dev, stream)
+        qzeros = _empty((ng, N // 8), torch.int32, dev, stream)
+        scales = _empty((ng, N), torch.float16, dev, stream)
     else:
         qweight, qzeros, scales = out
         _need(qweight, "qweight", torch.int32, (K, N // 8), dev)
@@ -493,7 +522,7 @@ def awq_repack(qweight, qzeros, scales, group_size=128, out=None, stream=None, b
     _need(scales, "scales", scales.dtype, (ng, N), dev)
     words = awq_repack_size(K, N, group_size, bits) // 4
     if out is None:
-        out = torch.empty((words,), dtype=torch.int32, device=dev)
+        out = _empty((words,), torch.int32, dev, stream)
     else:
         _need(out, "out", torch.int32, (words,), dev)
     f = lib.awq_repack_w8 if bits == 8 else lib.awq_repack
@@ -518,7 +547,7 @@ def packed_workspace(device, stream_handle):
     key = (int(device), int(stream_handle))
     ws = _workspaces.get(key)
     if ws is None:
-        with torch.cuda.device(int(device)):
+        with _allocating_for(key[1], key[0]):  # zeros in the stream's order, before the call
             ws = torch.zeros((awq_gemm_packed_workspace_size(),), dtype=torch.uint8, device=int(device))
         _workspaces[key] = ws
     return ws
@@ -549,7 +578,7 @@ def awq_gemm_packed(x, packed, bias, K, N, group_size=128, out=None, stream=None
     if bias is not None:
         _need(bias, "bias", dt, (N,), dev)
     if out is None:
-        out = torch.empty((M, N), dtype=dt, device=dev)
+        out = _empty((M, N), dt, dev, stream)
     else:
         _need(out, "out", dt, (M, N), dev)
     sh = _stream(stream)
@@ -593,7 +622,7 @@ def awq_gemm_packed_noalloc(x, packed, bias, K, N, group_size=128, out=None, str
     if bias is not None:
         _need(bias, "bias", torch.float16, (N,), dev)
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float16, device=dev)
+        out = _empty((M, N), torch.float16, dev, stream)
     else:
         _need(out, "out", torch.float16, (M, N), dev)
     _check(lib.awq_gemm_packed_noalloc(_ptr(x2), _ptr(packed), _ptr(bias), M, K, N, group_size, _ptr(out),
@@ -608,7 +637,7 @@ def awq_repack_experts(qweight, qzeros, scales, group_size=128, stream=None):
     E, K, C = qweight.shape
     N = 8 * C
     words = awq_repack_size(K, N, group_size) // 4
-    out = torch.empty((E * words,), dtype=torch.int32, device=qweight.device)
+    out = _empty((E * words,), torch.int32, _cuda_index(qweight, "qweight"), stream)
     for e in range(E):
         awq_repack(qweight[e], qzeros[e], scales[e], group_size, out=out[e * words:(e + 1) * words],
                    stream=stream)
@@ -636,7 +665,7 @@ def awq_gemm_packed_grouped(x, packed, offsets, K, N, bias=None, group_size=128,
     if bias is not None:
         _need(bias, "bias", dt, (E, N), dev)
     if out is None:
-        out = torch.empty((R, N), dtype=dt, device=dev)
+        out = _empty((R, N), dt, dev, stream)
     else:
         _need(out, "out", dt, (R, N), dev)
     _check(lib.awq_gemm_packed_grouped(_ptr(x), _ptr(packed), _ptr(bias), _ptr(offsets), R, E, K, N,

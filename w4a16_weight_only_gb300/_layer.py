@@ -9,8 +9,8 @@ import math
 import torch
 
 from . import _binding
-from ._binding import (AWQ_OK, DTYPE_BF16, DTYPE_F16, DTYPE_F32, AwqError, PagedKV, _cuda_index, _need, last_error,
-                       load_library)
+from ._binding import (AWQ_OK, DTYPE_BF16, DTYPE_F16, DTYPE_F32, AwqError, PagedKV, _allocating_for, _cuda_index, _current,
+                       _empty, _need, last_error, load_library)
 
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "banded": 4}
 _DTYPES = {torch.float16: DTYPE_F16, torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
@@ -25,14 +25,6 @@ _scratch = {}
 # 19 and 28 with a helper call per tensor).
 _half_dtypes = (torch.float16, torch.bfloat16)
 _i32, _f32 = torch.int32, torch.float32
-
-
-def _current(device):
-    return torch.cuda.current_stream(device).cuda_stream
-
-
-# the same without building a Stream object (1.1 us), where this PyTorch has it
-_current = getattr(torch._C, "_cuda_getCurrentRawStream", _current)
 
 
 def _handle(stream, device):
@@ -57,7 +49,8 @@ def scratch(device, handle, nbytes):
         kept = _scratch[(device, handle)] = []
     if not kept or kept[-1][1] < nbytes:
         size = (max(nbytes, 2 * kept[-1][1] if kept else 0) + _GRANULE - 1) // _GRANULE * _GRANULE
-        t = torch.empty((size,), dtype=torch.uint8, device=device)
+        with _allocating_for(handle, device):
+            t = torch.empty((size,), dtype=torch.uint8, device=device)
         kept.append((t.data_ptr(), size, t))
     return kept[-1]
 
@@ -122,7 +115,10 @@ def awq_rope_table(max_position, rotary_dim, base=10000.0, scaling="none", facto
     if attention_factor is None:
         attention_factor = 0.1 * math.log(factor) + 1.0 if scaling == "yarn" and factor > 1 else 1.0
     if out is None:
-        out = torch.empty((max_position, rotary_dim), dtype=torch.float32, device="cuda" if device is None else device)
+        where = torch.device("cuda" if device is None else device)
+        if where.type != "cuda":
+            raise ValueError(f"device must be a CUDA device, got {where}")
+        out = _empty((max_position, rotary_dim), _f32, torch.cuda.current_device() if where.index is None else where.index, stream)
     dev = _cuda_index(out, "out")
     _need(out, "out", torch.float32, (max_position, rotary_dim), dev)
     p0, p1 = (low_factor, high_factor) if scaling == "banded" else (beta_fast, beta_slow)
@@ -167,8 +163,8 @@ def awq_rope(q, k, positions, table, interleaved=False, q_out=None, k_out=None, 
     rest.  Pairs are (i, i + rotary_dim / 2), or (2 i, 2 i + 1) with interleaved=True.  Returns
     (q_out, k_out), dense, or written in place where q_out is q (k_out is k)."""
     dt, dev, (T, Hq, D), Hkv, (last, rot) = _rope_inputs(q, k, positions, table)
-    q_out = torch.empty((T, Hq, D), dtype=dt, device=dev) if q_out is None else _dense_or_same(q_out, q, "q_out", dt, dev)
-    k_out = torch.empty((T, Hkv, D), dtype=dt, device=dev) if k_out is None else _dense_or_same(k_out, k, "k_out", dt, dev)
+    q_out = _empty((T, Hq, D), dt, dev, stream) if q_out is None else _dense_or_same(q_out, q, "q_out", dt, dev)
+    k_out = _empty((T, Hkv, D), dt, dev, stream) if k_out is None else _dense_or_same(k_out, k, "k_out", dt, dev)
     st = _library().awq_rope(q.data_ptr(), k.data_ptr(), positions.data_ptr(), table.data_ptr(), T, Hq, Hkv, D, rot, last,
                              q.stride(0), q.stride(1), k.stride(0), k.stride(1), q_out.data_ptr(), k_out.data_ptr(),
                              1 if interleaved else 0, _DTYPES[dt], _handle(stream, dev))
@@ -188,7 +184,7 @@ def awq_rope_append(q, k, v, positions, table, k_cache, v_cache, slots, interlea
         _heads(v, "v", dt, (T, Hkv, D), dev)
         _need(slots, "slots", _i32, (T,), dev)
     cache = _cache(k_cache, v_cache, dt, Hkv, D, dev)
-    q_out = torch.empty((T, Hq, D), dtype=dt, device=dev) if q_out is None else _dense_or_same(q_out, q, "q_out", dt, dev)
+    q_out = _empty((T, Hq, D), dt, dev, stream) if q_out is None else _dense_or_same(q_out, q, "q_out", dt, dev)
     st = _library().awq_rope_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), positions.data_ptr(), table.data_ptr(), T, Hq,
                                     Hkv, D, rot, last, q.stride(0), q.stride(1), k.stride(0), k.stride(1), v.stride(0),
                                     v.stride(1), q_out.data_ptr(), cache, slots.data_ptr(), 1 if interleaved else 0,
@@ -244,7 +240,7 @@ def awq_attention_shared(q, k_cache, v_cache, prefix_pages, prefix_len, pages, l
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = torch.empty(qs, dtype=dt, device=dev)
+        out = _empty(qs, dt, dev, stream)
     else:
         _need(out, "out", dt, qs, dev)
     handle, lib = _handle(stream, dev), _library()
@@ -290,8 +286,8 @@ def awq_moe_route(logits, topk, scoring="softmax", bias=None, groups=1, topk_gro
     if bias is not None:
         _need(bias, "bias", _f32, (E,), dev)
     if out is None:
-        weights = torch.empty((T, topk), dtype=_f32, device=dev)
-        experts = torch.empty((T, topk), dtype=_i32, device=dev)
+        weights = _empty((T, topk), _f32, dev, stream)
+        experts = _empty((T, topk), _i32, dev, stream)
     else:
         weights, experts = out
         _need(weights, "weights", _f32, (T, topk), dev)
@@ -324,9 +320,9 @@ def awq_moe_dispatch(x, experts, num_experts, out=None, stream=None, workspace=N
         _need(experts, "experts", _i32, (xs[0], es[1]), dev)
     (T, W), k = xs, es[1]
     if out is None:
-        routed = torch.empty((T * k, W), dtype=dt, device=dev)
-        offsets = torch.empty((num_experts + 1,), dtype=_i32, device=dev)
-        rows = torch.empty((T, k), dtype=_i32, device=dev)
+        routed = _empty((T * k, W), dt, dev, stream)
+        offsets = _empty((num_experts + 1,), _i32, dev, stream)
+        rows = _empty((T, k), _i32, dev, stream)
     else:
         routed, offsets, rows = out
         _need(routed, "routed", dt, (T * k, W), dev)
@@ -372,7 +368,7 @@ def awq_moe_combine(y, weights, rows, base=None, out=None, stream=None):
     if base is not None:
         _need(base, "base", dt, (T, W), dev)
     if out is None:
-        out = torch.empty((T, W), dtype=dt, device=dev)
+        out = _empty((T, W), dt, dev, stream)
     else:
         _need(out, "out", dt, (T, W), dev)
     st = _library().awq_moe_combine(y.data_ptr(), R, W, weights.data_ptr(), rows.data_ptr(), T, k,
