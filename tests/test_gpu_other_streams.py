@@ -48,6 +48,7 @@ def calls(awq):
     stacked = [t[None].repeat(2, *[1] * t.dim()) for t in w]
     offsets = torch.tensor([0, 200, 512], dtype=torch.int32, device="cuda")
     dense = rand(4096, 2048)
+    wide = [t.repeat(1, 4) for t in w]
     return {
         "awq_rope": lambda **s: awq.awq_rope(q, k, pos, table, **s),
         "awq_rope_append": lambda **s: (awq.awq_rope_append(q, k, v, pos, table, *cache, slots, **s),),
@@ -67,7 +68,7 @@ def calls(awq):
         "awq_dequant": lambda **s: (awq.awq_dequant(*w, **s),),
         "awq_dequant_w8": lambda **s: (awq.awq_dequant_w8(*w8, **s),),
         "awq_quantize_rtn": lambda **s: awq.awq_quantize_rtn(dense, **s)[:1],
-        "awq_repack": lambda **s: (awq.awq_repack(*[t.repeat(1, 4) for t in w], **s),),
+        "awq_repack": lambda **s: (awq.awq_repack(*wide, **s),),
     }
 
 
