@@ -3,8 +3,10 @@ attention over a paged cache with a shared prefix, expert routing, dispatch and 
 marshalling only, as in _binding.py: every step of the computation runs in the library's kernels."""
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
+import threading
 
 import torch
 
@@ -38,27 +40,30 @@ def _library():
 
 
 def scratch(device, handle, nbytes):
-    """(address, bytes, tensor) of a workspace of at least ``nbytes`` that this module's calls on (device,
-    stream) share:
-    calls on one stream never overlap, and no call reads what an earlier one left.  It grows by
+    """(address, bytes, tensor, lock) of a workspace of at least ``nbytes`` that this module's calls on
+    (device, stream) share: kernels of one stream run in the order of their launches, and no call reads
+    what an earlier one left.  A call of several launches holds the lock while it enqueues them, since
+    another host thread's launches on the stream must not come between.  The workspace grows by
     allocation (at least doubling) and a smaller one is kept, since a captured CUDA graph may hold its
     address; make a stream's largest call once before capturing.  A graph keeps the workspace of the
     stream that captured it: replayed beside other calls of that stream, it needs a workspace of its own."""
-    kept = _scratch.get((device, handle))
-    if kept is None:
-        kept = _scratch[(device, handle)] = []
-    if not kept or kept[-1][1] < nbytes:
-        size = (max(nbytes, 2 * kept[-1][1] if kept else 0) + _GRANULE - 1) // _GRANULE * _GRANULE
-        with _allocating_for(handle, device):
-            t = torch.empty((size,), dtype=torch.uint8, device=device)
-        kept.append((t.data_ptr(), size, t))
-    return kept[-1]
+    lock, kept = _scratch.get((device, handle)) or _scratch.setdefault((device, handle), (threading.Lock(), []))
+    with lock:
+        if not kept or kept[-1][1] < nbytes:
+            size = (max(nbytes, 2 * kept[-1][1] if kept else 0) + _GRANULE - 1) // _GRANULE * _GRANULE
+            with _allocating_for(handle, device):
+                t = torch.empty((size,), dtype=torch.uint8, device=device)
+            kept.append((t.data_ptr(), size, t, lock))
+        return kept[-1]
+
+
+_no_lock = contextlib.nullcontext()  # calls that share a workspace given by the caller: the caller keeps them apart
 
 
 def _given(workspace, device, name):
     if workspace.dtype is not torch.uint8 or workspace.get_device() != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous uint8 tensor on {name}'s device")
-    return workspace.data_ptr(), workspace.numel(), workspace
+    return workspace.data_ptr(), workspace.numel(), workspace, _no_lock
 
 
 def _half(t, name):
@@ -250,9 +255,10 @@ def awq_attention_shared(q, k_cache, v_cache, prefix_pages, prefix_len, pages, l
         ws = scratch(dev, handle, need.value)
     else:
         ws = _given(workspace, dev, "q")
-    st = lib.awq_attention_shared(q.data_ptr(), B, n, Hq, sb, sn, sh, cache, prefix_pages.data_ptr(), prefix_len,
-                                  pages.data_ptr(), ps[1], pages.stride(0), lens.data_ptr(), max_len, scale, out.data_ptr(),
-                                  _DTYPES[dt], ws[0], ws[1], handle)
+    with ws[3]:
+        st = lib.awq_attention_shared(q.data_ptr(), B, n, Hq, sb, sn, sh, cache, prefix_pages.data_ptr(), prefix_len,
+                                      pages.data_ptr(), ps[1], pages.stride(0), lens.data_ptr(), max_len, scale,
+                                      out.data_ptr(), _DTYPES[dt], ws[0], ws[1], handle)
     if st != AWQ_OK:
         raise AwqError(st, last_error())
     return out
@@ -335,8 +341,9 @@ def awq_moe_dispatch(x, experts, num_experts, out=None, stream=None, workspace=N
         ws = scratch(dev, handle, need.value)
     else:
         ws = _given(workspace, dev, "x")
-    st = lib.awq_moe_dispatch(x.data_ptr(), T, W, x.stride(0), experts.data_ptr(), k, num_experts, routed.data_ptr(),
-                              offsets.data_ptr(), rows.data_ptr(), ws[0], ws[1], handle)
+    with ws[3]:
+        st = lib.awq_moe_dispatch(x.data_ptr(), T, W, x.stride(0), experts.data_ptr(), k, num_experts, routed.data_ptr(),
+                                  offsets.data_ptr(), rows.data_ptr(), ws[0], ws[1], handle)
     if st != AWQ_OK:
         raise AwqError(st, last_error())
     return routed, offsets, rows
