@@ -29,6 +29,18 @@ _half_dtypes = (torch.float16, torch.bfloat16)
 _i32, _f32 = torch.int32, torch.float32
 
 
+# torch.cuda.current_device() without its check that CUDA is up: a tensor of it exists where this is asked
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _on_current(t, name):
+    """The device of a CUDA tensor, which has to be the current one: that is where the library launches."""
+    dev = _cuda_index(t, name)
+    if dev != _device():
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{_device()}: call under torch.cuda.device")
+    return dev
+
+
 def _handle(stream, device):
     if stream is None:
         return _current(device)
@@ -124,7 +136,7 @@ def awq_rope_table(max_position, rotary_dim, base=10000.0, scaling="none", facto
         if where.type != "cuda":
             raise ValueError(f"device must be a CUDA device, got {where}")
         out = _empty((max_position, rotary_dim), _f32, torch.cuda.current_device() if where.index is None else where.index, stream)
-    dev = _cuda_index(out, "out")
+    dev = _on_current(out, "out")
     _need(out, "out", torch.float32, (max_position, rotary_dim), dev)
     p0, p1 = (low_factor, high_factor) if scaling == "banded" else (beta_fast, beta_slow)
     _ok(load_library().awq_rope_table(out.data_ptr(), max_position, rotary_dim, base, ROPE_SCALINGS[scaling], factor,
@@ -135,13 +147,13 @@ def awq_rope_table(max_position, rotary_dim, base=10000.0, scaling="none", facto
 def _rope_inputs(q, k, positions, table):
     dt, dev = q.dtype, q.get_device()
     qs, ks, ts = q.shape, k.shape, table.shape
-    if not (dt in _half_dtypes and dev >= 0 and len(qs) == 3 and len(ks) == 3 and len(ts) == 2 and k.dtype is dt and
+    if not (dt in _half_dtypes and dev == _device() and len(qs) == 3 and len(ks) == 3 and len(ts) == 2 and k.dtype is dt and
             ks[0] == qs[0] and ks[2] == qs[2] and k.get_device() == dev and positions.dtype is _i32 and
             positions.shape == qs[:1] and positions.is_contiguous() and positions.get_device() == dev and
             table.dtype is _f32 and table.is_contiguous() and table.get_device() == dev and
             (qs[2] <= 1 or (q.stride(2) == 1 and k.stride(2) == 1))):
         _half(q, "q")
-        dev = _cuda_index(q, "q")
+        dev = _on_current(q, "q")
         if len(qs) != 3 or len(ks) != 3:
             raise ValueError("q and k must be [tokens, heads, head_dim]")
         if len(ts) != 2:
@@ -221,12 +233,12 @@ def awq_attention_shared(q, k_cache, v_cache, prefix_pages, prefix_len, pages, l
     else:
         raise ValueError("q must be [B, n, heads, head_dim] or [B, heads, head_dim]")
     ps = pages.shape
-    if not (dt in _half_dtypes and dev >= 0 and one == 1 and len(ps) == 2 and ps[0] == B and pages.dtype is _i32 and
+    if not (dt in _half_dtypes and dev == _device() and one == 1 and len(ps) == 2 and ps[0] == B and pages.dtype is _i32 and
             pages.get_device() == dev and (ps[1] <= 1 or pages.stride(1) == 1) and prefix_pages.dtype is _i32 and
             prefix_pages.dim() == 1 and prefix_pages.is_contiguous() and prefix_pages.get_device() == dev and
             lens.dtype is _i32 and lens.shape == (B,) and lens.is_contiguous() and lens.get_device() == dev):
         _half(q, "q")
-        dev = _cuda_index(q, "q")
+        dev = _on_current(q, "q")
         _heads(q, "q", dt, qs, dev)
         if len(ps) != 2 or pages.dtype is not _i32 or ps[0] != B:
             raise ValueError(f"pages must be an int32 [{B}, W] table, got {pages.dtype} {tuple(ps)}")
@@ -279,7 +291,7 @@ def awq_moe_route(logits, topk, scoring="softmax", bias=None, groups=1, topk_gro
     scores divided by their sum if renormalize, times scale.  Equal keys go to the lower index.  Returns
     (weights fp32 [T, topk], experts int32 [T, topk]), or fills ``out``, a tuple of those two."""
     dt, dev, shape = logits.dtype, logits.get_device(), logits.shape
-    if not (dt in _DTYPES and len(shape) == 2 and dev >= 0 and (logits.stride(1) == 1 or shape[1] <= 1) and
+    if not (dt in _DTYPES and len(shape) == 2 and dev == _device() and (logits.stride(1) == 1 or shape[1] <= 1) and
             scoring in ("softmax", "sigmoid")):
         if dt not in _DTYPES:
             raise TypeError(f"logits must be float16, bfloat16 or float32, got {dt}")
@@ -287,7 +299,7 @@ def awq_moe_route(logits, topk, scoring="softmax", bias=None, groups=1, topk_gro
             raise ValueError("logits must be [tokens, experts]")
         if scoring not in ("softmax", "sigmoid"):
             raise ValueError(f"scoring must be 'softmax' or 'sigmoid', got {scoring!r}")
-        _heads(logits, "logits", dt, shape, _cuda_index(logits, "logits"))
+        _heads(logits, "logits", dt, shape, _on_current(logits, "logits"))
     T, E = shape
     if bias is not None:
         _need(bias, "bias", _f32, (E,), dev)
@@ -315,13 +327,13 @@ def awq_moe_dispatch(x, experts, num_experts, out=None, stream=None, workspace=N
     rows of routed behind offsets[-1] are zero.  workspace: a uint8 device tensor of
     awq_moe_dispatch_workspace_size bytes (default: this module's for the stream)."""
     dt, dev, xs, es = x.dtype, x.get_device(), x.shape, experts.shape
-    if not (dt in _half_dtypes and dev >= 0 and len(xs) == 2 and len(es) == 2 and es[0] == xs[0] and
+    if not (dt in _half_dtypes and dev == _device() and len(xs) == 2 and len(es) == 2 and es[0] == xs[0] and
             (x.stride(1) == 1 or xs[1] <= 1) and experts.dtype is _i32 and experts.is_contiguous() and
             experts.get_device() == dev):
         _half(x, "x")
         if len(xs) != 2 or len(es) != 2:
             raise ValueError("x must be [tokens, width], experts [tokens, k]")
-        dev = _cuda_index(x, "x")
+        dev = _on_current(x, "x")
         _heads(x, "x", dt, xs, dev)
         _need(experts, "experts", _i32, (xs[0], es[1]), dev)
     (T, W), k = xs, es[1]
@@ -361,13 +373,13 @@ def awq_moe_combine(y, weights, rows, base=None, out=None, stream=None):
     W] fp16 or bf16, weights fp32 [T, k], rows int32 [T, k] (outside [0, R): left out), base [T, W] or
     None.  Returns [T, W]; out may be base."""
     dt, dev, ys, rs = y.dtype, y.get_device(), y.shape, rows.shape
-    if not (dt in _half_dtypes and dev >= 0 and len(ys) == 2 and len(rs) == 2 and y.is_contiguous() and rows.dtype is _i32 and
+    if not (dt in _half_dtypes and dev == _device() and len(ys) == 2 and len(rs) == 2 and y.is_contiguous() and rows.dtype is _i32 and
             rows.is_contiguous() and rows.get_device() == dev and weights.dtype is _f32 and weights.shape == rs and
             weights.is_contiguous() and weights.get_device() == dev):
         _half(y, "y")
         if len(ys) != 2 or len(rs) != 2:
             raise ValueError("y must be [rows, width], rows [tokens, k]")
-        dev = _cuda_index(y, "y")
+        dev = _on_current(y, "y")
         _need(y, "y", dt, ys, dev)
         _need(weights, "weights", _f32, rs, dev)
         _need(rows, "rows", _i32, rs, dev)
