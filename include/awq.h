@@ -495,7 +495,8 @@ awq_status_t awq_rope(const void* q, const void* k, const int32_t* positions, co
 
 /* A paged key/value cache: cell (page, token, head) of keys starts at element page * page_stride +
  * token * token_stride + head * head_stride of k, of values at the same element of v; head_dim
- * elements contiguous.  Slot s is token s % page_size of page s / page_size. */
+ * elements contiguous; the stride of a dimension of one entry is not looked at.  Slot s is token
+ * s % page_size of page s / page_size. */
 typedef struct awq_paged_kv {
   void* k;
   void* v;
@@ -538,7 +539,7 @@ awq_status_t awq_rope_append(const void* q, const void* k, const void* v, const 
  *   workspace: awq_attention_shared_workspace_size bytes (partial sums; same host values), 256-byte
  *   aligned; any content.  Calls that overlap in time need workspaces of their own.
  * Repeated calls give the same bits.  Requirements: q, the cache's tensors and out 16-byte aligned,
- * q's and the cache's strides multiples of 8; prefix_len and max_len <= 2^31 - 256, other sizes below
+ * q's and the cache's strides multiples of 8 (of dimensions of more than one entry); prefix_len and max_len <= 2^31 - 256, other sizes below
  * 2^31.
  */
 awq_status_t awq_attention_shared_workspace_size(int64_t B, int64_t n, int64_t Hq, int64_t heads,

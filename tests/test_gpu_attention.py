@@ -378,3 +378,23 @@ def test_waits_that_give_up_are_reported(awq, case, word):
     with pytest.raises(awq.AwqError, match="bounded wait"):
         awq.device_status()
     assert torch.equal(awq.awq_attention_shared(**d, workspace=workspace), want)
+
+
+def test_strides_of_single_entries_do_not_matter(awq):
+    # one sequence of one token inside rows of odd length; one head whose stride differs between keys and values
+    d = make(1, 1, 2, 1, 64, 50, [20], 16, "fp16", seed=21)
+    want = awq.awq_attention_shared(**d)
+    e = dict(d, q=d["q"].as_strided((1, 1, 2, 64), (131, 257, 64, 1)))
+    pages = d["k_cache"].shape[0]
+    e["v_cache"] = d["v_cache"].as_strided((pages, 16, 1, 64), (1024, 64, 1024, 1))
+    e["k_cache"] = d["k_cache"].as_strided((pages, 16, 1, 64), (1024, 64, 3, 1))
+    assert torch.equal(awq.awq_attention_shared(**e), want)
+    many = make(40, 1, 2, 1, 64, 300, [20] * 40, 16, "fp16", seed=22)  # the prefix on the tensor cores
+    want = awq.awq_attention_shared(**many)
+    pages = many["k_cache"].shape[0]
+    many["k_cache"] = many["k_cache"].as_strided((pages, 16, 1, 64), (1024, 64, 3, 1))
+    assert torch.equal(awq.awq_attention_shared(**many), want)
+    table, cache = awq.awq_rope_table(16, 64), torch.zeros((2, 2, 16, 1, 64), dtype=torch.float16, device="cuda")
+    k, slots = torch.randn((3, 1, 64), device="cuda").half(), torch.arange(3, dtype=torch.int32, device="cuda")
+    awq.awq_rope_append(k, k, k, slots, table, cache[0].as_strided((2, 16, 1, 64), (1024, 64, 5, 1)), cache[1], slots)
+    assert torch.equal(cache[1, 0, :3], k) and cache[0, 0, :3].any()

@@ -123,3 +123,19 @@ def test_dispatch_and_combine(lib):
     assert combine(R=-1) == INVALID and combine(k=1025) == INVALID and combine(y=None) == INVALID and combine(out=None) == INVALID
     assert combine(dtype=1) == INVALID and combine(rows=ODD) == MISALIGNED and combine(y=P(0x100001)) == MISALIGNED
     assert combine(R=1 << 31) == SHAPE
+
+
+def test_strides_of_single_entries_do_not_matter(lib):
+    # a dimension of one entry is never stepped along, whatever its stride
+    def call(B=2, n=2, Hq=4, strides=(512, 256, 64), **kv):
+        c = cache(**kv)
+        return lib.awq_attention_shared(A, B, n, Hq, *strides, ctypes.byref(c), A, 10, A, 2, 2, A, 2, 0.125, P(0x200000), 0, A, 1 << 30,
+                                        None)
+    assert call() == DEVICE
+    assert call(strides=(513, 256, 64)) == MISALIGNED and call(B=1, strides=(513, 256, 64)) == DEVICE
+    assert call(strides=(512, 257, 64)) == MISALIGNED and call(n=1, strides=(512, 257, 64)) == DEVICE
+    assert call(Hq=2, heads=1, strides=(512, 256, 65)) == MISALIGNED and call(Hq=1, heads=1, strides=(512, 256, 65)) == DEVICE
+    assert call(head_stride=65) == MISALIGNED and call(heads=1, head_stride=65) == DEVICE
+    assert call(token_stride=129) == MISALIGNED and call(page_size=1, token_stride=129) == DEVICE
+    assert call(page_stride=2049) == MISALIGNED and call(num_pages=1, page_stride=2049) == DEVICE
+    assert call(heads=1, head_stride=-1) == DEVICE and call(head_stride=-64) == INVALID

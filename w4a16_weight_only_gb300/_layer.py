@@ -109,7 +109,7 @@ def _cache(k_cache, v_cache, dt, heads, dim, device):
                              f"got shape {tuple(shape)}")
         _heads(k_cache, "k_cache", dt, shape, device)
         _heads(v_cache, "v_cache", dt, shape, device)
-        if v_cache.stride() != s:
+        if any(a != b for a, b, size in zip(v_cache.stride(), s, shape) if size > 1):
             raise ValueError("k_cache and v_cache must have the same strides")
     return PagedKV(k_cache.data_ptr(), v_cache.data_ptr(), *shape, s[0], s[1], s[2])
 

@@ -684,7 +684,11 @@ awq_status_t check_cache(const awq_paged_kv_t* c, awq::PagedKV* out) {
   if (!c) return fail(AWQ_ERR_INVALID_ARGUMENT, "null cache");
   if (c->num_pages < 0 || c->page_size <= 0 || c->heads <= 0 || c->head_dim <= 0)
     return fail(AWQ_ERR_INVALID_ARGUMENT, "cache: num_pages >= 0, page_size, heads, head_dim > 0 needed");
-  if (c->page_stride < 0 || c->token_stride < 0 || c->head_stride < 0)
+  // a dimension of one entry is never stepped along: its stride may be anything
+  const int64_t page_stride = c->num_pages > 1 ? c->page_stride : c->head_dim;
+  const int64_t token_stride = c->page_size > 1 ? c->token_stride : c->head_dim;
+  const int64_t head_stride = c->heads > 1 ? c->head_stride : c->head_dim;
+  if (page_stride < 0 || token_stride < 0 || head_stride < 0)
     return fail(AWQ_ERR_INVALID_ARGUMENT, "cache strides must not be negative");
   if (c->num_pages > kDimLimit || c->page_size > kDimLimit || c->heads > 65536 || c->head_dim > 65536 ||
       c->num_pages * c->page_size > kDimLimit)
@@ -693,7 +697,7 @@ awq_status_t check_cache(const awq_paged_kv_t* c, awq::PagedKV* out) {
   if (!al(c->k, 2) || !al(c->v, 2)) return fail(AWQ_ERR_MISALIGNED, "cache tensors must be 2-byte aligned");
   *out = {static_cast<uint16_t*>(c->k), static_cast<uint16_t*>(c->v), static_cast<int>(c->num_pages),
           static_cast<int>(c->page_size), static_cast<int>(c->heads), static_cast<int>(c->head_dim),
-          c->page_stride, c->token_stride, c->head_stride};
+          page_stride, token_stride, head_stride};
   return AWQ_OK;
 }
 
@@ -884,6 +888,9 @@ awq_status_t awq_attention_shared(const void* q, int64_t B, int64_t n, int64_t H
     return fail(AWQ_ERR_INVALID_ARGUMENT, "awq_attention_shared: null pointer");
   if (!al(q, 16) || !al(out, 16) || !al(p.kv.k, 16) || !al(p.kv.v, 16))
     return fail(AWQ_ERR_MISALIGNED, "q, out and the cache's tensors must be 16-byte aligned");
+  if (B == 1) q_batch_stride = 0;
+  if (n == 1) q_token_stride = 0;
+  if (Hq == 1) q_head_stride = 0;
   if (q_batch_stride % 8 || q_token_stride % 8 || q_head_stride % 8 || p.kv.page_stride % 8 || p.kv.token_stride % 8 ||
       p.kv.head_stride % 8)
     return fail(AWQ_ERR_MISALIGNED, "strides of q and the cache must be multiples of 8 elements");
