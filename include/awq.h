@@ -535,7 +535,7 @@ awq_status_t awq_rope_append(const void* q, const void* k, const void* v, const 
  *   W * page_size.  prefix_len, max_len are host values: the plan depends on them.
  * A row uses only the keys that it sees: what the cache holds past a length, or a newer token's value,
  * may be infinite or NaN.  A page outside [0, num_pages) gives unspecified values for its sequence.
- * A row that sees no key is zero.  B, n or Hq 0: AWQ_OK, no launch.
+ * A row that sees no key is zero; one whose logits are all -inf is NaN.  B, n or Hq 0: AWQ_OK, no launch.
  *   workspace: awq_attention_shared_workspace_size bytes (partial sums; same host values), 256-byte
  *   aligned; any content.  Calls that overlap in time need workspaces of their own.
  * Repeated calls give the same bits.  Requirements: q, the cache's tensors and out 16-byte aligned,

@@ -398,3 +398,26 @@ def test_strides_of_single_entries_do_not_matter(awq):
     k, slots = torch.randn((3, 1, 64), device="cuda").half(), torch.arange(3, dtype=torch.int32, device="cuda")
     awq.awq_rope_append(k, k, k, slots, table, cache[0].as_strided((2, 16, 1, 64), (1024, 64, 5, 1)), cache[1], slots)
     assert torch.equal(cache[1, 0, :3], k) and cache[0, 0, :3].any()
+
+
+@pytest.mark.parametrize("B,n,hq,hkv,D,prefix,lens,page", [
+    (3, 2, 4, 2, 64, 20, [2, 7, 40], 16),       # streamed
+    (2, 1, 8, 2, 128, 0, [9, 30], 7),
+    (40, 1, 4, 1, 128, 300, [10] * 40, 16),     # the prefix on the tensor cores
+    (2, 20, 4, 4, 256, 19, [40, 20], 16),
+])
+def test_rows_whose_logits_are_all_minus_infinity(awq, B, n, hq, hkv, D, prefix, lens, page):
+    # 0 / 0 by the definition, not the zero of a row that sees no key; one finite logit is enough
+    for dtype in ("fp16", "bf16"):
+        d = make(B, n, hq, hkv, D, prefix, lens, page, dtype, seed=17)
+        d["q"][..., 0] = 1.0
+        d["q"][0, 0, 0, 0] = 0.5
+        d["k_cache"][..., 0] = float("-inf")
+        out = awq.awq_attention_shared(**d)
+        assert out.isnan().all()
+        j = lens[0] - n  # a key that all rows of the first sequence see
+        d["k_cache"][int(d["pages"][0, j // page]), j % page] = 0.25
+        out = awq.awq_attention_shared(**d)
+        assert out[1:].isnan().all()
+        value = d["v_cache"][int(d["pages"][0, j // page]), j % page]
+        assert torch.equal(out[0], value.repeat_interleave(hq // hkv, 0)[None].expand(n, hq, D))

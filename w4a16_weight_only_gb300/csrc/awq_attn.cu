@@ -523,7 +523,10 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
     }
     first = parts_within(first, pl.prefix_parts);
   }
-  if (pl.private_parts && __ldg(p.lens + b) > 0) {
+  bool sees = p.prefix_len > 0;  // any key at all
+  const int own_len = pl.private_parts ? own_length(p, b) : 0;
+  if (own_len > 0) {
+    sees |= own_len - p.n + 1 + bi - b * p.n > 0;
     const int own_row = (bi - b * p.n) * pl.group + h - hk * pl.group;
     own = parts_within(a.counts[pl.prefix_tiles * p.kv.heads +
                                 (static_cast<int64_t>(b) * pl.private_tiles + own_row / pl.tile) * p.kv.heads + hk],
@@ -579,7 +582,9 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
   }
 #pragma unroll
   for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-  const float inv = l > 0.f ? 1.f / l : l;  // a row that sees no key is zero; NaN stays
+  // l is at least 2^kLift where a logit is finite.  A row that sees no key is zero, one whose logits are all
+  // -inf 0 / 0; NaN stays.
+  const float inv = l > 0.f ? 1.f / l : l == 0.f && sees ? __int_as_float(0x7fffffff) : l;
   uint16_t* out = p.out + static_cast<int64_t>(r) * D + lane * V;
 #pragma unroll
   for (int c = 0; c < N; ++c) {
