@@ -248,3 +248,16 @@ def test_refusals(awq):
         awq.awq_moe_combine(x, torch.zeros((4, 3), device="cuda"), e)
     with pytest.raises(ValueError):
         awq.awq_moe_combine(x[:, ::2], torch.zeros((4, 2), device="cuda"), e)
+
+
+@pytest.mark.parametrize("W", [65535 * 128 + 1, 65535 * 1024 + 8])
+def test_rows_wider_than_a_grid_of_runs(awq, W):
+    # one element or one vector of eight more than 65535 blocks of 128 threads take
+    g = torch.Generator(device="cuda").manual_seed(W)
+    x = torch.randint(-100, 100, (2, W), generator=g, device="cuda", dtype=torch.int32).half()
+    routed, offsets, rows = awq.awq_moe_dispatch(x, torch.tensor([[1, 0], [0, -1]], dtype=torch.int32, device="cuda"), 2)
+    assert offsets.tolist() == [0, 2, 3] and rows.tolist() == [[2, 0], [1, -1]]
+    assert torch.equal(routed[:3], x[[0, 1, 0]]) and not routed[3].any()
+    weights = torch.tensor([[0.5, 0.25], [2.0, 7.0]], device="cuda")
+    out = awq.awq_moe_combine(routed, weights, rows, base=x)
+    assert torch.equal(out, x * torch.tensor([[1.75], [3.0]], dtype=torch.float16, device="cuda"))

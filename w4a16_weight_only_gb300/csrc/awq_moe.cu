@@ -406,14 +406,14 @@ constexpr int kRowThreads = 128;
 
 template <typename Vec>
 __device__ __forceinline__ void copy_row(const DispatchProblem& p, int64_t t, const int* dest, int n) {
-  const int c = blockIdx.y * kRowThreads + threadIdx.x;
-  if (c >= n) return;
-  const Vec v = __ldg(reinterpret_cast<const Vec*>(p.x + t * p.ld) + c);
+  for (uint32_t c = blockIdx.y * kRowThreads + threadIdx.x; c < static_cast<uint32_t>(n); c += gridDim.y * kRowThreads) {
+    const Vec v = __ldg(reinterpret_cast<const Vec*>(p.x + t * p.ld) + c);
 #pragma unroll 4
-  for (int j = 0; j < p.k; ++j) {
-    const int d = dest[j];
-    // a place without an expert is marked by the complement of its row
-    reinterpret_cast<Vec*>(p.routed + static_cast<int64_t>(d < 0 ? ~d : d) * p.W)[c] = d < 0 ? Vec{} : v;
+    for (int j = 0; j < p.k; ++j) {
+      const int d = dest[j];
+      // a place without an expert is marked by the complement of its row
+      reinterpret_cast<Vec*>(p.routed + static_cast<int64_t>(d < 0 ? ~d : d) * p.W)[c] = d < 0 ? Vec{} : v;
+    }
   }
 }
 
@@ -482,64 +482,68 @@ template <bool kBF, bool kVec>
 __global__ void __launch_bounds__(kRowThreads) combine_kernel(const CombineProblem p) {
   constexpr int PER = kVec ? 8 : 1, BATCH = 8;
   const int64_t t = blockIdx.x;
-  const int c = (blockIdx.y * kRowThreads + threadIdx.x) * PER;
-  if (c >= p.W) return;
-  float acc[PER];
-  const auto load = [&](const uint16_t* src, uint32_t (&v)[4]) {
-    if constexpr (kVec) *reinterpret_cast<uint4*>(v) = __ldg(reinterpret_cast<const uint4*>(src));
-    else v[0] = __ldg(src);
-  };
-  const auto value = [](const uint32_t (&v)[4], int i) {
-    if constexpr (kVec) {
-      const float2 f = pair_to_float2<kBF>(v[i >> 1]);
-      return i & 1 ? f.y : f.x;
-    } else {
-      return elem_to_float<kBF>(static_cast<uint16_t>(v[0]));
+  for (uint32_t c = (blockIdx.y * kRowThreads + threadIdx.x) * PER; c < static_cast<uint32_t>(p.W); c += gridDim.y * kRowThreads * PER) {
+    float acc[PER];
+    const auto load = [&](const uint16_t* src, uint32_t (&v)[4]) {
+      if constexpr (kVec) *reinterpret_cast<uint4*>(v) = __ldg(reinterpret_cast<const uint4*>(src));
+      else v[0] = __ldg(src);
+    };
+    const auto value = [](const uint32_t (&v)[4], int i) {
+      if constexpr (kVec) {
+        const float2 f = pair_to_float2<kBF>(v[i >> 1]);
+        return i & 1 ? f.y : f.x;
+      } else {
+        return elem_to_float<kBF>(static_cast<uint16_t>(v[0]));
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+    if (p.base) {
+      uint32_t v[4];
+      if constexpr (kVec) *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(p.base + t * p.W + c);  // out may be base
+      else v[0] = p.base[t * p.W + c];
+#pragma unroll
+      for (int i = 0; i < PER; ++i) acc[i] = value(v, i);
     }
-  };
+    for (int j0 = 0; j0 < p.k; j0 += BATCH) {
+      uint32_t v[BATCH][4];
+      float w[BATCH];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-  if (p.base) {
-    uint32_t v[4];
-    if constexpr (kVec) *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(p.base + t * p.W + c);  // out may be base
-    else v[0] = p.base[t * p.W + c];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) acc[i] = value(v, i);
-  }
-  for (int j0 = 0; j0 < p.k; j0 += BATCH) {
-    uint32_t v[BATCH][4];
-    float w[BATCH];
-#pragma unroll
-    for (int u = 0; u < BATCH; ++u) {
-      w[u] = 0.f;
-      v[u][0] = v[u][1] = v[u][2] = v[u][3] = 0u;
-      if (j0 + u < p.k) {
-        const int r = __ldg(p.rows + t * p.k + j0 + u);
-        if (r >= 0 && r < p.R) {
-          w[u] = __ldg(p.weights + t * p.k + j0 + u);
-          load(p.y + static_cast<int64_t>(r) * p.W + c, v[u]);
+      for (int u = 0; u < BATCH; ++u) {
+        w[u] = 0.f;
+        v[u][0] = v[u][1] = v[u][2] = v[u][3] = 0u;
+        if (j0 + u < p.k) {
+          const int r = __ldg(p.rows + t * p.k + j0 + u);
+          if (r >= 0 && r < p.R) {
+            w[u] = __ldg(p.weights + t * p.k + j0 + u);
+            load(p.y + static_cast<int64_t>(r) * p.W + c, v[u]);
+          }
         }
       }
+#pragma unroll
+      for (int u = 0; u < BATCH; ++u) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) acc[i] += w[u] * value(v[u], i);
+      }
     }
+    if constexpr (kVec) {
+      uint32_t v[4];
 #pragma unroll
-    for (int u = 0; u < BATCH; ++u) {
-#pragma unroll
-      for (int i = 0; i < PER; ++i) acc[i] += w[u] * value(v[u], i);
+      for (int i = 0; i < 4; ++i)
+        v[i] = static_cast<uint32_t>(float_to_elem<kBF>(acc[2 * i])) | (static_cast<uint32_t>(float_to_elem<kBF>(acc[2 * i + 1])) << 16);
+      *reinterpret_cast<uint4*>(p.out + t * p.W + c) = *reinterpret_cast<const uint4*>(v);
+    } else {
+      p.out[t * p.W + c] = float_to_elem<kBF>(acc[0]);
     }
-  }
-  if constexpr (kVec) {
-    uint32_t v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      v[i] = static_cast<uint32_t>(float_to_elem<kBF>(acc[2 * i])) | (static_cast<uint32_t>(float_to_elem<kBF>(acc[2 * i + 1])) << 16);
-    *reinterpret_cast<uint4*>(p.out + t * p.W + c) = *reinterpret_cast<const uint4*>(v);
-  } else {
-    p.out[t * p.W + c] = float_to_elem<kBF>(acc[0]);
   }
 }
 
-// Column runs of a row; rows of more than 65535 runs are not launched.
-unsigned runs(int64_t vectors) { return static_cast<unsigned>((vectors + kRowThreads - 1) / kRowThreads); }
+// Column runs of a row, one block each; beyond the most that a grid's second dimension takes, a block takes
+// several.
+unsigned runs(int64_t vectors) {
+  const int64_t n = (vectors + kRowThreads - 1) / kRowThreads;
+  return static_cast<unsigned>(n < 1 ? 1 : n < 65535 ? n : 65535);
+}
 
 // A launch that may be set up while the kernel before it on the stream still runs; the kernel waits
 // for that one's results itself.
@@ -561,8 +565,7 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t sm
 template <typename Vec>
 cudaError_t run_dispatch(const DispatchProblem& p) {
   const int64_t R = p.T * p.k, vectors = p.W / static_cast<int>(sizeof(Vec) / 2);
-  const dim3 rows(static_cast<unsigned>(p.T), runs(vectors) ? runs(vectors) : 1u);
-  if (rows.y > 65535u) return cudaErrorInvalidConfiguration;
+  const dim3 rows(static_cast<unsigned>(p.T), runs(vectors));
   if (R <= kFewPlaces && p.k <= kFewK) {
     dispatch_few_kernel<Vec><<<rows, kRowThreads, (p.E + 1) * 4, p.stream>>>(p);
     return cudaGetLastError();
@@ -603,7 +606,6 @@ cudaError_t launch_dispatch(const DispatchProblem& p) {
 cudaError_t launch_combine(const CombineProblem& p) {
   const bool vec = p.W % 8 == 0 && aligned(p.y, 16) && aligned(p.out, 16) && aligned(p.base, 16);
   const dim3 grid(static_cast<unsigned>(p.T), runs(vec ? p.W / 8 : p.W));
-  if (grid.y > 65535u) return cudaErrorInvalidConfiguration;
   if (vec) {
     if (p.bf16) combine_kernel<true, true><<<grid, kRowThreads, 0, p.stream>>>(p);
     else combine_kernel<false, true><<<grid, kRowThreads, 0, p.stream>>>(p);
