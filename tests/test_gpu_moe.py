@@ -261,3 +261,15 @@ def test_rows_wider_than_a_grid_of_runs(awq, W):
     weights = torch.tensor([[0.5, 0.25], [2.0, 7.0]], device="cuda")
     out = awq.awq_moe_combine(routed, weights, rows, base=x)
     assert torch.equal(out, x * torch.tensor([[1.75], [3.0]], dtype=torch.float16, device="cuda"))
+
+
+def test_sigmoid_weights_keep_their_last_bit(awq):
+    # 1 / (1 + e), e = exp(-x): exp to one ulp (2^-23, moving the result by e / (1 + e) of that), a rounded sum
+    # and a rounded quotient (2^-24 each)
+    x = torch.linspace(-12.0, 25.0, 1 << 20, device="cuda").view(-1, 8)
+    w, e = awq.awq_moe_route(x, 8, scoring="sigmoid", renormalize=False)
+    got = torch.empty_like(w).scatter_(1, e.long(), w)
+    big = torch.exp(-x.double())
+    want = 1 / (1 + big)
+    tol = (2.0 ** -23 * big / (1 + big) + 2.0 ** -23) * (1 + 2.0 ** -20)
+    assert (((got.double() - want) / want).abs() <= tol).all()

@@ -28,7 +28,9 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
   else return elem_to_float<DT == 2>(__ldg(static_cast<const uint16_t*>(p) + i));
 }
 
-__device__ __forceinline__ float reciprocal(float x) {  // good to the last bit or two
+// Good to one unit in the last place: for the keys, of which every expert has one (rounded reciprocals: 19.0
+// against 18.3 us for 16381 tokens of 256 experts).  The k weights take the rounded one.
+__device__ __forceinline__ float reciprocal(float x) {
   float y;
   asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
@@ -72,7 +74,7 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteProblem p) {
 
   // scores; an expert whose logit is -inf is out
   float top = -INFINITY, inv = 0.f;
-  const auto score_of = [&](float v) { return p.sigmoid ? reciprocal(1.f + expf(-v)) : expf(v - top) * inv; };
+  const auto score_of = [&](float v) { return p.sigmoid ? __frcp_rn(1.f + expf(-v)) : expf(v - top) * inv; };
   float score[VT];
   if (p.sigmoid) {
 #pragma unroll
