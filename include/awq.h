@@ -441,7 +441,7 @@ awq_status_t awq_gemm_packed_w8(const void* x_f16, const void* packed, const voi
  * whose sequences share a prefix, routing of tokens to experts, and the dispatch / combine pair
  * around the grouped linears above.  Elements are fp16 or bf16 (dtype AWQ_DTYPE_F16 or
  * AWQ_DTYPE_BF16) unless stated; strides are in elements; arithmetic is fp32 (or wider), rounded
- * once to the element type.  The conventions at the top of this file hold: device pointers, no
+ * once to the element type (awq_attention_shared rounds its probabilities as well).  The conventions at the top of this file hold: device pointers, no
  * allocation, asynchronous on `stream`, argument errors on the host before any launch.  Values
  * that only the device sees (positions, slots, pages, lengths, expert ids, rows) are checked
  * there: one outside its range never leads to an access outside the tensors.
@@ -520,7 +520,7 @@ awq_status_t awq_rope_append(const void* q, const void* k, const void* v, const 
 
 /*
  * awq_attention_shared -- attention of the n newest tokens of B sequences that share a prefix, the
- * prefix read and multiplied once for all of them:
+ * prefix's keys and values taken for the query rows of all sequences together:
  *
  *   out[b][i][h] = sum_j softmax_j(scale * q[b][i][h] . k_j) v_j
  *
@@ -533,6 +533,16 @@ awq_status_t awq_rope_append(const void* q, const void* k, const void* v, const 
  *   pages int32 [B, W] (row stride pages_stride), lens int32 [B]: each sequence's own pages and its
  *   number of own tokens; max_len >= every lens[b] (a longer one is cut to max_len), max_len <=
  *   W * page_size.  prefix_len, max_len are host values: the plan depends on them.
+ * The B * n * Hq / heads rows that share a key/value head read the prefix once if they are more than
+ * 32 and D <= 128, else once per 8 to 32 rows (D = 256: per 16).  A sequence's own keys are read
+ * once per 8 to 32 of its rows: the call is made for few new tokens per sequence, and a prompt is right
+ * but slow (4096 tokens, 64 / 8 heads of 128: 4.5 ms).
+ * max_len sets the least share of the own keys that a warp takes: up to four times the average length
+ * it costs nothing, far beyond that time grows with it (128 sequences of 1024 own keys on average over
+ * 32768: 0.16 ms at max_len 2048 and 8192, 0.37 ms at 32768, 1.35 ms at 131072).
+ * Precision: logits, statistics and sums are fp32.  Each probability is rounded to the element type as
+ * the factor of its value (the second matrix product's operand type; the sum that divides uses the
+ * unrounded ones), the result once more.
  * A row uses only the keys that it sees: what the cache holds past a length, or a newer token's value,
  * may be infinite or NaN.  A page outside [0, num_pages) gives unspecified values for its sequence.
  * A row that sees no key is zero; one whose logits are all -inf is NaN.  B, n or Hq 0: AWQ_OK, no launch.

@@ -219,7 +219,9 @@ def awq_attention_shared(q, k_cache, v_cache, prefix_pages, prefix_len, pages, l
     page_size, heads, D] (D 64, 96, 128 or 256; Hq a multiple of heads), equal strides; prefix_pages
     int32 [>= ceil(prefix_len / page_size)]; pages int32 [B, W]; lens int32 [B]: own tokens of each
     sequence, the n new ones last (causal among themselves).  prefix_len and max_len (>= every length;
-    default W * page_size) are host integers.  scale defaults to 1 / sqrt(D).  Returns q's shape, dense.
+    default W * page_size) are host integers; pass a max_len near the longest length where the table is
+    much wider: far above four times the average length the call slows down with it (awq.h).  scale
+    defaults to 1 / sqrt(D).  Returns q's shape, dense.
     workspace: a uint8 device tensor of awq_attention_shared_workspace_size bytes (default: this
     module's for the stream)."""
     dt, dev, qs = q.dtype, q.get_device(), q.shape

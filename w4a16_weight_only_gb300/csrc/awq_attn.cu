@@ -604,7 +604,11 @@ Plan make_plan(const AttentionProblem& p, int sms) {
   pl.group = p.Hq / p.kv.heads;
   pl.own_rows = p.n * pl.group;
   const int64_t stacked = static_cast<int64_t>(p.B) * pl.own_rows;  // rows that share a prefix key
-  // from 33 rows on; its steps are counted in 32 bits
+  // Tensor cores from 33 rows on; their steps are counted in 32 bits.  Both sides measured (us a call, tensor
+  // cores and streaming kernel; 64 own keys per row's sequence): 40 rows of one head of 128 over 256, 2048 and
+  // 16384 keys 13.7 / 14.6, 13.3 / 17.3, 16.3 / 41.8, of eight heads 13.4 / 15.8, 14.5 / 25.1, 27.3 / 65.6; 8 rows
+  // of eight heads 13.3 / 10.2, 13.6 / 12.8, 23.6 / 23.5.  Between 17 and 32 rows the tensor cores are the faster
+  // ones already (24 rows of eight heads: 13.4 / 15.5, 14.1 / 21.0, 26.4 / 49.8), which this rule leaves.
   pl.tc = p.prefix_len > 0 && tc_head_dim_supported(p.kv.head_dim) && stacked > 32 &&
           static_cast<int64_t>(p.kv.heads) * ceil_div(stacked, kTcRows) * ceil_div(p.prefix_len, kTcKeys) < (int64_t{1} << 30);
   const int64_t rows = pl.tc || p.prefix_len == 0 ? pl.own_rows : stacked;
@@ -654,8 +658,8 @@ Layout layout(const AttentionProblem& p, const Plan& pl) {
 }
 
 // The kernel, set up and where there is room run while the one before it still runs; it waits for that
-// one's end itself.  Behind the tensor-core kernel: the streaming kernel runs beside it.  Without it the
-// launch attribute's host time is more than what is saved (30.3 against 27.7 us a call for 3 over 1000).
+// one's end itself.  Behind the tensor-core kernel: the streaming kernel runs beside it.  Without that one
+// only the join could be early: 0.2 us of 12.0 for 3 over 1000, lost in a call's host time of 22 us.
 template <typename A>
 cudaError_t launch_early(void (*kernel)(A), unsigned blocks, int threads, size_t smem, cudaStream_t stream, const A& a, bool early) {
   cudaLaunchAttribute attr[1];

@@ -113,8 +113,14 @@ __host__ __device__ inline int tc_last_group(const Plan& pl, int u, int per) { r
 // up to 64 own keys over 32768: 109 us, 131 with 4 SMs).  Blocks of the tensor-core kernel beyond its
 // share leave at once; the streaming kernel's blocks are one wave on the SMs left, or, where whole groups
 // leave it much less than its share, as many as all SMs hold.  128 sequences of 1024 own keys over 32768
-// shared ones, 8 heads: some 100 SMs and 50, 149 us a call with the join; one after the other on all SMs 188
-// us; 64 of 512 over 8192: 52 and 61 us.
+// shared ones, 8 heads: some 100 SMs and 50, 151 us of kernels with the join; one after the other on all
+// SMs 192 us; 64 of 512 over 8197: 48 and 65 us.
+//
+// The costs were fitted to heads of 128, eight query rows per head and full row tiles.  With 0.35 to 2.8 times
+// the streaming step's cost, the constants here are within 2 % of the best for heads of 64 and 96, 16-row
+// units, row tiles filled to an eighth or a half, and one query head per key/value head; 14 % above it for
+// pages of 20 tokens (212 us, 186 at 0.71 times the cost: 128 sequences over 16384) and 65 % for 32-row units
+// (64 sequences of four new tokens: 350 us, 212 at 2.8 times the cost).
 constexpr int64_t kTcStepNs = 1660, kTcFixedSteps = 3, kStreamStepNs = 108, kStreamFixedSteps = 2;
 
 constexpr int kLeastShare = 12;
