@@ -616,6 +616,150 @@ awq_status_t awq_moe_combine(const void* y, int64_t R, int64_t W, const float* w
                              const int32_t* rows, int64_t T, int64_t k, const void* base, void* out,
                              awq_dtype_t dtype, awq_stream_t stream);
 
+/* ------------------------------------------------------------------------------------------
+ * A key/value cache held in 4 bits, and what stands around it in a decode step: the append that
+ * quantizes, attention with a sliding window and first tokens that stay visible, the norms around a
+ * residual sum, and a mixture-of-experts layer for a few tokens.  As above: fp16 or bf16 elements,
+ * strides in elements unless stated, fp32 arithmetic, values that only the device sees checked there.
+ * ------------------------------------------------------------------------------------------ */
+
+/*
+ * A paged cache of 4-bit keys and values.  `group_size` (32, 64 or 128, dividing head_dim) neighbouring
+ * elements x of a token's head are kept as 4-bit codes c, a minimum m and a scale s of the 16-bit
+ * element type; c stands for c * s + m:
+ *
+ *   m = min x,  s = rn16((max x - m) / 15),  c = clamp(rint((x - m) / s), 0, 15)   (s = 0: c = 0)
+ *
+ * a group that holds an infinity or a NaN reads NaN.  Page p's tokens of head h are the page_size / 16 tiles
+ * of 16 tokens from byte p * page_stride + h * head_stride of data on.  A tile has 16 (D + 8 G) bytes, D =
+ * head_dim, G = D / group_size:
+ *
+ *   8 D bytes of key codes, 8 D of value codes, 64 G of the keys' (s, m) pairs, [token][group], 64 G of the
+ *   values'.  The low nibble of a byte is an even element's, the high one the next element's.
+ *   Keys: element 8 w + j (j < 8) of token r, w = 16 a + 4 b + t (t < 4; b < W, W = min(D, 128) / 32), is in byte
+ *     1024 a + 16 W r + 4 (W t + b) + j / 2.
+ *   Values: element 32 u + 4 g + j (j < 4) of token r = 8 h + 2 t + o (o < 2) is in byte
+ *     512 (u / 2) + 16 (4 g + t) + 8 (u % 2) + 4 h + 2 o + j / 2, or, for the last u of an odd number,
+ *     512 (u / 2) +  8 (4 g + t)               + 4 h + 2 o + j / 2.
+ *
+ * (the order in which tensor-core fragments take them).  Slot s is token s % page_size of page s / page_size.
+ * Requirements: D = 64, 96, 128 or 256; page_size a multiple of 16; data 16-byte aligned, page_stride and
+ * head_stride (bytes; of a dimension of more than one entry) multiples of 16, not negative; num_pages *
+ * page_size below 2^31.
+ */
+typedef struct awq_kv4_cache {
+  void* data;
+  int64_t num_pages, page_size, heads, head_dim, group_size;
+  int64_t page_stride, head_stride;
+} awq_kv4_cache_t;
+
+/* Bytes of one head's tokens of a page: page_size * (head_dim + 8 * head_dim / group_size).  Host only. */
+awq_status_t awq_kv4_page_bytes(int64_t page_size, int64_t head_dim, int64_t group_size, size_t* bytes);
+
+/*
+ * awq_rope_append_kv4 -- awq_rope_append to a 4-bit cache: rotated keys, rounded to the element type, and
+ * values are quantized to cell slots[t].  A rotated element is a c - b s with both products and the
+ * difference rounded to fp32 by themselves, in q_out as in the cache.  table NULL: nothing is rotated
+ * (positions, rotary_dim, max_position are not looked at), q is copied; Hq may be 0.  Otherwise as
+ * awq_rope_append: a slot outside the cache keeps nothing, two tokens must not share a slot, q_out may
+ * be q.  A position outside the table gives NaN: groups of the key that hold rotated elements read NaN.
+ * T * (Hq + 2 Hkv) must be below 2^31.  One launch.
+ */
+awq_status_t awq_rope_append_kv4(const void* q, const void* k, const void* v, const int32_t* positions,
+                                 const float* table, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                                 int64_t rotary_dim, int64_t max_position, int64_t q_token_stride,
+                                 int64_t q_head_stride, int64_t k_token_stride, int64_t k_head_stride,
+                                 int64_t v_token_stride, int64_t v_head_stride, void* q_out,
+                                 const awq_kv4_cache_t* cache, const int32_t* slots, int interleaved,
+                                 awq_dtype_t dtype, awq_stream_t stream);
+
+/*
+ * awq_kv4_read -- the keys and values that the cache holds at slots int32 [T], c * s + m rounded once to
+ * the element type: k, v [T, heads, head_dim] dense.  A slot outside the cache reads zero.  T * heads must
+ * be below 2^31.  One launch.
+ */
+awq_status_t awq_kv4_read(const awq_kv4_cache_t* cache, const int32_t* slots, int64_t T, void* k, void* v,
+                          awq_dtype_t dtype, awq_stream_t stream);
+
+/*
+ * awq_attention_kv4 -- attention of the n newest tokens of B sequences over a 4-bit cache:
+ *
+ *   out[b][i][h] = sum_j softmax_j(scale * q[b][i][h] . k_j) v_j
+ *
+ * over the keys j that query token i of sequence b, at P = lens[b] - n + i, sees: j <= P, and with a window
+ * > 0 of these j > P - window or j < sinks (the first tokens of a sequence stay visible).  Query head h
+ * reads key/value head h / (Hq / heads).
+ *   q [B, n, Hq, D]: strides given, a head contiguous; out [B, n, Hq, D] dense
+ *   pages int32 [B, W] (row stride pages_stride): the sequences' pages, in order; lens int32 [B], the n new
+ *   tokens counted (one above W * page_size is cut to it).  Pages that a window leaves out may be any
+ *   number: they are not read.
+ * k_j and v_j are what the codes stand for, unrounded; logits, statistics and sums are fp32; the factor of a
+ * value, probability times scale, is rounded to fp16's 11 bits.  A row uses only the keys that it sees: what the cache holds elsewhere
+ * may be anything.  A page outside [0, num_pages) gives unspecified values for its sequence.  A row that
+ * sees no key is zero; one whose logits are all -inf is NaN.  B, n or Hq 0: AWQ_OK, no launch.
+ *   workspace: awq_attention_kv4_workspace_size bytes, 256-byte aligned; any content.  Calls that overlap in
+ *   time need workspaces of their own.
+ * Repeated calls give the same bits.  The call is made for few new tokens per sequence: a prompt is right
+ * but slow.  Requirements: q and out 16-byte aligned, q's strides multiples of 8 (of dimensions of more than
+ * one entry), Hq a multiple of heads; W * page_size below 2^31, window and sinks in 0..2^31 - 1.
+ */
+awq_status_t awq_attention_kv4_workspace_size(int64_t B, int64_t n, int64_t Hq, int64_t heads, int64_t D,
+                                              size_t* bytes);
+awq_status_t awq_attention_kv4(const void* q, int64_t B, int64_t n, int64_t Hq, int64_t q_batch_stride,
+                               int64_t q_token_stride, int64_t q_head_stride, const awq_kv4_cache_t* cache,
+                               const int32_t* pages, int64_t W, int64_t pages_stride, const int32_t* lens,
+                               int64_t window, int64_t sinks, float scale, void* out, awq_dtype_t dtype,
+                               void* workspace, size_t workspace_bytes, awq_stream_t stream);
+
+typedef enum awq_norm { AWQ_NORM_RMS = 0, AWQ_NORM_LAYER = 1 } awq_norm_t;
+
+/*
+ * awq_residual_norm -- the norms before and after a block, around its residual sum:
+ *
+ *   t = norm(x) * post_weight (+ post_bias), or x where post_weight is NULL
+ *   h = residual + scale * gate * t          (a NULL residual counts 0, a NULL gate 1)
+ *   y = norm(h) * weight (+ bias)            (not formed where weight is NULL)
+ *   norm(z) = z / sqrt(mean(z^2) + eps) over the row; LAYER: of z - mean(z)
+ *
+ *   x, residual [T, W]: row strides given; gate [T, W] with a row stride, 0 for one row of all tokens;
+ *   weights and biases [W]; h, y [T, W] dense.  h may be residual and y may be x where those are dense.
+ * fp32 arithmetic, y from the unrounded h, each output rounded once.  T == 0 or W == 0: AWQ_OK, no launch.
+ * Requirements: post_bias only with post_weight, bias only with weight, y with weight; eps >= 0; outputs
+ * overlap nothing else.  One launch.
+ */
+awq_status_t awq_residual_norm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                               const void* gate, int64_t gate_stride, const void* post_weight,
+                               const void* post_bias, float scale, const void* weight, const void* bias,
+                               int64_t T, int64_t W, awq_norm_t kind, float eps, void* h, void* y,
+                               awq_dtype_t dtype, awq_stream_t stream);
+
+/*
+ * awq_moe_layer -- a mixture-of-experts layer of a few tokens on 4-bit experts, in two launches:
+ *
+ *   act[t][j] = silu(x[t] Wg) * (x[t] Wu),   out[t] = base[t] + sum_j weights[t][j] * (act[t][j] Wd)
+ *
+ * with the matrices of expert experts[t][j] (awq_moe_route's ids and weights), w = (code - zero) * scale.
+ *   x [T, H] (row stride given), weights fp32 [T, k], experts int32 [T, k]; base [T, H] or NULL, out [T, H]
+ *   dense (may be base, not x)
+ *   up_qweight int32 [E, H, 2 I / 8], up_qzeros [E, H / G, 2 I / 8], up_scales 16-bit [E, H / G, 2 I]: gate
+ *   columns, then up columns; down_qweight [E, I, H / 8], down_qzeros [E, I / G, H / 8], down_scales [E, I /
+ *   G, H]: stacked linears as awq_gemm_grouped takes them, G = group_size
+ * A place whose id lies outside [0, E) (-1) is left out, whatever its weight.  Sums are fp32, of a token's
+ * places in their order; act is rounded to the element type as the factor of the second product, the
+ * result once more.  Repeated calls give the same bits.
+ *   workspace: awq_moe_layer_workspace_size bytes, 256-byte aligned; any content.  Calls that overlap in
+ *   time need workspaces of their own.
+ * Requirements: 0 <= T <= 16 (more: awq_moe_dispatch and the grouped linears), 0 <= k <= 32, 1 <= E <= 4096;
+ * H and I multiples of 8 and of G > 0; E * H * 2 I below 2^40.  T == 0 or H == 0: AWQ_OK, no launch.
+ */
+awq_status_t awq_moe_layer_workspace_size(int64_t T, int64_t k, int64_t I, size_t* bytes);
+awq_status_t awq_moe_layer(const void* x, int64_t T, int64_t H, int64_t row_stride, const int32_t* experts,
+                           const float* weights, int64_t k, int64_t E, int64_t I, int64_t group_size,
+                           const int32_t* up_qweight, const int32_t* up_qzeros, const void* up_scales,
+                           const int32_t* down_qweight, const int32_t* down_qzeros, const void* down_scales,
+                           const void* base, void* out, awq_dtype_t dtype, void* workspace,
+                           size_t workspace_bytes, awq_stream_t stream);
+
 /* Synchronizes `stream`, then reads and clears the library's device status word on the
  * current device.  Returns AWQ_ERR_TIMEOUT if a kernel gave up a bounded wait since the
  * last check (its output is then unspecified), AWQ_OK otherwise. */

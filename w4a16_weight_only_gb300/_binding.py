@@ -29,7 +29,14 @@ class PagedKV(ctypes.Structure):
                                                               "page_stride", "token_stride", "head_stride")]
 
 
+class Kv4Cache(ctypes.Structure):
+    """awq_kv4_cache_t."""
+    _fields_ = [("data", _vp)] + [(n, _i64) for n in ("num_pages", "page_size", "heads", "head_dim", "group_size",
+                                                     "page_stride", "head_stride")]
+
+
 _kv = ctypes.POINTER(PagedKV)
+_kv4 = ctypes.POINTER(Kv4Cache)
 _size = ctypes.POINTER(ctypes.c_size_t)
 
 # Every entry point of include/awq.h: name -> (restype, argtypes)
@@ -76,6 +83,17 @@ SIGNATURES = {
     "awq_moe_dispatch_workspace_size": (_i32, [_i64, _i64, _i64, _size]),
     "awq_moe_dispatch": (_i32, [_vp, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
     "awq_moe_combine": (_i32, [_vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _i32, _vp]),
+    "awq_kv4_page_bytes": (_i32, [_i64, _i64, _i64, _size]),
+    "awq_rope_append_kv4": (_i32, [_vp] * 5 + [_i64] * 12 + [_vp, _kv4, _vp, _i32, _i32, _vp]),
+    "awq_kv4_read": (_i32, [_kv4, _vp, _i64, _vp, _vp, _i32, _vp]),
+    "awq_attention_kv4_workspace_size": (_i32, [_i64] * 5 + [_size]),
+    "awq_attention_kv4": (_i32, [_vp] + [_i64] * 6 + [_kv4, _vp, _i64, _i64, _vp, _i64, _i64, _f32, _vp, _i32, _vp,
+                                 ctypes.c_size_t, _vp]),
+    "awq_residual_norm": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _f32, _vp, _vp, _i64, _i64, _i32, _f32, _vp, _vp,
+                                 _i32, _vp]),
+    "awq_moe_layer_workspace_size": (_i32, [_i64] * 3 + [_size]),
+    "awq_moe_layer": (_i32, [_vp, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _i64, _i64] + [_vp] * 8 + [_i32, _vp, ctypes.c_size_t,
+                                                                                                    _vp]),
 }
 GEMM_STATIC_WEIGHTS = 1
 

@@ -8,6 +8,7 @@
 #include "../../include/awq.h"
 #include "awq_internal.cuh"
 #include "awq_layer.cuh"
+#include "awq_step.cuh"
 
 namespace {
 
@@ -1014,6 +1015,303 @@ awq_status_t awq_moe_combine(const void* y, int64_t R, int64_t W, const float* w
                               dtype == AWQ_DTYPE_BF16, reinterpret_cast<cudaStream_t>(stream)};
   const cudaError_t e = awq::launch_combine(p);
   if (e != cudaSuccess) return cuda_fail(e, "awq_moe_combine launch");
+  return ok();
+}
+
+// ------------------------------- a 4-bit cache, norms, a layer of a few tokens' experts ----
+
+namespace {
+
+awq_status_t check_kv4_shape(int64_t page_size, int64_t head_dim, int64_t group_size) {
+  if (page_size <= 0 || head_dim <= 0 || group_size <= 0)
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "cache: page_size, head_dim, group_size > 0 needed");
+  if (!awq::kv4_shape_supported(head_dim, group_size))
+    return fail(AWQ_ERR_UNSUPPORTED_SHAPE,
+                "cache: head_dim must be 64, 96, 128 or 256 and group_size 32, 64 or 128 dividing it (got %lld, %lld)",
+                (long long)head_dim, (long long)group_size);
+  if (page_size % 16) return fail(AWQ_ERR_UNSUPPORTED_SHAPE, "cache: page_size must be a multiple of 16 (got %lld)", (long long)page_size);
+  if (page_size > kDimLimit) return fail(AWQ_ERR_UNSUPPORTED_SHAPE, "cache: page_size must be below 2^31");
+  return AWQ_OK;
+}
+
+awq_status_t check_kv4(const awq_kv4_cache_t* c, awq::Kv4Cache* out) {
+  if (!c) return fail(AWQ_ERR_INVALID_ARGUMENT, "null cache");
+  const awq_status_t st = check_kv4_shape(c->page_size, c->head_dim, c->group_size);
+  if (st != AWQ_OK) return st;
+  if (c->num_pages < 0 || c->heads <= 0) return fail(AWQ_ERR_INVALID_ARGUMENT, "cache: num_pages >= 0 and heads > 0 needed");
+  if (c->num_pages > kDimLimit || c->heads > 65536 || c->num_pages * c->page_size > kDimLimit)
+    return fail(AWQ_ERR_UNSUPPORTED_SHAPE, "cache: num_pages * page_size must be below 2^31, heads <= 65536");
+  // a dimension of one entry is never stepped along: its stride may be anything
+  const int64_t page_stride = c->num_pages > 1 ? c->page_stride : 0, head_stride = c->heads > 1 ? c->head_stride : 0;
+  if (page_stride < 0 || head_stride < 0) return fail(AWQ_ERR_INVALID_ARGUMENT, "cache strides must not be negative");
+  if (c->num_pages > 0 && !c->data) return fail(AWQ_ERR_INVALID_ARGUMENT, "cache: null data");
+  if (!al(c->data, 16) || page_stride % 16 || head_stride % 16)
+    return fail(AWQ_ERR_MISALIGNED, "cache: data must be 16-byte aligned, its strides multiples of 16 bytes");
+  *out = {static_cast<uint8_t*>(c->data), static_cast<int>(c->num_pages), static_cast<int>(c->page_size), static_cast<int>(c->heads),
+          static_cast<int>(c->head_dim), static_cast<int>(c->group_size), page_stride, head_stride};
+  return AWQ_OK;
+}
+
+awq_status_t attention_kv4_shape(int64_t B, int64_t n, int64_t Hq, int64_t heads, int64_t D, awq::AttentionKv4Problem* p) {
+  if (B < 0 || n < 0 || Hq < 0) return fail(AWQ_ERR_INVALID_ARGUMENT, "B, n, Hq must be >= 0");
+  if (heads <= 0 || Hq % heads)
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "Hq must be a multiple of the cache's heads (got %lld of %lld)", (long long)Hq,
+                (long long)heads);
+  if (!awq::kv4_shape_supported(D, 32))
+    return fail(AWQ_ERR_UNSUPPORTED_SHAPE, "head_dim must be 64, 96, 128 or 256 (got %lld)", (long long)D);
+  if (Hq > 65536 || B > kDimLimit || n > kDimLimit || B * n > kDimLimit || B * n * Hq > kDimLimit)
+    return fail(AWQ_ERR_UNSUPPORTED_SHAPE, "B * n * Hq must be below 2^31, Hq <= 65536");
+  p->B = static_cast<int>(B);
+  p->n = static_cast<int>(n);
+  p->Hq = static_cast<int>(Hq);
+  p->cache.heads = static_cast<int>(heads);
+  p->cache.head_dim = static_cast<int>(D);
+  return AWQ_OK;
+}
+
+awq_status_t check_workspace(const void* workspace, size_t have, size_t need) {
+  if (need && !workspace) return fail(AWQ_ERR_INVALID_ARGUMENT, "null workspace");
+  if (!al(workspace, 256)) return fail(AWQ_ERR_MISALIGNED, "workspace must be 256-byte aligned");
+  if (have < need) return fail(AWQ_ERR_INVALID_ARGUMENT, "the workspace has %zu bytes, this call needs %zu", have, need);
+  return AWQ_OK;
+}
+
+awq_status_t moe_layer_shape(int64_t T, int64_t k, int64_t I) {
+  if (T < 0 || T > awq::kMoeLayerMaxT)
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "T must be in 0..%d (got %lld): route more tokens through awq_moe_dispatch",
+                awq::kMoeLayerMaxT, (long long)T);
+  if (k < 0 || k > awq::kRouteMaxK) return fail(AWQ_ERR_INVALID_ARGUMENT, "k must be in 0..%d (got %lld)", awq::kRouteMaxK, (long long)k);
+  if (I < 0) return fail(AWQ_ERR_INVALID_ARGUMENT, "I must be >= 0 (got %lld)", (long long)I);
+  if (I >= (int64_t{1} << 30)) return fail(AWQ_ERR_UNSUPPORTED_SHAPE, "I must be below 2^30");
+  return AWQ_OK;
+}
+
+}  // namespace
+
+awq_status_t awq_kv4_page_bytes(int64_t page_size, int64_t head_dim, int64_t group_size, size_t* bytes) {
+  if (!bytes) return fail(AWQ_ERR_INVALID_ARGUMENT, "null bytes pointer");
+  const awq_status_t st = check_kv4_shape(page_size, head_dim, group_size);
+  if (st != AWQ_OK) return st;
+  *bytes = static_cast<size_t>(page_size) * (head_dim + 8 * (head_dim / group_size));
+  return ok();
+}
+
+awq_status_t awq_rope_append_kv4(const void* q, const void* k, const void* v, const int32_t* positions, const float* table,
+                                 int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t rotary_dim, int64_t max_position,
+                                 int64_t q_token_stride, int64_t q_head_stride, int64_t k_token_stride, int64_t k_head_stride,
+                                 int64_t v_token_stride, int64_t v_head_stride, void* q_out, const awq_kv4_cache_t* cache,
+                                 const int32_t* slots, int interleaved, awq_dtype_t dtype, awq_stream_t stream) {
+  awq::AppendKv4Problem p{};
+  awq_status_t st = check_half(dtype);
+  if (st == AWQ_OK) st = check_kv4(cache, &p.cache);
+  if (st != AWQ_OK) return st;
+  if (!table) rotary_dim = max_position = 0;
+  if (T < 0 || Hq < 0 || Hkv < 0 || max_position < 0)
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "T, Hq, Hkv, max_position must be >= 0");
+  if (table && (rotary_dim < 2 || rotary_dim % 2 || rotary_dim > D))
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "rotary_dim must be even, in 2..D (got %lld of D %lld)", (long long)rotary_dim, (long long)D);
+  if (p.cache.heads != Hkv || p.cache.head_dim != D)
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "the cache must have Hkv heads of D elements");
+  if (Hq + 2 * Hkv > 65536 || T > kDimLimit || T * (Hq + 2 * Hkv) > kDimLimit || max_position > kDimLimit)
+    return fail(AWQ_ERR_UNSUPPORTED_SHAPE, "Hq + 2 Hkv must be <= 65536, T * (Hq + 2 Hkv) and max_position below 2^31");
+  if (T == 0) return ok();
+  if ((Hq && (!q || !q_out)) || !k || !v || (table && !positions) || !slots)
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "awq_rope_append_kv4: null pointer");
+  if (!al(q, 2) || !al(k, 2) || !al(v, 2) || !al(q_out, 2)) return fail(AWQ_ERR_MISALIGNED, "16-bit tensors must be 2-byte aligned");
+  if (!al(positions, 4) || !al(table, 4) || !al(slots, 4))
+    return fail(AWQ_ERR_MISALIGNED, "positions, slots and table must be 4-byte aligned");
+  st = check_device();
+  if (st != AWQ_OK) return st;
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.positions = positions;
+  p.table = table;
+  p.T = T;
+  p.Hq = static_cast<int>(Hq);
+  p.Hkv = static_cast<int>(Hkv);
+  p.D = static_cast<int>(D);
+  p.rot = static_cast<int>(rotary_dim);
+  p.max_position = static_cast<int>(max_position);
+  p.q_st = q_token_stride;
+  p.q_sh = q_head_stride;
+  p.k_st = k_token_stride;
+  p.k_sh = k_head_stride;
+  p.v_st = v_token_stride;
+  p.v_sh = v_head_stride;
+  p.q_out = static_cast<uint16_t*>(q_out);
+  p.qo_st = q_out == q ? q_token_stride : Hq * D;  // in place: the input's strides
+  p.qo_sh = q_out == q ? q_head_stride : D;
+  p.slots = slots;
+  p.interleaved = interleaved != 0;
+  p.bf16 = dtype == AWQ_DTYPE_BF16;
+  p.stream = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = awq::launch_append_kv4(p);
+  if (e != cudaSuccess) return cuda_fail(e, "awq_rope_append_kv4 launch");
+  return ok();
+}
+
+awq_status_t awq_kv4_read(const awq_kv4_cache_t* cache, const int32_t* slots, int64_t T, void* k, void* v, awq_dtype_t dtype,
+                          awq_stream_t stream) {
+  awq::ReadKv4Problem p{};
+  awq_status_t st = check_half(dtype);
+  if (st == AWQ_OK) st = check_kv4(cache, &p.cache);
+  if (st != AWQ_OK) return st;
+  if (T < 0) return fail(AWQ_ERR_INVALID_ARGUMENT, "T must be >= 0 (got %lld)", (long long)T);
+  if (T > kDimLimit || T * p.cache.heads > kDimLimit) return fail(AWQ_ERR_UNSUPPORTED_SHAPE, "T * heads must be below 2^31");
+  if (T == 0) return ok();
+  if (!slots || !k || !v) return fail(AWQ_ERR_INVALID_ARGUMENT, "awq_kv4_read: null pointer");
+  if (!al(k, 2) || !al(v, 2) || !al(slots, 4)) return fail(AWQ_ERR_MISALIGNED, "k, v and slots must be aligned to their elements");
+  st = check_device();
+  if (st != AWQ_OK) return st;
+  p.slots = slots;
+  p.T = T;
+  p.k = static_cast<uint16_t*>(k);
+  p.v = static_cast<uint16_t*>(v);
+  p.bf16 = dtype == AWQ_DTYPE_BF16;
+  p.stream = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = awq::launch_read_kv4(p);
+  if (e != cudaSuccess) return cuda_fail(e, "awq_kv4_read launch");
+  return ok();
+}
+
+awq_status_t awq_attention_kv4_workspace_size(int64_t B, int64_t n, int64_t Hq, int64_t heads, int64_t D, size_t* bytes) {
+  if (!bytes) return fail(AWQ_ERR_INVALID_ARGUMENT, "null bytes pointer");
+  awq::AttentionKv4Problem p{};
+  const awq_status_t st = attention_kv4_shape(B, n, Hq, heads, D, &p);
+  if (st != AWQ_OK) return st;
+  *bytes = B * n * Hq == 0 ? 0 : awq::attention_kv4_workspace_bytes(p, sm_count());
+  return ok();
+}
+
+awq_status_t awq_attention_kv4(const void* q, int64_t B, int64_t n, int64_t Hq, int64_t q_batch_stride, int64_t q_token_stride,
+                               int64_t q_head_stride, const awq_kv4_cache_t* cache, const int32_t* pages, int64_t W,
+                               int64_t pages_stride, const int32_t* lens, int64_t window, int64_t sinks, float scale, void* out,
+                               awq_dtype_t dtype, void* workspace, size_t workspace_bytes, awq_stream_t stream) {
+  awq::AttentionKv4Problem p{};
+  awq_status_t st = check_half(dtype);
+  if (st == AWQ_OK) st = check_kv4(cache, &p.cache);
+  if (st == AWQ_OK) st = attention_kv4_shape(B, n, Hq, p.cache.heads, p.cache.head_dim, &p);
+  if (st != AWQ_OK) return st;
+  if (W < 0 || W > kDimLimit || W * p.cache.page_size > kDimLimit)
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "W * page_size must be in 0..2^31 - 1");
+  if (window < 0 || window > kDimLimit || sinks < 0 || sinks > kDimLimit)
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "window and sinks must be in 0..2^31 - 1");
+  if (B * n * Hq == 0) return ok();
+  if (!q || !out || !lens || (W && !pages)) return fail(AWQ_ERR_INVALID_ARGUMENT, "awq_attention_kv4: null pointer");
+  if (!al(q, 16) || !al(out, 16)) return fail(AWQ_ERR_MISALIGNED, "q and out must be 16-byte aligned");
+  if (B == 1) q_batch_stride = 0;
+  if (n == 1) q_token_stride = 0;
+  if (Hq == 1) q_head_stride = 0;
+  if (q_batch_stride % 8 || q_token_stride % 8 || q_head_stride % 8)
+    return fail(AWQ_ERR_MISALIGNED, "strides of q must be multiples of 8 elements");
+  if (!al(pages, 4) || !al(lens, 4)) return fail(AWQ_ERR_MISALIGNED, "pages and lens must be 4-byte aligned");
+  st = check_device();
+  if (st != AWQ_OK) return st;
+  const int sms = sm_count();
+  st = check_workspace(workspace, workspace_bytes, awq::attention_kv4_workspace_bytes(p, sms));
+  if (st != AWQ_OK) return st;
+  p.q = static_cast<const uint16_t*>(q);
+  p.q_sb = q_batch_stride;
+  p.q_sn = q_token_stride;
+  p.q_sh = q_head_stride;
+  p.pages = pages;
+  p.pages_ld = pages_stride;
+  p.W = static_cast<int>(W);
+  p.lens = lens;
+  p.window = static_cast<int>(window);
+  p.sinks = static_cast<int>(sinks);
+  p.scale = scale;
+  p.out = static_cast<uint16_t*>(out);
+  p.bf16 = dtype == AWQ_DTYPE_BF16;
+  p.workspace = workspace;
+  p.stream = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = awq::launch_attention_kv4(p, sms);
+  if (e != cudaSuccess) return cuda_fail(e, "awq_attention_kv4 launch");
+  return ok();
+}
+
+awq_status_t awq_residual_norm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride, const void* gate,
+                               int64_t gate_stride, const void* post_weight, const void* post_bias, float scale,
+                               const void* weight, const void* bias, int64_t T, int64_t W, awq_norm_t kind, float eps, void* h,
+                               void* y, awq_dtype_t dtype, awq_stream_t stream) {
+  awq_status_t st = check_half(dtype);
+  if (st != AWQ_OK) return st;
+  if (T < 0 || W < 0) return fail(AWQ_ERR_INVALID_ARGUMENT, "T and W must be >= 0");
+  if (kind != AWQ_NORM_RMS && kind != AWQ_NORM_LAYER) return fail(AWQ_ERR_INVALID_ARGUMENT, "unknown norm %d", static_cast<int>(kind));
+  if (!(eps >= 0.f) || !(eps < 1e30f)) return fail(AWQ_ERR_INVALID_ARGUMENT, "eps must be finite and >= 0");
+  if (T > kDimLimit || W > kDimLimit || T * W >= kProdLimit)
+    return fail(AWQ_ERR_UNSUPPORTED_SHAPE, "T and W must be below 2^31, T * W below 2^40");
+  if ((post_bias && !post_weight) || (bias && !weight)) return fail(AWQ_ERR_INVALID_ARGUMENT, "a bias needs its weight");
+  if (T == 0 || W == 0) return ok();
+  if (!x || !h || (weight && !y)) return fail(AWQ_ERR_INVALID_ARGUMENT, "awq_residual_norm: null pointer");
+  if (!al(x, 2) || !al(residual, 2) || !al(gate, 2) || !al(post_weight, 2) || !al(post_bias, 2) || !al(weight, 2) || !al(bias, 2) ||
+      !al(h, 2) || !al(y, 2))
+    return fail(AWQ_ERR_MISALIGNED, "16-bit tensors must be 2-byte aligned");
+  if (T == 1) x_stride = residual_stride = W;  // a dimension of one entry: its stride may be anything
+  if ((h == residual && residual_stride != W) || (weight && y == x && x_stride != W))
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "in place needs dense rows");
+  st = check_device();
+  if (st != AWQ_OK) return st;
+  const auto u16 = [](const void* t) { return static_cast<const uint16_t*>(t); };
+  const awq::ResidualNormProblem p{u16(x), u16(residual), u16(gate), x_stride, residual_stride, gate_stride, u16(post_weight),
+                                   u16(post_bias), u16(weight), u16(bias), scale, eps, T, static_cast<int>(W),
+                                   kind == AWQ_NORM_LAYER, static_cast<uint16_t*>(h), static_cast<uint16_t*>(y),
+                                   dtype == AWQ_DTYPE_BF16, reinterpret_cast<cudaStream_t>(stream)};
+  const cudaError_t e = awq::launch_residual_norm(p);
+  if (e != cudaSuccess) return cuda_fail(e, "awq_residual_norm launch");
+  return ok();
+}
+
+awq_status_t awq_moe_layer_workspace_size(int64_t T, int64_t k, int64_t I, size_t* bytes) {
+  if (!bytes) return fail(AWQ_ERR_INVALID_ARGUMENT, "null bytes pointer");
+  const awq_status_t st = moe_layer_shape(T, k, I);
+  if (st != AWQ_OK) return st;
+  *bytes = awq::moe_layer_workspace_bytes(static_cast<int>(T), static_cast<int>(k), static_cast<int>(I));
+  return ok();
+}
+
+awq_status_t awq_moe_layer(const void* x, int64_t T, int64_t H, int64_t row_stride, const int32_t* experts, const float* weights,
+                           int64_t k, int64_t E, int64_t I, int64_t group_size, const int32_t* up_qweight,
+                           const int32_t* up_qzeros, const void* up_scales, const int32_t* down_qweight,
+                           const int32_t* down_qzeros, const void* down_scales, const void* base, void* out, awq_dtype_t dtype,
+                           void* workspace, size_t workspace_bytes, awq_stream_t stream) {
+  awq_status_t st = check_half(dtype);
+  if (st == AWQ_OK) st = moe_layer_shape(T, k, I);
+  if (st != AWQ_OK) return st;
+  if (H < 0) return fail(AWQ_ERR_INVALID_ARGUMENT, "H must be >= 0 (got %lld)", (long long)H);
+  if (E < 1 || E > awq::kDispatchMaxE)
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "E must be in 1..%d (got %lld)", awq::kDispatchMaxE, (long long)E);
+  if (group_size <= 0) return fail(AWQ_ERR_INVALID_ARGUMENT, "group_size must be positive (got %lld)", (long long)group_size);
+  if (H > (1 << 30) || H * I >= kProdLimit / 2 || E * (2 * H * I) >= kProdLimit)
+    return fail(AWQ_ERR_UNSUPPORTED_SHAPE, "H must be below 2^30, E * H * 2 I below 2^40");
+  if (H % 8 || I % 8 || H % group_size || I % group_size)
+    return fail(AWQ_ERR_UNSUPPORTED_SHAPE, "H and I must be multiples of 8 and of group_size");
+  if (T == 0 || H == 0) return ok();
+  if (!x || !out || (k && (!experts || !weights))) return fail(AWQ_ERR_INVALID_ARGUMENT, "awq_moe_layer: null pointer");
+  if (k && I && (!up_qweight || !up_qzeros || !up_scales || !down_qweight || !down_qzeros || !down_scales))
+    return fail(AWQ_ERR_INVALID_ARGUMENT, "awq_moe_layer: null weights");
+  if (out == x) return fail(AWQ_ERR_INVALID_ARGUMENT, "out must not be x");
+  if (!al(x, 2) || !al(base, 2) || !al(out, 2) || !al(up_scales, 2) || !al(down_scales, 2))
+    return fail(AWQ_ERR_MISALIGNED, "16-bit tensors must be 2-byte aligned");
+  if (!al(experts, 4) || !al(weights, 4) || !al(up_qweight, 4) || !al(up_qzeros, 4) || !al(down_qweight, 4) || !al(down_qzeros, 4))
+    return fail(AWQ_ERR_MISALIGNED, "experts, weights, qweight and qzeros must be 4-byte aligned");
+  st = check_device();
+  if (st != AWQ_OK) return st;
+  st = check_workspace(workspace, workspace_bytes,
+                       awq::moe_layer_workspace_bytes(static_cast<int>(T), static_cast<int>(k), static_cast<int>(I)));
+  if (st != AWQ_OK) return st;
+  const auto stacked = [](const int32_t* qw, const int32_t* qz, const void* sc) {
+    return awq::Stacked{reinterpret_cast<const uint32_t*>(qw), reinterpret_cast<const uint32_t*>(qz), static_cast<const uint16_t*>(sc)};
+  };
+  const awq::MoeLayerProblem p{static_cast<const uint16_t*>(x), row_stride, static_cast<int>(T), static_cast<int>(H),
+                               static_cast<int>(I), static_cast<int>(E), I ? static_cast<int>(k) : 0,  // I == 0: nothing to add
+                               static_cast<int>(group_size), experts, weights, stacked(up_qweight, up_qzeros, up_scales),
+                               stacked(down_qweight, down_qzeros, down_scales), static_cast<const uint16_t*>(base),
+                               static_cast<uint16_t*>(out), dtype == AWQ_DTYPE_BF16, workspace,
+                               reinterpret_cast<cudaStream_t>(stream)};
+  const cudaError_t e = awq::launch_moe_layer(p, sm_count());
+  if (e != cudaSuccess) return cuda_fail(e, "awq_moe_layer launch");
   return ok();
 }
 
