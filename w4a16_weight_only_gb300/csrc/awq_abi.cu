@@ -1224,6 +1224,7 @@ awq_status_t awq_attention_kv4(const void* q, int64_t B, int64_t n, int64_t Hq, 
   p.scale = scale;
   p.out = static_cast<uint16_t*>(out);
   p.bf16 = dtype == AWQ_DTYPE_BF16;
+  p.give_up = g_attention_gives_up;
   p.workspace = workspace;
   p.stream = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = awq::launch_attention_kv4(p, sms);

@@ -1,84 +1,64 @@
-// Attention of the newest tokens of each sequence over a 4-bit key/value cache (awq_attention_kv4).
-#include "awq_step.cuh"
+// Host side of awq_attention_kv4: how a call is cut, its workspace, and the choice of a kernel
+// (awq_kv4_attn.cuh).
+#include "awq_kv4_attn.cuh"
 
 namespace awq {
 namespace {
 
-// One warp per output row; a lane owns quads of elements.
-template <bool kBF>
-__global__ void __launch_bounds__(128) attention_any_kernel(const AttentionKv4Problem p) {
-  const Kv4Cache& c = p.cache;
-  const int lane = threadIdx.x & 31, D = c.head_dim, G = c.groups(), quads = D / 4;
-  const int64_t row = blockIdx.x * int64_t{4} + (threadIdx.x >> 5);
-  if (row >= static_cast<int64_t>(p.B) * p.n * p.Hq) return;
-  const int h = static_cast<int>(row % p.Hq), i = static_cast<int>(row / p.Hq % p.n), b = static_cast<int>(row / p.Hq / p.n);
-  const int hk = h / (p.Hq / c.heads);
-  const uint16_t* q = p.q + b * p.q_sb + i * p.q_sn + h * p.q_sh;
-  const int len = static_cast<int>(min(static_cast<int64_t>(max(p.lens[b], 0)), static_cast<int64_t>(p.W) * c.page_size));
-  const int at = len - p.n + i;
-  float qv[2][4], o[2][4], top = -INFINITY, sum = 0.f;
-  for (int u = 0; u < 2; ++u)
-    for (int j = 0; j < 4; ++j) {
-      const int x = lane + 32 * u;
-      qv[u][j] = x < quads ? elem_to_float<kBF>(q[4 * x + j]) : 0.f;
-      o[u][j] = 0.f;
-    }
-  for (int key = 0; key <= at; ++key) {
-    if (p.window && key <= at - p.window && key >= p.sinks) {
-      key = max(p.sinks, at - p.window + 1) - 1;
-      continue;
-    }
-    const int page = p.pages[b * p.pages_ld + key / c.page_size];
-    if (page < 0 || page >= c.num_pages) continue;
-    const int token = key % c.page_size, r = token & 15;
-    const uint8_t* tile = c.data + page * c.page_stride + hk * c.head_stride + static_cast<int64_t>(token >> 4) * c.tile_bytes();
-    float v[2][4], z = 0.f;
-    for (int u = 0; u < 2; ++u) {
-      const int x = lane + 32 * u;
-      if (x >= quads) continue;
-      const uint32_t kw = *reinterpret_cast<const uint16_t*>(tile + Kv4::key_byte(D, r, 2 * x));
-      const uint32_t vw = *reinterpret_cast<const uint16_t*>(tile + 8 * D + Kv4::value_byte(D, r, 2 * x));
-      const uint16_t* kp = reinterpret_cast<const uint16_t*>(tile + 16 * D) + 2 * (r * G + 4 * x / c.group);
-      const uint16_t* vp = kp + 32 * G;
-      const float ks = elem_to_float<kBF>(kp[0]), km = elem_to_float<kBF>(kp[1]);
-      const float vs = elem_to_float<kBF>(vp[0]), vm = elem_to_float<kBF>(vp[1]);
-      for (int j = 0; j < 4; ++j) {
-        z += qv[u][j] * (static_cast<float>((kw >> (4 * j)) & 15u) * ks + km);
-        v[u][j] = static_cast<float>((vw >> (4 * j)) & 15u) * vs + vm;
-      }
-    }
-    for (int d = 16; d; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
-    z *= p.scale;
-    const float now = fmaxf(top, z);
-    const float shrink = top == -INFINITY ? 0.f : expf(top - now), e = expf(z - now);
-    top = now;
-    sum = sum * shrink + e;
-    for (int u = 0; u < 2; ++u)
-      for (int j = 0; j < 4; ++j)
-        if (lane + 32 * u < quads) o[u][j] = o[u][j] * shrink + e * v[u][j];
-  }
-  for (int u = 0; u < 2; ++u)
-    for (int j = 0; j < 4; ++j) {
-      const int x = lane + 32 * u;
-      if (x < quads) p.out[row * D + 4 * x + j] = float_to_elem<kBF>(at >= 0 ? o[u][j] / sum : 0.f);
-    }
+using namespace kv4;
+
+int row_tile(const AttentionKv4Problem& p) {  // query rows of a unit, in eights
+  const int64_t rows = static_cast<int64_t>(p.n) * (p.Hq / p.cache.heads);
+  return rows > 8 && p.cache.head_dim <= 128 ? 2 : 1;
+}
+
+size_t part_bytes(const AttentionKv4Problem& p, int nt) { return static_cast<size_t>(8 * nt) * (p.cache.head_dim + 2) * 4; }
+
+int most_blocks(const AttentionKv4Problem& p, int nt, int sms) { return sms * blocks_per_sm(p.cache.head_dim, nt); }
+
+struct Layout {
+  size_t firsts, line, bytes;  // parts first
+};
+
+Layout layout(const AttentionKv4Problem& p, int sms) {
+  const int nt = row_tile(p), grid = most_blocks(p, nt, sms);
+  Layout l;
+  l.firsts = 2 * grid * part_bytes(p, nt);
+  l.line = l.firsts + static_cast<size_t>(grid) * kWarps * part_bytes(p, nt);
+  l.bytes = l.line + (static_cast<size_t>(p.B) + 2) * 8;
+  return l;
 }
 
 }  // namespace
 
-size_t attention_kv4_workspace_bytes(const AttentionKv4Problem& p, int sms) {
-  (void)p;
-  (void)sms;
-  return 0;
-}
+size_t attention_kv4_workspace_bytes(const AttentionKv4Problem& p, int sms) { return layout(p, sms).bytes; }
 
 cudaError_t launch_attention_kv4(const AttentionKv4Problem& p, int sms) {
-  (void)sms;
-  const int64_t rows = static_cast<int64_t>(p.B) * p.n * p.Hq;
-  const unsigned blocks = static_cast<unsigned>((rows + 3) / 4);
-  if (p.bf16) attention_any_kernel<true><<<blocks, 128, 0, p.stream>>>(p);
-  else attention_any_kernel<false><<<blocks, 128, 0, p.stream>>>(p);
-  return cudaGetLastError();
+  Args a{};
+  a.p = p;
+  const cudaError_t e = status_word_ptr(&a.status);
+  if (e != cudaSuccess) return e;
+  const int nt = row_tile(p);
+  a.group = p.Hq / p.cache.heads;
+  a.row_tiles = static_cast<int>((static_cast<int64_t>(p.n) * a.group + 8 * nt - 1) / (8 * nt));
+  a.tiles_per_page = p.cache.page_size / kTileKeys;
+  a.per_min = 1;
+  const Layout l = layout(p, sms);
+  uint8_t* ws = static_cast<uint8_t*>(p.workspace);
+  a.parts = reinterpret_cast<float*>(ws);
+  a.firsts = reinterpret_cast<float*>(ws + l.firsts);
+  a.line = reinterpret_cast<int64_t*>(ws + l.line);
+  // no more blocks than the tiles that the page tables can hold give work
+  const int64_t tiles = static_cast<int64_t>(p.W) * a.tiles_per_page;                   // of a sequence, below 2^27
+  const int64_t units = static_cast<int64_t>(p.B) * p.cache.heads * a.row_tiles;        // below 2^32: B n Hq < 2^31
+  const int64_t need = units * tiles / (kWarps * a.per_min) + 1;
+  const int grid = static_cast<int>(need < most_blocks(p, nt, sms) ? need : most_blocks(p, nt, sms));
+  switch (p.cache.head_dim) {
+    case 64: return run_64(a, nt, grid);
+    case 96: return run_96(a, nt, grid);
+    case 128: return run_128(a, nt, grid);
+    default: return run_256(a, nt, grid);
+  }
 }
 
 }  // namespace awq

@@ -76,6 +76,7 @@ struct AttentionKv4Problem {
   float scale;
   uint16_t* out;  // [B, n, Hq, D]
   bool bf16;
+  bool give_up;  // self test: the kernel's bounded waits give up at once
   void* workspace;
   cudaStream_t stream;
 };
