@@ -326,7 +326,9 @@ def test_bad_pages_and_lengths_stay_inside(awq):
     bad["lens"][1] = 2 ** 31 - 1  # cut to what the pages hold
     bad["lens"][2] = -3
     out = awq.awq_attention_kv4(**bad)
-    assert torch.equal(out[0], good[0]) and (out[2] == 0).all()
+    assert (out[2] == 0).all()  # the others' lengths move where a sequence's keys are cut: equal to rounding
+    first = dict(call, q=call["q"][:1], lens=call["lens"][:1])
+    check(out[:1], first, keys[:1], values[:1], "fp16")
 
 
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
@@ -360,6 +362,19 @@ def test_all_logits_minus_infinity(awq):
     assert torch.isnan(out[0, 0, 0]).all()
 
 
+def test_waits_that_give_up(awq):
+    # as if no copy arrived in time: an error status, and the next call is right
+    call, keys, values = make(awq, 3, 1, 8, 2, 128, 128, [100, 900, 60], 16, "bf16", seed=13)
+    awq.selftest_attention_give_up(True)
+    try:
+        awq.awq_attention_kv4(**call)
+    finally:
+        awq.selftest_attention_give_up(False)
+    with pytest.raises(awq.AwqError):
+        awq.device_status()
+    check(awq.awq_attention_kv4(**call), call, keys, values, "bf16")
+
+
 def test_empty(awq):
     cache = torch.zeros((1, 2, awq.awq_kv4_page_bytes(16, 64, 64)), dtype=torch.uint8, device="cuda")
     i32 = dict(dtype=torch.int32, device="cuda")
@@ -389,8 +404,6 @@ def test_graph_and_streams(awq):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
-    call["lens"].copy_(torch.tensor([10, 900, 0, 901], dtype=torch.int32))
-    call["lens"].clamp_(max=call["pages"].shape[1] * 16)
     call["lens"].copy_(torch.tensor([10, 20, 0, 1], dtype=torch.int32))
     graph.replay()
     torch.cuda.synchronize()
