@@ -746,13 +746,14 @@ awq_status_t awq_residual_norm(const void* x, int64_t x_stride, const void* resi
  *   G, H]: stacked linears as awq_gemm_grouped takes them, G = group_size
  * A place whose id lies outside [0, E) (-1) is left out, whatever its weight.  Sums are fp32, of a token's
  * places in their order; act is rounded to the element type as the factor of the second product, the
- * result once more.  Repeated calls give the same bits.
+ * result once more.  A token with an element that is not finite gives NaN.  Repeated calls give the same
+ * bits.
  *   workspace: awq_moe_layer_workspace_size bytes, 256-byte aligned; any content.  Calls that overlap in
  *   time need workspaces of their own.
  * Requirements: 0 <= T <= 16 (more: awq_moe_dispatch and the grouped linears), 0 <= k <= 32, 1 <= E <= 4096;
  * H and I multiples of 8 and of G > 0; E * H * 2 I below 2^40.  T == 0 or H == 0: AWQ_OK, no launch.
  */
-awq_status_t awq_moe_layer_workspace_size(int64_t T, int64_t k, int64_t I, size_t* bytes);
+awq_status_t awq_moe_layer_workspace_size(int64_t T, int64_t k, int64_t H, int64_t I, size_t* bytes);
 awq_status_t awq_moe_layer(const void* x, int64_t T, int64_t H, int64_t row_stride, const int32_t* experts,
                            const float* weights, int64_t k, int64_t E, int64_t I, int64_t group_size,
                            const int32_t* up_qweight, const int32_t* up_qzeros, const void* up_scales,

@@ -156,7 +156,7 @@ def test_extreme_activations(awq):
 def test_graph_and_streams(awq):
     d = inputs(6, 4, 12, 512, 256, 128, "bf16", seed=45)
     want = awq.awq_moe_layer(**d)
-    ws = torch.empty((awq.awq_moe_layer_workspace_size(6, 4, 256),), dtype=torch.uint8, device="cuda")
+    ws = torch.empty((awq.awq_moe_layer_workspace_size(6, 4, 512, 256),), dtype=torch.uint8, device="cuda")
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         out = awq.awq_moe_layer(**d, workspace=ws)

@@ -133,8 +133,8 @@ def test_moe_layer(lib):
     assert moe(lib, ids=ODD) == MISALIGNED and moe(lib, up=ODD) == MISALIGNED and moe(lib, base=P(0x100001)) == MISALIGNED
     assert moe(lib, H=1 << 20, I=1 << 20) == SHAPE
     n = ctypes.c_size_t(0)
-    assert lib.awq_moe_layer_workspace_size(4, 2, 128, ctypes.byref(n)) == 0 and n.value >= 4 * 2 * 128 * 2
-    assert lib.awq_moe_layer_workspace_size(4, 2, 128, None) == INVALID and lib.awq_moe_layer_workspace_size(17, 2, 128, ctypes.byref(n)) == INVALID
+    assert lib.awq_moe_layer_workspace_size(4, 2, 256, 128, ctypes.byref(n)) == 0 and n.value >= 4 * 2 * 128 * 2
+    assert lib.awq_moe_layer_workspace_size(4, 2, 256, 128, None) == INVALID and lib.awq_moe_layer_workspace_size(17, 2, 256, 128, ctypes.byref(n)) == INVALID
 
 
 @pytest.mark.parametrize("D,group", [(64, 32), (64, 64), (96, 32), (128, 32), (128, 128), (256, 64)])

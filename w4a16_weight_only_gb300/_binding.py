@@ -91,7 +91,7 @@ SIGNATURES = {
                                  ctypes.c_size_t, _vp]),
     "awq_residual_norm": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _f32, _vp, _vp, _i64, _i64, _i32, _f32, _vp, _vp,
                                  _i32, _vp]),
-    "awq_moe_layer_workspace_size": (_i32, [_i64] * 3 + [_size]),
+    "awq_moe_layer_workspace_size": (_i32, [_i64] * 4 + [_size]),
     "awq_moe_layer": (_i32, [_vp, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _i64, _i64] + [_vp] * 8 + [_i32, _vp, ctypes.c_size_t,
                                                                                                     _vp]),
 }

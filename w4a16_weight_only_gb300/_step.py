@@ -277,7 +277,7 @@ def awq_moe_layer(x, weights, experts, up, down, group_size=128, base=None, out=
     handle, lib = _handle(stream, dev), _library()
     if workspace is None:
         need = ctypes.c_size_t(0)
-        _ok(lib.awq_moe_layer_workspace_size(T, k, I, need))
+        _ok(lib.awq_moe_layer_workspace_size(T, k, H, I, need))
         ws = scratch(dev, handle, need.value)
     else:
         ws = _given(workspace, dev, "x")
@@ -289,8 +289,8 @@ def awq_moe_layer(x, weights, experts, up, down, group_size=128, base=None, out=
     return out
 
 
-def awq_moe_layer_workspace_size(T, k, I) -> int:
+def awq_moe_layer_workspace_size(T, k, H, I) -> int:
     """Bytes of workspace an awq_moe_layer call of these sizes needs (host only)."""
     b = ctypes.c_size_t(0)
-    _ok(load_library().awq_moe_layer_workspace_size(T, k, I, ctypes.byref(b)))
+    _ok(load_library().awq_moe_layer_workspace_size(T, k, H, I, ctypes.byref(b)))
     return b.value

@@ -1076,13 +1076,13 @@ awq_status_t check_workspace(const void* workspace, size_t have, size_t need) {
   return AWQ_OK;
 }
 
-awq_status_t moe_layer_shape(int64_t T, int64_t k, int64_t I) {
+awq_status_t moe_layer_shape(int64_t T, int64_t k, int64_t H, int64_t I) {
   if (T < 0 || T > awq::kMoeLayerMaxT)
     return fail(AWQ_ERR_INVALID_ARGUMENT, "T must be in 0..%d (got %lld): route more tokens through awq_moe_dispatch",
                 awq::kMoeLayerMaxT, (long long)T);
   if (k < 0 || k > awq::kRouteMaxK) return fail(AWQ_ERR_INVALID_ARGUMENT, "k must be in 0..%d (got %lld)", awq::kRouteMaxK, (long long)k);
-  if (I < 0) return fail(AWQ_ERR_INVALID_ARGUMENT, "I must be >= 0 (got %lld)", (long long)I);
-  if (I >= (int64_t{1} << 30)) return fail(AWQ_ERR_UNSUPPORTED_SHAPE, "I must be below 2^30");
+  if (H < 0 || I < 0) return fail(AWQ_ERR_INVALID_ARGUMENT, "H and I must be >= 0 (got %lld, %lld)", (long long)H, (long long)I);
+  if (H >= (int64_t{1} << 30) || I >= (int64_t{1} << 30)) return fail(AWQ_ERR_UNSUPPORTED_SHAPE, "H and I must be below 2^30");
   return AWQ_OK;
 }
 
@@ -1264,11 +1264,11 @@ awq_status_t awq_residual_norm(const void* x, int64_t x_stride, const void* resi
   return ok();
 }
 
-awq_status_t awq_moe_layer_workspace_size(int64_t T, int64_t k, int64_t I, size_t* bytes) {
+awq_status_t awq_moe_layer_workspace_size(int64_t T, int64_t k, int64_t H, int64_t I, size_t* bytes) {
   if (!bytes) return fail(AWQ_ERR_INVALID_ARGUMENT, "null bytes pointer");
-  const awq_status_t st = moe_layer_shape(T, k, I);
+  const awq_status_t st = moe_layer_shape(T, k, H, I);
   if (st != AWQ_OK) return st;
-  *bytes = awq::moe_layer_workspace_bytes(static_cast<int>(T), static_cast<int>(k), static_cast<int>(I));
+  *bytes = awq::moe_layer_workspace_bytes(static_cast<int>(T), static_cast<int>(k), static_cast<int>(H), static_cast<int>(I));
   return ok();
 }
 
@@ -1278,14 +1278,13 @@ awq_status_t awq_moe_layer(const void* x, int64_t T, int64_t H, int64_t row_stri
                            const int32_t* down_qzeros, const void* down_scales, const void* base, void* out, awq_dtype_t dtype,
                            void* workspace, size_t workspace_bytes, awq_stream_t stream) {
   awq_status_t st = check_half(dtype);
-  if (st == AWQ_OK) st = moe_layer_shape(T, k, I);
+  if (st == AWQ_OK) st = moe_layer_shape(T, k, H, I);
   if (st != AWQ_OK) return st;
-  if (H < 0) return fail(AWQ_ERR_INVALID_ARGUMENT, "H must be >= 0 (got %lld)", (long long)H);
   if (E < 1 || E > awq::kDispatchMaxE)
     return fail(AWQ_ERR_INVALID_ARGUMENT, "E must be in 1..%d (got %lld)", awq::kDispatchMaxE, (long long)E);
   if (group_size <= 0) return fail(AWQ_ERR_INVALID_ARGUMENT, "group_size must be positive (got %lld)", (long long)group_size);
-  if (H > (1 << 30) || H * I >= kProdLimit / 2 || E * (2 * H * I) >= kProdLimit)
-    return fail(AWQ_ERR_UNSUPPORTED_SHAPE, "H must be below 2^30, E * H * 2 I below 2^40");
+  if (H * I >= kProdLimit / 2 || E * (2 * H * I) >= kProdLimit)
+    return fail(AWQ_ERR_UNSUPPORTED_SHAPE, "E * H * 2 I must be below 2^40");
   if (H % 8 || I % 8 || H % group_size || I % group_size)
     return fail(AWQ_ERR_UNSUPPORTED_SHAPE, "H and I must be multiples of 8 and of group_size");
   if (T == 0 || H == 0) return ok();
@@ -1300,7 +1299,7 @@ awq_status_t awq_moe_layer(const void* x, int64_t T, int64_t H, int64_t row_stri
   st = check_device();
   if (st != AWQ_OK) return st;
   st = check_workspace(workspace, workspace_bytes,
-                       awq::moe_layer_workspace_bytes(static_cast<int>(T), static_cast<int>(k), static_cast<int>(I)));
+                       awq::moe_layer_workspace_bytes(static_cast<int>(T), static_cast<int>(k), static_cast<int>(H), static_cast<int>(I)));
   if (st != AWQ_OK) return st;
   const auto stacked = [](const int32_t* qw, const int32_t* qz, const void* sc) {
     return awq::Stacked{reinterpret_cast<const uint32_t*>(qw), reinterpret_cast<const uint32_t*>(qz), static_cast<const uint16_t*>(sc)};

@@ -1,17 +1,37 @@
 // A mixture-of-experts layer of a few tokens on 4-bit experts, in two kernels (awq_moe_layer):
 //
-//   act[t, j] = silu(x[t] Wg) * (x[t] Wu)          of expert experts[t, j], fp32 to the workspace
+//   act[t, j] = silu(x[t] Wg) * (x[t] Wu)          of expert experts[t, j], rounded to the element type
 //   out[t]    = base[t] + sum_j weights[t, j] * (act[t, j] Wd)
 //
 // with  w = (code - zero) * scale  per group of G rows, sums in fp32, the result rounded once.
 #include "awq_step.cuh"
+#include "awq_ptx.cuh"
 
 namespace awq {
 namespace {
 
+constexpr int kMaxPlaces = kMoeLayerMaxT * 32;
+constexpr int kRows = 8;      // places of a job: the columns of an m16n8k16
+constexpr int kBlockK = 64;   // rows of a weight that a warp has in flight
+
+struct Layout {
+  size_t y, counters, bytes;  // offsets; act first
+};
+
+__host__ Layout layout(int T, int k, int H, int I) {
+  Layout l;
+  const auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  l.y = up(static_cast<size_t>(T) * k * I * 4);  // the kernels for any shape keep act in fp32
+  l.counters = l.y + up(static_cast<size_t>(T) * k * H * 4);
+  l.bytes = l.counters + up(static_cast<size_t>((H + 127) / 128) * 4);
+  return l;
+}
+
+// ---- any shape ----
+
 // Sum over K of x[k] * w[k][8 c + j] of one expert for the eight columns of word column c.
-template <typename F>
-__device__ __forceinline__ void dot8(const Stacked& w, int64_t e, int K, int N, int G, int c, bool bf16, F&& x, float (&acc)[8]) {
+template <bool kBF, typename F>
+__device__ __forceinline__ void dot8(const Stacked& w, int64_t e, int K, int N, int G, int c, F&& x, float (&acc)[8]) {
   const uint32_t* qw = w.qw + (e * K) * (N / 8) + c;
   const int64_t g0 = e * (K / G);
   for (int j = 0; j < 8; ++j) acc[j] = 0.f;
@@ -25,14 +45,11 @@ __device__ __forceinline__ void dot8(const Stacked& w, int64_t e, int K, int N, 
       for (int i = 0; i < 8; ++i)
         sum[nibble_column(i)] += v * static_cast<float>(static_cast<int>((word >> (4 * i)) & 15u) - static_cast<int>((z >> (4 * i)) & 15u));
     }
-    for (int j = 0; j < 8; ++j) {
-      const uint16_t s = w.sc[(g0 + g) * N + 8 * c + j];
-      acc[j] += sum[j] * (bf16 ? elem_to_float<true>(s) : elem_to_float<false>(s));
-    }
+    for (int j = 0; j < 8; ++j) acc[j] += sum[j] * elem_to_float<kBF>(w.sc[(g0 + g) * N + 8 * c + j]);
   }
 }
 
-// Any shape: one thread per (place, eight columns).
+// One thread per (place, eight columns).
 template <bool kBF>
 __global__ void __launch_bounds__(128) moe_up_any_kernel(const MoeLayerProblem p, float* act) {
   const int c = blockIdx.x * 128 + threadIdx.x, place = blockIdx.y;
@@ -42,10 +59,10 @@ __global__ void __launch_bounds__(128) moe_up_any_kernel(const MoeLayerProblem p
   const uint16_t* x = p.x + static_cast<int64_t>(place / p.k) * p.x_st;
   float gate[8], up[8];
   const auto at = [&](int k) { return elem_to_float<kBF>(x[k]); };
-  dot8(p.up, e, p.H, 2 * p.I, p.G, c, kBF, at, gate);
-  dot8(p.up, e, p.H, 2 * p.I, p.G, p.I / 8 + c, kBF, at, up);
+  dot8<kBF>(p.up, e, p.H, 2 * p.I, p.G, c, at, gate);
+  dot8<kBF>(p.up, e, p.H, 2 * p.I, p.G, p.I / 8 + c, at, up);
   for (int j = 0; j < 8; ++j)
-    act[static_cast<int64_t>(place) * p.I + 8 * c + j] = gate[j] / (1.f + expf(-gate[j])) * up[j];
+    act[static_cast<int64_t>(place) * p.I + 8 * c + j] = elem_to_float<kBF>(float_to_elem<kBF>(gate[j] / (1.f + expf(-gate[j])) * up[j]));
 }
 
 // One thread per (token, eight columns).
@@ -61,15 +78,385 @@ __global__ void __launch_bounds__(128) moe_down_any_kernel(const MoeLayerProblem
     if (e < 0 || e >= p.E) continue;
     float y[8];
     const float* a = act + static_cast<int64_t>(place) * p.I;
-    dot8(p.down, e, p.I, p.H, p.G, c, kBF, [&](int k) { return a[k]; }, y);
+    dot8<kBF>(p.down, e, p.I, p.H, p.G, c, [&](int k) { return a[k]; }, y);
     for (int i = 0; i < 8; ++i) sum[i] += p.weights[place] * y[i];
   }
   for (int j = 0; j < 8; ++j) p.out[static_cast<int64_t>(t) * p.H + 8 * c + j] = float_to_elem<kBF>(sum[j]);
 }
 
+// ---- tensor-core kernels ----
+
+// The places, eight of one expert at a time.
+struct Jobs {
+  int expert[kMaxPlaces];
+  uint16_t place[kMaxPlaces][kRows];
+  int rows[kMaxPlaces];
+  int count;
+};
+
+// Built by every block alike from the experts' ids: place p is row (rank % 8) of its expert's job rank / 8,
+// jobs in the order of their first places.
+template <int kThreads>
+__device__ void build_jobs(const MoeLayerProblem& p, Jobs& jobs, int* ids, int* head_job) {
+  const int places = p.T * p.k;
+  for (int i = threadIdx.x; i < places; i += kThreads) {
+    ids[i] = __ldg(p.experts + i);
+    jobs.rows[i] = 0;
+  }
+  __syncthreads();
+  // head_job[i]: first the head of place i's job (i itself where it is one)
+  constexpr int kPer = (kMaxPlaces + kThreads - 1) / kThreads;
+  int row[kPer];
+#pragma unroll
+  for (int n = 0; n < kPer; ++n) {
+    const int i = n * kThreads + threadIdx.x;
+    row[n] = -1;
+    if (i >= places) continue;
+    const int e = ids[i];
+    if (e < 0 || e >= p.E) {
+      head_job[i] = -1;
+      continue;
+    }
+    int rank = 0, head = i;
+    for (int q = 0; q < i; ++q)
+      if (ids[q] == e) {
+        if ((rank & (kRows - 1)) == 0) head = q;
+        ++rank;
+      }
+    row[n] = rank & (kRows - 1);
+    head_job[i] = row[n] == 0 ? i : head;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int n = 0; n < kPer; ++n) {
+    const int i = n * kThreads + threadIdx.x;
+    if (row[n] < 0) continue;
+    const int head = head_job[i];
+    int job = 0;  // heads before this one
+    for (int q = 0; q < head; ++q) job += head_job[q] == q;
+    jobs.place[job][row[n]] = static_cast<uint16_t>(i);
+    atomicAdd(&jobs.rows[job], 1);
+    if (row[n] == 0) jobs.expert[job] = ids[i];
+  }
+  if (threadIdx.x < 32) {
+    int count = 0;
+    for (int q = threadIdx.x; q < places; q += 32) count += head_job[q] == q;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) count += __shfl_xor_sync(0xffffffffu, count, d);
+    if (threadIdx.x == 0) jobs.count = count;
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ float silu(float v) { return v / (1.f + __expf(-v)); }
+
+// One product of the layer.  A unit is a job times 128 columns (kUp: 64 gate columns and their 64 up
+// columns); its K rows are cut over the block's warps.  The product is taken transposed, Y^T = W^T X^T:
+// columns of the weight fill the 16 rows of an m16n8k16, the job's places its 8 columns.  Lane (g, t) has
+// word columns g (a word is eight columns) of rows 8 t .. 8 t + 7 of every 32, so that an x fragment is part of
+// one 16-byte load and a weight fragment is four words of one column octet, bytes exchanged between pairs of
+// rows.  fp16: a pair of codes ANDed out of the words is c 2^-24 or c 2^-20, a subnormal number, exact;
+// bf16: with the exponent ORed in it is 128 + c.  The zero (and 128) leaves with the sum of x, which an
+// mma against ones gives in the same layout; a group's sums are scaled into fp32 totals.
+// Words are loaded a block of 64 rows ahead into the registers just used.
+template <bool kBF, bool kUp, int kW>
+__global__ void __launch_bounds__(kW * 32, 16 / kW) moe_kernel(const MoeLayerProblem p, uint16_t* act, float* y, int* counters) {
+  extern __shared__ float4 red[];  // [2][kW][8 quads][32 lanes]
+  __shared__ Jobs jobs;
+  __shared__ int ids[kMaxPlaces], head_job[kMaxPlaces];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int K = kUp ? p.H : p.I, N = kUp ? 2 * p.I : p.H, words = N / 8;
+  const Stacked& w = kUp ? p.up : p.down;
+  ptx::launch_dependents();
+  build_jobs<kW * 32>(p, jobs, ids, head_job);
+  if (kUp && blockIdx.x == 0)
+    for (int i = threadIdx.x; i < (p.H + 127) / 128; i += kW * 32) counters[i] = 0;
+  const int tiles = kUp ? (p.I + 63) / 64 : (p.H + 127) / 128, units = jobs.count * tiles;
+  const int blocks = K / kBlockK, b0 = blocks * warp / kW, b1 = blocks * (warp + 1) / kW;
+  const bool work = b1 > b0;
+
+  // where the lane's words of a unit begin; columns behind the last are loaded from the last and not kept
+  const auto words_of = [&](int unit, int& c0, int& c1) {
+    const int tile = unit % tiles;
+    if constexpr (kUp) {
+      c0 = min(8 * tile + g, p.I / 8 - 1);
+      c1 = p.I / 8 + c0;
+    } else {
+      c0 = min(16 * tile + 2 * g, words - 2);
+      c1 = c0 + 1;
+    }
+  };
+
+  uint32_t buf[4][4][2];  // step of 16 rows, row, octet
+  uint4 xf[2];            // eight elements of x per 32 rows
+  int pu = blockIdx.x, pb = b0;  // the next block of words to load
+  const uint32_t* src = nullptr;
+  const auto point = [&] {
+    if (pu >= units) return;
+    int c0, c1;
+    words_of(pu, c0, c1);
+    src = w.qw + (static_cast<int64_t>(jobs.expert[pu / tiles]) * K + pb * kBlockK + 8 * t) * words + c0;
+  };
+  const int apart = kUp ? p.I / 8 : 1;  // from the first octet's word to the second's
+  const auto load_step = [&](int s) {
+    if (pu >= units) return;
+    const uint32_t* at = src + static_cast<int64_t>((s >> 1) * 32 + (s & 1) * 4) * words;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (kUp) {
+        buf[s][j][0] = __ldg(at + static_cast<int64_t>(j) * words);
+        buf[s][j][1] = __ldg(at + static_cast<int64_t>(j) * words + apart);
+      } else {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(at + static_cast<int64_t>(j) * words));
+        buf[s][j][0] = v.x;
+        buf[s][j][1] = v.y;
+      }
+    }
+  };
+  const uint16_t* xrow = nullptr;
+  bool xin = false;
+  const auto point_x = [&] {
+    if (pu >= units) return;
+    const int job = pu / tiles;
+    xin = g < jobs.rows[job];
+    const int place = xin ? jobs.place[job][g] : 0;
+    xrow = kUp ? p.x + static_cast<int64_t>(place / p.k) * p.x_st : act + static_cast<int64_t>(place) * p.I;
+  };
+  const auto load_x = [&](int half) {
+    if (pu >= units) return;
+    const uint16_t* at = xrow + pb * kBlockK + half * 32 + 8 * t;
+    xf[half] = xin ? *reinterpret_cast<const uint4*>(at) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  const auto advance = [&] {
+    if (++pb == b1) {
+      pb = b0;
+      pu += gridDim.x;
+      point();
+      point_x();
+    } else {
+      src += static_cast<int64_t>(kBlockK) * words;
+    }
+  };
+  if (work) {
+    point();
+#pragma unroll
+    for (int s = 0; s < 4; ++s) load_step(s);
+  }
+  if (!kUp) ptx::grid_dependency_wait();  // act, and the counters' zeros
+  if (work) {
+    point_x();
+    load_x(0);
+    load_x(1);
+    advance();
+  }
+
+  int parity = 0;
+  for (int unit = blockIdx.x; unit < units; unit += gridDim.x, parity ^= 1) {
+    const int job = unit / tiles, tile = unit - job * tiles;
+    float total[2][4][4];  // octet, mma, fragment
+#pragma unroll
+    for (int o = 0; o < 2; ++o)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) total[o][i][0] = total[o][i][1] = total[o][i][2] = total[o][i][3] = 0.f;
+    if (work) {
+      int c[2];
+      words_of(unit, c[0], c[1]);
+      const int64_t groups = static_cast<int64_t>(jobs.expert[job]) * (K / p.G);
+      float acc[2][4][4], ones[4];
+      uint32_t zero[2];
+      uint4 scale[2];
+      bool fresh = true;
+      for (int b = b0; b < b1; ++b) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int row = b * kBlockK + half * 32;
+          if (fresh) {
+            const int64_t at = groups + row / p.G;
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+              zero[o] = __ldg(w.qz + at * words + c[o]);
+              scale[o] = __ldg(reinterpret_cast<const uint4*>(w.sc + at * N + 8 * c[o]));
+#pragma unroll
+              for (int i = 0; i < 4; ++i) acc[o][i][0] = acc[o][i][1] = acc[o][i][2] = acc[o][i][3] = 0.f;
+            }
+            ones[0] = ones[1] = ones[2] = ones[3] = 0.f;
+          }
+#pragma unroll
+          for (int odd = 0; odd < 2; ++odd) {
+            const int s = 2 * half + odd;
+            const uint32_t x0 = odd ? xf[half].z : xf[half].x, x1 = odd ? xf[half].w : xf[half].y;
+            constexpr uint32_t one = kBF ? 0x3f803f80u : 0x3c003c00u;
+            const auto mma = [&](float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+              if constexpr (kBF) ptx::mma16816_bf16(d, a0, a1, a2, a3, x0, x1);
+              else ptx::mma16816(d, a0, a1, a2, a3, x0, x1);
+            };
+            mma(ones, one, one, one, one);
+#pragma unroll
+            for (int o = 0; o < 2; ++o)
+#pragma unroll
+              for (int high = 0; high < 2; ++high) {  // columns 0, 2, 4, 6; 1, 3, 5, 7
+                const uint32_t sel = high ? 0x7632u : 0x5410u;
+                const uint32_t u = ptx::prmt(buf[s][0][o], buf[s][1][o], sel), v = ptx::prmt(buf[s][2][o], buf[s][3][o], sel);
+                if constexpr (kBF) {
+                  const auto code = [](uint32_t q, int shift) { return ptx::and_or(q >> shift, 0x000f000fu, 0x43004300u); };
+                  mma(acc[o][2 * high], code(u, 0), code(u, 8), code(v, 0), code(v, 8));
+                  mma(acc[o][2 * high + 1], code(u, 4), code(u, 12), code(v, 4), code(v, 12));
+                } else {
+                  const uint32_t u8 = u >> 8, v8 = v >> 8;
+                  mma(acc[o][2 * high], u & 0x000f000fu, u8 & 0x000f000fu, v & 0x000f000fu, v8 & 0x000f000fu);
+                  mma(acc[o][2 * high + 1], u & 0x00f000f0u, u8 & 0x00f000f0u, v & 0x00f000f0u, v8 & 0x00f000f0u);
+                }
+              }
+            load_step(s);
+          }
+          load_x(half);
+          fresh = (row + 32) % p.G == 0 || (half == 1 && b + 1 == b1);
+          if (fresh) {  // the group's sums, or as much of them as is this warp's
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+              const uint32_t sw[4] = {scale[o].x, scale[o].y, scale[o].z, scale[o].w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int second = 0; second < 2; ++second) {
+                  // mma i has columns 2 (i % 2) + i / 2 and four further
+                  const int col = 2 * (i & 1) + (i >> 1) + 4 * second, nibble = (col & 1) * 4 + (col >> 1);
+                  const float2 s2 = ptx::pair_to_float2<kBF>(sw[col >> 1]);
+                  const float s = col & 1 ? s2.y : s2.x;
+                  const float z = static_cast<float>((zero[o] >> (4 * nibble)) & 15u) + (kBF ? 128.f : 0.f);
+                  const float lift = kBF ? 1.f : i & 1 ? 1048576.f : 16777216.f;
+#pragma unroll
+                  for (int h = 0; h < 2; ++h)
+                    total[o][i][2 * second + h] += s * (acc[o][i][2 * second + h] * lift - z * ones[h]);
+                }
+            }
+          }
+        }
+        advance();
+      }
+    }
+    // the warps' sums; warp n then has mma n % 4 of octet n / 4
+    float4* mine = red + (static_cast<size_t>(parity) * kW + warp) * 256 + lane;
+#pragma unroll
+    for (int o = 0; o < 2; ++o)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mine[(4 * o + i) * 32] = make_float4(total[o][i][0], total[o][i][1], total[o][i][2], total[o][i][3]);
+    __syncthreads();  // the other half of red is written next: one barrier a unit
+    const auto sum = [&](int quad) {
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int n = 0; n < kW; ++n) {
+        const float4 u = red[(static_cast<size_t>(parity) * kW + n) * 256 + quad * 32 + lane];
+        v.x += u.x;
+        v.y += u.y;
+        v.z += u.z;
+        v.w += u.w;
+      }
+      return v;
+    };
+    if (warp < (kUp ? 4 : 8)) {
+      const int i = warp & 3, col = 2 * (i & 1) + (i >> 1);
+      const float4 a = sum(warp);
+      const float first[4] = {a.x, a.y, a.z, a.w};
+      if constexpr (kUp) {
+        const float4 b = sum(4 + warp);
+        const float second[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const int r = 2 * t + (n & 1), column = 64 * tile + 8 * g + col + 4 * (n >> 1);
+          if (r < jobs.rows[job] && column < p.I)
+            act[static_cast<int64_t>(jobs.place[job][r]) * p.I + column] = float_to_elem<kBF>(silu(first[n]) * second[n]);
+        }
+      } else {
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const int r = 2 * t + (n & 1), column = 128 * tile + 16 * g + 8 * (warp >> 2) + col + 4 * (n >> 1);
+          if (r < jobs.rows[job] && column < p.H) y[static_cast<int64_t>(jobs.place[job][r]) * p.H + column] = first[n];
+        }
+      }
+    }
+  }
+  if constexpr (!kUp) {
+    // The block that is the last with a tile of columns adds the places up, in their order.
+    __shared__ int last[kW * 32];
+    const int mine = (units - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+    __threadfence();
+    __syncthreads();
+    for (int n0 = 0; n0 < mine; n0 += kW * 32) {
+      const int n = n0 + threadIdx.x;
+      last[threadIdx.x] = -1;
+      if (n < mine) {
+        const int tile = static_cast<int>((blockIdx.x + static_cast<int64_t>(n) * gridDim.x) % tiles);
+        if (atomicAdd(counters + tile, 1) == jobs.count - 1) last[threadIdx.x] = tile;
+      }
+      __syncthreads();
+      __threadfence();
+      for (int i = 0; i < min(mine - n0, kW * 32); ++i) {
+        const int tile = last[i];
+        if (tile < 0) continue;
+        for (int v = threadIdx.x; v < p.T * 128; v += kW * 32) {
+          const int tok = v >> 7, column = 128 * tile + (v & 127);
+          if (column >= p.H) continue;
+          const int64_t at = static_cast<int64_t>(tok) * p.H + column;
+          float total = p.base ? elem_to_float<kBF>(p.base[at]) : 0.f;
+          for (int j = 0; j < p.k; ++j) {
+            const int place = tok * p.k + j;
+            if (ids[place] >= 0 && ids[place] < p.E) total += __ldg(p.weights + place) * __ldcg(y + static_cast<int64_t>(place) * p.H + column);
+          }
+          p.out[at] = float_to_elem<kBF>(total);
+        }
+      }
+      __syncthreads();
+    }
+    if (jobs.count == 0)  // no place has an expert
+      for (int64_t v = static_cast<int64_t>(blockIdx.x) * (kW * 32) + threadIdx.x; v < static_cast<int64_t>(p.T) * p.H;
+           v += static_cast<int64_t>(gridDim.x) * (kW * 32))
+        p.out[v] = p.base ? p.base[v] : 0;
+  }
+}
+
+template <bool kBF, bool kUp, int kW>
+cudaError_t launch_product(const MoeLayerProblem& p, uint16_t* act, float* y, int* counters, int grid) {
+  const auto kernel = moe_kernel<kBF, kUp, kW>;
+  constexpr int smem = 2 * kW * 256 * 16;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];  // the second product's weights are on their way before the first has ended
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kW * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = p.stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = kUp ? 0 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p, act, y, counters);
+}
+
+bool tensor_cores_fit(const MoeLayerProblem& p) {
+  const auto fits = [](const Stacked& w) { return aligned(w.qw, 16) && aligned(w.qz, 4) && aligned(w.sc, 16); };
+  return p.H % kBlockK == 0 && p.I % kBlockK == 0 && p.G % 32 == 0 && p.I > 0 && fits(p.up) && fits(p.down) && aligned(p.x, 16) &&
+         (p.x_st % 8 == 0 || p.T == 1);
+}
+
 template <bool kBF>
-cudaError_t launch(const MoeLayerProblem& p) {
-  float* act = static_cast<float*>(p.workspace);
+cudaError_t launch(const MoeLayerProblem& p, int sms) {
+  const Layout l = layout(p.T, p.k, p.H, p.I);
+  uint8_t* ws = static_cast<uint8_t*>(p.workspace);
+  if (p.k > 0 && tensor_cores_fit(p)) {
+    uint16_t* act = reinterpret_cast<uint16_t*>(ws);
+    float* y = reinterpret_cast<float*>(ws + l.y);
+    int* counters = reinterpret_cast<int*>(ws + l.counters);
+    const auto grid = [&](int64_t tiles) {
+      const int64_t units = tiles * p.T * p.k, most = 2 * static_cast<int64_t>(sms);
+      return static_cast<int>(units < 1 ? 1 : units < most ? units : most);
+    };
+    cudaError_t e = launch_product<kBF, true, 8>(p, act, y, counters, grid((p.I + 63) / 64));
+    if (e != cudaSuccess) return e;
+    return launch_product<kBF, false, 8>(p, act, y, counters, grid((p.H + 127) / 128));
+  }
+  float* act = reinterpret_cast<float*>(ws);
   if (p.k > 0 && p.I > 0) {
     moe_up_any_kernel<kBF><<<dim3((p.I / 8 + 127) / 128, p.T * p.k), 128, 0, p.stream>>>(p, act);
     const cudaError_t e = cudaGetLastError();
@@ -81,11 +468,8 @@ cudaError_t launch(const MoeLayerProblem& p) {
 
 }  // namespace
 
-size_t moe_layer_workspace_bytes(int T, int k, int I) { return static_cast<size_t>(T) * k * I * 4; }
+size_t moe_layer_workspace_bytes(int T, int k, int H, int I) { return T * k == 0 ? 0 : layout(T, k, H, I).bytes; }
 
-cudaError_t launch_moe_layer(const MoeLayerProblem& p, int sms) {
-  (void)sms;
-  return p.bf16 ? launch<true>(p) : launch<false>(p);
-}
+cudaError_t launch_moe_layer(const MoeLayerProblem& p, int sms) { return p.bf16 ? launch<true>(p, sms) : launch<false>(p, sms); }
 
 }  // namespace awq

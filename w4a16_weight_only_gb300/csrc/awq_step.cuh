@@ -122,7 +122,7 @@ cudaError_t launch_read_kv4(const ReadKv4Problem& p);
 size_t attention_kv4_workspace_bytes(const AttentionKv4Problem& p, int sms);
 cudaError_t launch_attention_kv4(const AttentionKv4Problem& p, int sms);
 cudaError_t launch_residual_norm(const ResidualNormProblem& p);
-size_t moe_layer_workspace_bytes(int T, int k, int I);
+size_t moe_layer_workspace_bytes(int T, int k, int H, int I);
 cudaError_t launch_moe_layer(const MoeLayerProblem& p, int sms);
 
 }  // namespace awq
