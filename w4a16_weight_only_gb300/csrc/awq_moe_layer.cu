@@ -86,19 +86,25 @@ __global__ void __launch_bounds__(128) moe_down_any_kernel(const MoeLayerProblem
 
 // ---- tensor-core kernels ----
 
-// The places, eight of one expert at a time.
+// The places, eight of one expert at a time, in shared memory for T k of them.
 struct Jobs {
-  int expert[kMaxPlaces];
-  uint16_t place[kMaxPlaces][kRows];
-  int rows[kMaxPlaces];
+  int* expert;
+  int* rows;
+  int* ids;                     // of the places
+  uint16_t (*place)[kRows];
   int count;
+  __device__ Jobs(uint8_t* at, int places)
+      : expert(reinterpret_cast<int*>(at)), rows(expert + places), ids(rows + places),
+        place(reinterpret_cast<uint16_t(*)[kRows]>(ids + places)), count(0) {}
+  __host__ __device__ static constexpr int bytes(int places) { return places * (3 * 4 + kRows * 2); }
 };
 
 // Built by every block alike from the experts' ids: place p is row (rank % 8) of its expert's job rank / 8,
 // jobs in the order of their first places.
 template <int kThreads>
-__device__ void build_jobs(const MoeLayerProblem& p, Jobs& jobs, int* ids, int* head_job) {
+__device__ __forceinline__ void build_jobs(const MoeLayerProblem& p, Jobs& jobs, int* head_job, int* count) {
   const int places = p.T * p.k;
+  int* ids = jobs.ids;
   for (int i = threadIdx.x; i < places; i += kThreads) {
     ids[i] = __ldg(p.experts + i);
     jobs.rows[i] = 0;
@@ -139,151 +145,195 @@ __device__ void build_jobs(const MoeLayerProblem& p, Jobs& jobs, int* ids, int* 
     if (row[n] == 0) jobs.expert[job] = ids[i];
   }
   if (threadIdx.x < 32) {
-    int count = 0;
-    for (int q = threadIdx.x; q < places; q += 32) count += head_job[q] == q;
+    int n = 0;
+    for (int q = threadIdx.x; q < places; q += 32) n += head_job[q] == q;
 #pragma unroll
-    for (int d = 16; d; d >>= 1) count += __shfl_xor_sync(0xffffffffu, count, d);
-    if (threadIdx.x == 0) jobs.count = count;
+    for (int d = 16; d; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
+    if (threadIdx.x == 0) *count = n;
   }
   __syncthreads();
+  jobs.count = *count;
 }
 
 __device__ __forceinline__ float silu(float v) { return v / (1.f + __expf(-v)); }
+
+constexpr uint64_t kWaitLimitNs = 200ull * 1000 * 1000;
+constexpr unsigned int kStatusMoeTimeout = 0x20u;
+
+struct Args {
+  MoeLayerProblem p;
+  CUtensorMap map;  // the words of this product's weights
+  uint16_t* act;
+  float* y;
+  int* counters;
+  unsigned int* status;
+};
+
+// A stage: the words of 64 rows, two boxes of eight columns of words, and for their group of rows the scales
+// and zeros of both boxes' columns.
+struct Stage {
+  static constexpr int BOX = 64 * 32, WORDS = 2 * BOX, PARAMS = 2 * 128 + 2 * 32;
+  static constexpr int scales(int o) { return o * 128; }
+  static constexpr int zeros(int o) { return 256 + o * 32; }
+};
+
+// Shared memory: the warps' sums, the rings' words, their parameters, barriers, then the jobs.
+template <int kW>
+struct Shared {
+  static constexpr int STAGES = 2;
+  static constexpr int WORDS = kW * 4096;
+  static constexpr int PARAMS = WORDS + kW * STAGES * Stage::WORDS;
+  static constexpr int BARS = PARAMS + kW * STAGES * Stage::PARAMS;
+  static constexpr int JOBS = BARS + kW * STAGES * 8;
+  static_assert(WORDS >= kMaxPlaces * 4, "the heads of the jobs are built in the sums' place");
+};
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(ptx::smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(ptx::smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void box_load(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %4, %5}], [%2];" ::"r"(
+          ptx::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(ptx::smem_u32(bar)), "r"(x), "r"(0), "r"(w)
+      : "memory");
+}
 
 // One product of the layer.  A unit is a job times 128 columns (kUp: 64 gate columns and their 64 up
 // columns); its K rows are cut over the block's warps.  The product is taken transposed, Y^T = W^T X^T:
 // columns of the weight fill the 16 rows of an m16n8k16, the job's places its 8 columns.  Lane (g, t) has
 // word columns g (a word is eight columns) of rows 8 t .. 8 t + 7 of every 32, so that an x fragment is part of
 // one 16-byte load and a weight fragment is four words of one column octet, bytes exchanged between pairs of
-// rows.  fp16: a pair of codes ANDed out of the words is c 2^-24 or c 2^-20, a subnormal number, exact;
+// rows; the boxes come with the rows 8 t + i of the four t side by side, so that a warp reads 128 bytes in a
+// row.  fp16: a pair of codes ANDed out of the words is c 2^-24 or c 2^-20, a subnormal number, exact;
 // bf16: with the exponent ORed in it is 128 + c.  The zero (and 128) leaves with the sum of x, which an
 // mma against ones gives in the same layout; a group's sums are scaled into fp32 totals.
-// Words are loaded a block of 64 rows ahead into the registers just used.
+// Each warp has a ring of stages of its own, filled by TMA across units.
 template <bool kBF, bool kUp, int kW>
-__global__ void __launch_bounds__(kW * 32, 16 / kW) moe_kernel(const MoeLayerProblem p, uint16_t* act, float* y, int* counters) {
-  extern __shared__ float4 red[];  // [2][kW][8 quads][32 lanes]
-  __shared__ Jobs jobs;
-  __shared__ int ids[kMaxPlaces], head_job[kMaxPlaces];
+__global__ void __launch_bounds__(kW * 32, 16 / kW) moe_kernel(const __grid_constant__ Args args) {
+  using SH = Shared<kW>;
+  constexpr int STAGES = SH::STAGES;
+  extern __shared__ __align__(128) uint8_t smem[];
+  float4* red = reinterpret_cast<float4*>(smem);  // [kW][8 quads][32 lanes]
+  __shared__ int job_count;
+  const MoeLayerProblem& p = args.p;
+  Jobs jobs(smem + SH::JOBS, p.T * p.k);
+  uint16_t* act = args.act;
+  float* y = args.y;
+  int* counters = args.counters;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int K = kUp ? p.H : p.I, N = kUp ? 2 * p.I : p.H, words = N / 8;
   const Stacked& w = kUp ? p.up : p.down;
   ptx::launch_dependents();
-  build_jobs<kW * 32>(p, jobs, ids, head_job);
+  uint8_t* ring = smem + SH::WORDS + warp * (STAGES * Stage::WORDS);
+  uint8_t* params = smem + SH::PARAMS + warp * (STAGES * Stage::PARAMS);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + SH::BARS) + warp * STAGES;
+  if (lane == 0) {
+    for (int s = 0; s < STAGES; ++s) ptx::mbar_init(&full[s], 1);
+    ptx::fence_mbar_init();
+  }
+  build_jobs<kW * 32>(p, jobs, reinterpret_cast<int*>(smem), &job_count);
   if (kUp && blockIdx.x == 0)
     for (int i = threadIdx.x; i < (p.H + 127) / 128; i += kW * 32) counters[i] = 0;
-  const int tiles = kUp ? (p.I + 63) / 64 : (p.H + 127) / 128, units = jobs.count * tiles;
+  const int tiles = kUp ? p.I / 64 : (p.H + 127) / 128, units = jobs.count * tiles;
   const int blocks = K / kBlockK, b0 = blocks * warp / kW, b1 = blocks * (warp + 1) / kW;
   const bool work = b1 > b0;
 
-  // where the lane's words of a unit begin; columns behind the last are loaded from the last and not kept
-  const auto words_of = [&](int unit, int& c0, int& c1) {
-    const int tile = unit % tiles;
-    if constexpr (kUp) {
-      c0 = min(8 * tile + g, p.I / 8 - 1);
-      c1 = p.I / 8 + c0;
-    } else {
-      c0 = min(16 * tile + 2 * g, words - 2);
-      c1 = c0 + 1;
+  // ---- what is loaded next: block pb of unit pu ----
+  int pu = blockIdx.x, pb = b0;
+  const auto issue = [&](int stage) {
+    if (lane == 0) {
+      const int job = pu / tiles, tile = pu - job * tiles, e = jobs.expert[job];
+      const int c0 = kUp ? 8 * tile : 16 * tile;
+      const int c1 = kUp ? p.I / 8 + c0 : c0 + 8 < words ? c0 + 8 : c0;  // half a tile at the end: its columns are not kept
+      uint8_t* to = ring + stage * Stage::WORDS;
+      uint8_t* to_params = params + stage * Stage::PARAMS;
+      uint64_t* bar = &full[stage];
+      ptx::mbar_arrive_expect_tx(bar, Stage::WORDS + Stage::PARAMS);
+      const int slab = e * (K / 32) + pb * (kBlockK / 32);
+      box_load(to, &args.map, bar, c0, slab);
+      box_load(to + Stage::BOX, &args.map, bar, c1, slab);
+      const int64_t at = static_cast<int64_t>(e) * (K / p.G) + pb * kBlockK / p.G;
+      bulk_load(to_params + Stage::scales(0), w.sc + at * N + 8 * c0, 128, bar);
+      bulk_load(to_params + Stage::scales(1), w.sc + at * N + 8 * c1, 128, bar);
+      bulk_load(to_params + Stage::zeros(0), w.qz + at * words + c0, 32, bar);
+      bulk_load(to_params + Stage::zeros(1), w.qz + at * words + c1, 32, bar);
     }
-  };
-
-  uint32_t buf[4][4][2];  // step of 16 rows, row, octet
-  uint4 xf[2];            // eight elements of x per 32 rows
-  int pu = blockIdx.x, pb = b0;  // the next block of words to load
-  const uint32_t* src = nullptr;
-  const auto point = [&] {
-    if (pu >= units) return;
-    int c0, c1;
-    words_of(pu, c0, c1);
-    src = w.qw + (static_cast<int64_t>(jobs.expert[pu / tiles]) * K + pb * kBlockK + 8 * t) * words + c0;
-  };
-  const int apart = kUp ? p.I / 8 : 1;  // from the first octet's word to the second's
-  const auto load_step = [&](int s) {
-    if (pu >= units) return;
-    const uint32_t* at = src + static_cast<int64_t>((s >> 1) * 32 + (s & 1) * 4) * words;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (kUp) {
-        buf[s][j][0] = __ldg(at + static_cast<int64_t>(j) * words);
-        buf[s][j][1] = __ldg(at + static_cast<int64_t>(j) * words + apart);
-      } else {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(at + static_cast<int64_t>(j) * words));
-        buf[s][j][0] = v.x;
-        buf[s][j][1] = v.y;
-      }
-    }
-  };
-  const uint16_t* xrow = nullptr;
-  bool xin = false;
-  const auto point_x = [&] {
-    if (pu >= units) return;
-    const int job = pu / tiles;
-    xin = g < jobs.rows[job];
-    const int place = xin ? jobs.place[job][g] : 0;
-    xrow = kUp ? p.x + static_cast<int64_t>(place / p.k) * p.x_st : act + static_cast<int64_t>(place) * p.I;
-  };
-  const auto load_x = [&](int half) {
-    if (pu >= units) return;
-    const uint16_t* at = xrow + pb * kBlockK + half * 32 + 8 * t;
-    xf[half] = xin ? *reinterpret_cast<const uint4*>(at) : make_uint4(0u, 0u, 0u, 0u);
-  };
-  const auto advance = [&] {
+    __syncwarp();
     if (++pb == b1) {
       pb = b0;
       pu += gridDim.x;
-      point();
-      point_x();
-    } else {
-      src += static_cast<int64_t>(kBlockK) * words;
     }
   };
-  if (work) {
-    point();
-#pragma unroll
-    for (int s = 0; s < 4; ++s) load_step(s);
-  }
-  if (!kUp) ptx::grid_dependency_wait();  // act, and the counters' zeros
-  if (work) {
-    point_x();
-    load_x(0);
-    load_x(1);
-    advance();
-  }
+  int loaded = 0, used = 0;
+  if (work)
+    for (; loaded < STAGES && pu < units; ++loaded) issue(loaded);
 
-  int parity = 0;
-  for (int unit = blockIdx.x; unit < units; unit += gridDim.x, parity ^= 1) {
+  // x of block b of a unit: eight elements of the lane's place per 32 rows
+  const auto row_of = [&](int unit) -> const uint16_t* {
+    const int job = unit / tiles;
+    if (g >= jobs.rows[job]) return nullptr;
+    const int place = jobs.place[job][g];
+    return (kUp ? p.x + static_cast<int64_t>(place / p.k) * p.x_st : act + static_cast<int64_t>(place) * p.I) + 8 * t;
+  };
+  const auto load_x = [&](const uint16_t* row, int b, uint4 (&v)[2]) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+      v[half] = row ? *reinterpret_cast<const uint4*>(row + b * kBlockK + 32 * half) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  // Block number n of this warp has arrived: a bounded wait, the clock read before the test that decides.
+  const auto arrived = [&](int n) -> bool {
+    const uint32_t parity = static_cast<uint32_t>(n / STAGES) & 1u;
+    uint64_t* bar = &full[n % STAGES];
+    const auto there = [&] { return __all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity)) != 0; };
+    if (there()) return true;
+    const uint64_t t0 = ptx::globaltimer_ns();
+    while (true) {
+      const bool late = __any_sync(0xffffffffu, ptx::globaltimer_ns() - t0 > kWaitLimitNs);
+      if (there()) return true;
+      if (late) return false;
+    }
+  };
+
+  if (!kUp) ptx::grid_dependency_wait();  // act, and the counters' zeros
+  bool gave_up = false;
+  uint4 next_x[2];
+  if (work && blockIdx.x < units) load_x(row_of(blockIdx.x), b0, next_x);
+  for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
     const int job = unit / tiles, tile = unit - job * tiles;
     float total[2][4][4];  // octet, mma, fragment
 #pragma unroll
     for (int o = 0; o < 2; ++o)
 #pragma unroll
       for (int i = 0; i < 4; ++i) total[o][i][0] = total[o][i][1] = total[o][i][2] = total[o][i][3] = 0.f;
-    if (work) {
-      int c[2];
-      words_of(unit, c[0], c[1]);
-      const int64_t groups = static_cast<int64_t>(jobs.expert[job]) * (K / p.G);
+    if (work && !gave_up) {
+      const uint16_t* row_x = row_of(unit);
       float acc[2][4][4], ones[4];
-      uint32_t zero[2];
-      uint4 scale[2];
       bool fresh = true;
       for (int b = b0; b < b1; ++b) {
+        const uint4 xf[2] = {next_x[0], next_x[1]};
+        if (b + 1 < b1) load_x(row_x, b + 1, next_x);
+        else if (unit + gridDim.x < units) load_x(row_of(unit + gridDim.x), b0, next_x);
+        if (!arrived(used)) {
+          gave_up = true;
+          break;
+        }
+        const int stage = used % STAGES;
+        const uint8_t* at = ring + stage * Stage::WORDS;
+        const uint8_t* from = params + stage * Stage::PARAMS;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const int row = b * kBlockK + half * 32;
           if (fresh) {
-            const int64_t at = groups + row / p.G;
 #pragma unroll
-            for (int o = 0; o < 2; ++o) {
-              zero[o] = __ldg(w.qz + at * words + c[o]);
-              scale[o] = __ldg(reinterpret_cast<const uint4*>(w.sc + at * N + 8 * c[o]));
+            for (int o = 0; o < 2; ++o)
 #pragma unroll
               for (int i = 0; i < 4; ++i) acc[o][i][0] = acc[o][i][1] = acc[o][i][2] = acc[o][i][3] = 0.f;
-            }
             ones[0] = ones[1] = ones[2] = ones[3] = 0.f;
           }
 #pragma unroll
           for (int odd = 0; odd < 2; ++odd) {
-            const int s = 2 * half + odd;
             const uint32_t x0 = odd ? xf[half].z : xf[half].x, x1 = odd ? xf[half].w : xf[half].y;
             constexpr uint32_t one = kBF ? 0x3f803f80u : 0x3c003c00u;
             const auto mma = [&](float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
@@ -292,11 +342,13 @@ __global__ void __launch_bounds__(kW * 32, 16 / kW) moe_kernel(const MoeLayerPro
             };
             mma(ones, one, one, one, one);
 #pragma unroll
-            for (int o = 0; o < 2; ++o)
+            for (int o = 0; o < 2; ++o) {
+              const uint32_t* word = reinterpret_cast<const uint32_t*>(at + o * Stage::BOX + half * 1024 + odd * 512) + 8 * t + g;
+              const uint32_t w0 = word[0], w1 = word[32], w2 = word[64], w3 = word[96];
 #pragma unroll
               for (int high = 0; high < 2; ++high) {  // columns 0, 2, 4, 6; 1, 3, 5, 7
                 const uint32_t sel = high ? 0x7632u : 0x5410u;
-                const uint32_t u = ptx::prmt(buf[s][0][o], buf[s][1][o], sel), v = ptx::prmt(buf[s][2][o], buf[s][3][o], sel);
+                const uint32_t u = ptx::prmt(w0, w1, sel), v = ptx::prmt(w2, w3, sel);
                 if constexpr (kBF) {
                   const auto code = [](uint32_t q, int shift) { return ptx::and_or(q >> shift, 0x000f000fu, 0x43004300u); };
                   mma(acc[o][2 * high], code(u, 0), code(u, 8), code(v, 0), code(v, 8));
@@ -307,14 +359,21 @@ __global__ void __launch_bounds__(kW * 32, 16 / kW) moe_kernel(const MoeLayerPro
                   mma(acc[o][2 * high + 1], u & 0x00f000f0u, u8 & 0x00f000f0u, v & 0x00f000f0u, v8 & 0x00f000f0u);
                 }
               }
-            load_step(s);
+            }
           }
-          load_x(half);
-          fresh = (row + 32) % p.G == 0 || (half == 1 && b + 1 == b1);
+          fresh = (b * kBlockK + half * 32 + 32) % p.G == 0 || (half == 1 && b + 1 == b1);
           if (fresh) {  // the group's sums, or as much of them as is this warp's
 #pragma unroll
             for (int o = 0; o < 2; ++o) {
-              const uint32_t sw[4] = {scale[o].x, scale[o].y, scale[o].z, scale[o].w};
+              uint4 scale = *reinterpret_cast<const uint4*>(from + Stage::scales(o) + 16 * g);
+              uint32_t zero = *reinterpret_cast<const uint32_t*>(from + Stage::zeros(o) + 4 * g);
+              if (half && p.G == 32) {  // the block's second group
+                const int64_t group = static_cast<int64_t>(jobs.expert[job]) * (K / 32) + 2 * b + 1;
+                const int c = min((kUp ? 8 : 16) * tile + (o ? kUp ? p.I / 8 : 8 : 0) + g, words - 1);
+                scale = __ldg(reinterpret_cast<const uint4*>(w.sc + group * N + 8 * c));
+                zero = __ldg(w.qz + group * words + c);
+              }
+              const uint32_t sw[4] = {scale.x, scale.y, scale.z, scale.w};
 #pragma unroll
               for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -323,7 +382,7 @@ __global__ void __launch_bounds__(kW * 32, 16 / kW) moe_kernel(const MoeLayerPro
                   const int col = 2 * (i & 1) + (i >> 1) + 4 * second, nibble = (col & 1) * 4 + (col >> 1);
                   const float2 s2 = ptx::pair_to_float2<kBF>(sw[col >> 1]);
                   const float s = col & 1 ? s2.y : s2.x;
-                  const float z = static_cast<float>((zero[o] >> (4 * nibble)) & 15u) + (kBF ? 128.f : 0.f);
+                  const float z = static_cast<float>((zero >> (4 * nibble)) & 15u) + (kBF ? 128.f : 0.f);
                   const float lift = kBF ? 1.f : i & 1 ? 1048576.f : 16777216.f;
 #pragma unroll
                   for (int h = 0; h < 2; ++h)
@@ -332,21 +391,27 @@ __global__ void __launch_bounds__(kW * 32, 16 / kW) moe_kernel(const MoeLayerPro
             }
           }
         }
-        advance();
+        __syncwarp();  // the stage has been read
+        ++used;
+        if (pu < units) {
+          issue(stage);
+          ++loaded;
+        }
       }
     }
     // the warps' sums; warp n then has mma n % 4 of octet n / 4
-    float4* mine = red + (static_cast<size_t>(parity) * kW + warp) * 256 + lane;
+    __syncthreads();  // the last unit's sums have been read
+    float4* mine = red + warp * 256 + lane;
 #pragma unroll
     for (int o = 0; o < 2; ++o)
 #pragma unroll
       for (int i = 0; i < 4; ++i) mine[(4 * o + i) * 32] = make_float4(total[o][i][0], total[o][i][1], total[o][i][2], total[o][i][3]);
-    __syncthreads();  // the other half of red is written next: one barrier a unit
+    __syncthreads();
     const auto sum = [&](int quad) {
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int n = 0; n < kW; ++n) {
-        const float4 u = red[(static_cast<size_t>(parity) * kW + n) * 256 + quad * 32 + lane];
+        const float4 u = red[n * 256 + quad * 32 + lane];
         v.x += u.x;
         v.y += u.y;
         v.z += u.z;
@@ -364,17 +429,20 @@ __global__ void __launch_bounds__(kW * 32, 16 / kW) moe_kernel(const MoeLayerPro
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
           const int r = 2 * t + (n & 1), column = 64 * tile + 8 * g + col + 4 * (n >> 1);
-          if (r < jobs.rows[job] && column < p.I)
-            act[static_cast<int64_t>(jobs.place[job][r]) * p.I + column] = float_to_elem<kBF>(silu(first[n]) * second[n]);
+          if (r < jobs.rows[job]) act[static_cast<int64_t>(jobs.place[job][r]) * p.I + column] = float_to_elem<kBF>(silu(first[n]) * second[n]);
         }
       } else {
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-          const int r = 2 * t + (n & 1), column = 128 * tile + 16 * g + 8 * (warp >> 2) + col + 4 * (n >> 1);
+          const int r = 2 * t + (n & 1), column = 128 * tile + 64 * (warp >> 2) + 8 * g + col + 4 * (n >> 1);
           if (r < jobs.rows[job] && column < p.H) y[static_cast<int64_t>(jobs.place[job][r]) * p.H + column] = first[n];
         }
       }
     }
+  }
+  if (gave_up) {  // its copies in flight land first
+    if (lane == 0) atomicOr(args.status, kStatusMoeTimeout);
+    for (; used < loaded; ++used) arrived(used);
   }
   if constexpr (!kUp) {
     // The block that is the last with a tile of columns adds the places up, in their order.
@@ -401,7 +469,7 @@ __global__ void __launch_bounds__(kW * 32, 16 / kW) moe_kernel(const MoeLayerPro
           float total = p.base ? elem_to_float<kBF>(p.base[at]) : 0.f;
           for (int j = 0; j < p.k; ++j) {
             const int place = tok * p.k + j;
-            if (ids[place] >= 0 && ids[place] < p.E) total += __ldg(p.weights + place) * __ldcg(y + static_cast<int64_t>(place) * p.H + column);
+            if (jobs.ids[place] >= 0 && jobs.ids[place] < p.E) total += __ldg(p.weights + place) * __ldcg(y + static_cast<int64_t>(place) * p.H + column);
           }
           p.out[at] = float_to_elem<kBF>(total);
         }
@@ -415,10 +483,19 @@ __global__ void __launch_bounds__(kW * 32, 16 / kW) moe_kernel(const MoeLayerPro
   }
 }
 
+// The words of a product's weights as [32 rows][row % 8][row / 8 % 4][word] for boxes of 64 rows of eight words.
+bool make_map(CUtensorMap* map, const Stacked& w, int E, int K, int N) {
+  const uint64_t row = static_cast<uint64_t>(N) / 2;  // bytes
+  const uint64_t dims[4] = {static_cast<uint64_t>(N) / 8, 4, 8, static_cast<uint64_t>(E) * (K / 32)};
+  const uint64_t strides[3] = {8 * row, row, 32 * row};
+  const uint32_t box[4] = {8, 4, 8, kBlockK / 32};
+  return make_tmap_4d(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, w.qw, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
 template <bool kBF, bool kUp, int kW>
-cudaError_t launch_product(const MoeLayerProblem& p, uint16_t* act, float* y, int* counters, int grid) {
+cudaError_t launch_product(const Args& args, int grid) {
   const auto kernel = moe_kernel<kBF, kUp, kW>;
-  constexpr int smem = 2 * kW * 256 * 16;
+  const int smem = Shared<kW>::JOBS + Jobs::bytes(args.p.T * args.p.k);
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];  // the second product's weights are on their way before the first has ended
@@ -428,33 +505,42 @@ cudaError_t launch_product(const MoeLayerProblem& p, uint16_t* act, float* y, in
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kW * 32);
   cfg.dynamicSmemBytes = smem;
-  cfg.stream = p.stream;
+  cfg.stream = args.p.stream;
   cfg.attrs = attr;
   cfg.numAttrs = kUp ? 0 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p, act, y, counters);
+  return cudaLaunchKernelEx(&cfg, kernel, args);
 }
 
 bool tensor_cores_fit(const MoeLayerProblem& p) {
-  const auto fits = [](const Stacked& w) { return aligned(w.qw, 16) && aligned(w.qz, 4) && aligned(w.sc, 16); };
-  return p.H % kBlockK == 0 && p.I % kBlockK == 0 && p.G % 32 == 0 && p.I > 0 && fits(p.up) && fits(p.down) && aligned(p.x, 16) &&
-         (p.x_st % 8 == 0 || p.T == 1);
+  const auto fits = [](const Stacked& w) { return aligned(w.qw, 16) && aligned(w.qz, 16) && aligned(w.sc, 16); };
+  return p.k > 0 && p.H % kBlockK == 0 && p.I % kBlockK == 0 && (p.G == 32 || p.G % 64 == 0) && fits(p.up) && fits(p.down) &&
+         aligned(p.x, 16) && (p.x_st % 8 == 0 || p.T == 1) && static_cast<int64_t>(p.E) * (p.H > p.I ? p.H : p.I) < (int64_t{1} << 31);
 }
 
 template <bool kBF>
 cudaError_t launch(const MoeLayerProblem& p, int sms) {
   const Layout l = layout(p.T, p.k, p.H, p.I);
   uint8_t* ws = static_cast<uint8_t*>(p.workspace);
-  if (p.k > 0 && tensor_cores_fit(p)) {
-    uint16_t* act = reinterpret_cast<uint16_t*>(ws);
-    float* y = reinterpret_cast<float*>(ws + l.y);
-    int* counters = reinterpret_cast<int*>(ws + l.counters);
+  Args up{}, down{};
+  if (tensor_cores_fit(p) && make_map(&up.map, p.up, p.E, p.H, 2 * p.I) && make_map(&down.map, p.down, p.E, p.I, p.H)) {
+    up.p = p;
+    up.act = reinterpret_cast<uint16_t*>(ws);
+    up.y = reinterpret_cast<float*>(ws + l.y);
+    up.counters = reinterpret_cast<int*>(ws + l.counters);
+    cudaError_t e = status_word_ptr(&up.status);
+    if (e != cudaSuccess) return e;
+    down.p = p;
+    down.act = up.act;
+    down.y = up.y;
+    down.counters = up.counters;
+    down.status = up.status;
     const auto grid = [&](int64_t tiles) {
       const int64_t units = tiles * p.T * p.k, most = 2 * static_cast<int64_t>(sms);
-      return static_cast<int>(units < 1 ? 1 : units < most ? units : most);
+      return static_cast<int>(units < most ? units : most);
     };
-    cudaError_t e = launch_product<kBF, true, 8>(p, act, y, counters, grid((p.I + 63) / 64));
+    e = launch_product<kBF, true, 8>(up, grid(p.I / 64));
     if (e != cudaSuccess) return e;
-    return launch_product<kBF, false, 8>(p, act, y, counters, grid((p.H + 127) / 128));
+    return launch_product<kBF, false, 8>(down, grid((p.H + 127) / 128));
   }
   float* act = reinterpret_cast<float*>(ws);
   if (p.k > 0 && p.I > 0) {
