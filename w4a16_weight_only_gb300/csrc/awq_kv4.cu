@@ -10,6 +10,7 @@
 // / (s / 2): the same quotient, without overflow for bf16.  A group with an infinity or a NaN has no
 // codes: its minimum and scale are NaN, and all of it reads NaN.
 #include "awq_step.cuh"
+#include "awq_ptx.cuh"
 
 namespace awq {
 namespace {
@@ -26,6 +27,25 @@ __device__ __forceinline__ uint8_t* tile_of(const Kv4Cache& c, int slot, int hea
 }
 
 __device__ __forceinline__ float quiet_nan() { return __int_as_float(0x7fffffff); }
+
+// Codes of a group of elements within low .. high.
+template <bool kBF>
+struct Quantizer {
+  uint16_t sb, mb;
+  float low, s;
+  __device__ __forceinline__ Quantizer(float lo, float hi, bool bad) : low(lo) {
+    const uint16_t nan = float_to_elem<kBF>(quiet_nan());
+    sb = bad ? nan : float_to_elem<kBF>(__fdiv_rn(__fsub_rn(hi * 0.5f, lo * 0.5f), 7.5f));
+    mb = bad ? nan : float_to_elem<kBF>(lo);
+    s = elem_to_float<kBF>(sb);
+  }
+  __device__ __forceinline__ uint32_t code(float x) const {
+    if (!(s > 0.f)) return 0u;
+    const float c = rintf(__fdiv_rn(__fsub_rn(x * 0.5f, low * 0.5f), s * 0.5f));
+    return static_cast<uint32_t>(fminf(fmaxf(c, 0.f), 15.f));
+  }
+  __device__ __forceinline__ uint32_t params() const { return sb | (static_cast<uint32_t>(mb) << 16); }
+};
 
 // Elements 4 x .. 4 x + 3 of a head of token t, rotated and rounded to the element type.
 template <bool kBF>
@@ -46,10 +66,10 @@ __device__ __forceinline__ void load_quad(const AppendKv4Problem& p, const uint1
   }
 }
 
-// One warp per (token, head): query heads first, then key heads, then value heads.  A lane owns quads of
+// Any size, stride and alignment: one warp per (token, head), query heads first, then key heads, then value heads.  A lane owns quads of
 // elements, so a group is 8, 16 or 32 neighbouring lanes.
 template <bool kBF>
-__global__ void __launch_bounds__(256) append_kernel(const AppendKv4Problem p) {
+__global__ void __launch_bounds__(256) append_any_kernel(const AppendKv4Problem p) {
   const int heads = p.Hq + 2 * p.Hkv, lane = threadIdx.x & 31;
   const int64_t item = blockIdx.x * int64_t{8} + (threadIdx.x >> 5);
   const int64_t t = item / heads;
@@ -111,30 +131,23 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendKv4Problem p) {
       high = fmaxf(high, __shfl_xor_sync(kFull, high, d));
       bad |= __shfl_xor_sync(kFull, bad ? 1 : 0, d) != 0;
     }
-    const float range = __fsub_rn(high * 0.5f, low * 0.5f);
-    const uint16_t sb = bad ? float_to_elem<kBF>(quiet_nan()) : float_to_elem<kBF>(__fdiv_rn(range, 7.5f));
-    const float s = elem_to_float<kBF>(sb);
+    const Quantizer<kBF> quantizer(low, high, bad);
     uint32_t word = 0;
-    if (s > 0.f) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float c = rintf(__fdiv_rn(__fsub_rn(f[j] * 0.5f, low * 0.5f), s * 0.5f));
-        word |= static_cast<uint32_t>(fminf(fmaxf(c, 0.f), 15.f)) << (4 * j);
-      }
-    }
+    for (int j = 0; j < 4; ++j) word |= quantizer.code(f[j]) << (4 * j);
     if (!in) continue;
     *reinterpret_cast<uint16_t*>(codes + (value ? Kv4::value_byte(p.D, row, 2 * x) : Kv4::key_byte(p.D, row, 2 * x))) =
         static_cast<uint16_t>(word);
     if (x % per == 0) {
-      params[2 * (x / per)] = sb;
-      params[2 * (x / per) + 1] = bad ? sb : float_to_elem<kBF>(low);
+      params[2 * (x / per)] = quantizer.sb;
+      params[2 * (x / per) + 1] = quantizer.mb;
     }
   }
 }
 
-// One warp per (token, head).
+// Any alignment: one warp per (token, head).
 template <bool kBF>
-__global__ void __launch_bounds__(256) read_kernel(const ReadKv4Problem p) {
+__global__ void __launch_bounds__(256) read_any_kernel(const ReadKv4Problem p) {
   const Kv4Cache& c = p.cache;
   const int lane = threadIdx.x & 31, D = c.head_dim, G = c.groups();
   const int64_t item = blockIdx.x * int64_t{8} + (threadIdx.x >> 5);
@@ -163,6 +176,200 @@ __global__ void __launch_bounds__(256) read_kernel(const ReadKv4Problem p) {
   }
 }
 
+// Aligned tensors, a rotated part of whole vector pairs.  A thread owns vector x (eight elements) of a head
+// and keeps its cosines and sines; it goes through the heads, rows of D / 8 threads side by side, first the
+// query heads (rotated and written), then keys and values, whose groups are 4, 8 or 16 neighbouring lanes.  A
+// vector's codes are one word of the keys, half a word each of two of the values.
+constexpr int kThreads = 128;
+
+template <bool kBF>
+__device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 e = ptx::pair_to_float2<kBF>(w[j]);
+    f[2 * j] = e.x;
+    f[2 * j + 1] = e.y;
+  }
+}
+
+template <bool kBF>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  return static_cast<uint32_t>(float_to_elem<kBF>(lo)) | (static_cast<uint32_t>(float_to_elem<kBF>(hi)) << 16);
+}
+
+template <bool kBF, bool kInterleaved>
+__global__ void __launch_bounds__(kThreads) append_vec_kernel(const AppendKv4Problem p, int q_parts, int q_per, int kv_per) {
+  const int L = p.D / 8, R = kThreads / L;  // threads of a row, rows of the block
+  const int x = threadIdx.x % L, row = threadIdx.x / L;
+  const int64_t t = blockIdx.x;
+  const bool turns = p.table && 8 * x < p.rot;
+  const int half = p.rot / 16;  // vectors of half the rotated part
+  const bool second = !kInterleaved && x >= half;
+  float cs[8], sn[8];  // interleaved: four of each
+  if (turns) {
+    const int pos = __ldg(p.positions + t);
+    if (pos >= 0 && pos < p.max_position) {
+      const float* line = p.table + static_cast<int64_t>(pos) * p.rot + (kInterleaved ? 4 * x : 8 * (second ? x - half : x));
+      *reinterpret_cast<float4*>(cs) = __ldg(reinterpret_cast<const float4*>(line));
+      *reinterpret_cast<float4*>(sn) = __ldg(reinterpret_cast<const float4*>(line + p.rot / 2));
+      if constexpr (!kInterleaved) {
+        *reinterpret_cast<float4*>(cs + 4) = __ldg(reinterpret_cast<const float4*>(line + 4));
+        *reinterpret_cast<float4*>(sn + 4) = __ldg(reinterpret_cast<const float4*>(line + p.rot / 2 + 4));
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) cs[j] = sn[j] = quiet_nan();
+    }
+  }
+  const auto own = [&](const uint16_t* src) { return *(reinterpret_cast<const uint4*>(src) + x); };
+  const auto other = [&](const uint16_t* src) {  // the vector of the pairs' other elements
+    return !kInterleaved && turns ? *(reinterpret_cast<const uint4*>(src) + (second ? x - half : x + half)) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  const auto rotate = [&](const uint4& a, const uint4& b) {
+    uint4 out;
+    uint32_t* w = reinterpret_cast<uint32_t*>(&out);
+    float f[8], o[8];
+    unpack8<kBF>(a, f);
+    if constexpr (kInterleaved) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[j] = pack2<kBF>(__fsub_rn(__fmul_rn(f[2 * j], cs[j]), __fmul_rn(f[2 * j + 1], sn[j])),
+                          __fadd_rn(__fmul_rn(f[2 * j + 1], cs[j]), __fmul_rn(f[2 * j], sn[j])));
+    } else {
+      unpack8<kBF>(b, o);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float m = __fmul_rn(f[j], cs[j]), n = __fmul_rn(o[j], sn[j]);
+        f[j] = second ? __fadd_rn(m, n) : __fsub_rn(m, n);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = pack2<kBF>(f[2 * j], f[2 * j + 1]);
+    }
+    return out;
+  };
+
+  if (static_cast<int>(blockIdx.y) < q_parts) {
+    // Query heads, two in flight.  In place, a vector's partner is read by one thread and written by another:
+    // all of a step's reads come before its writes.
+    const int h0 = blockIdx.y * q_per, h1 = min(p.Hq, h0 + q_per);
+    for (int base = h0; base < h1; base += 2 * R) {
+      uint4 a[2], b[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int h = base + u * R + row;
+        if (row >= R || h >= h1) continue;
+        const uint16_t* src = p.q + t * p.q_st + h * p.q_sh;
+        a[u] = own(src);
+        b[u] = other(src);
+      }
+      if (p.q_out == p.q) __syncthreads();
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int h = base + u * R + row;
+        if (row >= R || h >= h1) continue;
+        *(reinterpret_cast<uint4*>(p.q_out + t * p.qo_st + h * p.qo_sh) + x) = turns ? rotate(a[u], b[u]) : a[u];
+      }
+    }
+    return;
+  }
+  const int h0 = (blockIdx.y - q_parts) * kv_per, h1 = min(2 * p.Hkv, h0 + kv_per);  // key heads, then value heads
+  const int per = p.cache.group / 8, G = p.cache.groups(), slot = __ldg(p.slots + t);
+  for (int base = h0; base < h1; base += R) {
+    const int n = base + row;
+    const bool in = row < R && n < h1, value = n >= p.Hkv;
+    const int h = value ? n - p.Hkv : n;
+    uint4 e = make_uint4(0u, 0u, 0u, 0u);
+    if (in) {
+      const uint16_t* src = value ? p.v + t * p.v_st + h * p.v_sh : p.k + t * p.k_st + h * p.k_sh;
+      e = own(src);
+      if (turns && !value) e = rotate(e, other(src));
+    }
+    float f[8];
+    unpack8<kBF>(e, f);
+    float low = f[0], high = f[0];
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      low = fminf(low, f[j]);
+      high = fmaxf(high, f[j]);
+      bad |= !(fabsf(f[j]) <= 3.4028235e38f);
+    }
+    for (int d = 1; d < per; d <<= 1) {
+      low = fminf(low, __shfl_xor_sync(kFull, low, d));
+      high = fmaxf(high, __shfl_xor_sync(kFull, high, d));
+      bad |= __shfl_xor_sync(kFull, bad ? 1 : 0, d) != 0;
+    }
+    int r = 0;
+    uint8_t* tile = in ? tile_of(p.cache, slot, h, &r) : nullptr;
+    if (!tile) continue;
+    const Quantizer<kBF> quantizer(low, high, bad);
+    uint32_t word = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) word |= quantizer.code(f[j]) << (4 * j);
+    if (value) {
+      uint8_t* codes = tile + 8 * p.D;
+      *reinterpret_cast<uint16_t*>(codes + Kv4::value_byte(p.D, r, 4 * x)) = static_cast<uint16_t>(word);
+      *reinterpret_cast<uint16_t*>(codes + Kv4::value_byte(p.D, r, 4 * x + 2)) = static_cast<uint16_t>(word >> 16);
+    } else {
+      *reinterpret_cast<uint32_t*>(tile + Kv4::key_byte(p.D, r, 4 * x)) = word;
+    }
+    if (x % per == 0)
+      *(reinterpret_cast<uint32_t*>(tile + 16 * p.D + (value ? 64 * G : 0)) + r * G + x / per) = quantizer.params();
+  }
+}
+
+bool vectors_fit(const AppendKv4Problem& p) {
+  return (p.q_st | p.q_sh | p.k_st | p.k_sh | p.v_st | p.v_sh | p.qo_st | p.qo_sh) % 8 == 0 && p.rot % 16 == 0 && aligned(p.q, 16) &&
+         aligned(p.k, 16) && aligned(p.v, 16) && aligned(p.q_out, 16) && aligned(p.table, 16);
+}
+
+template <bool kBF, bool kInterleaved>
+cudaError_t launch_vec(const AppendKv4Problem& p) {
+  const int R = kThreads / (p.D / 8);
+  // few tokens: as many blocks as give a thread one or two heads; many: a token's query heads, its others
+  const bool few = p.T * ((p.Hq + 2 * R - 1) / (2 * R) + (2 * p.Hkv + R - 1) / R) < 1216;
+  const int q_per = few ? 2 * R : p.Hq, kv_per = few ? R : 2 * p.Hkv;
+  const int q_parts = p.Hq ? (p.Hq + q_per - 1) / q_per : 0, kv_parts = (2 * p.Hkv + kv_per - 1) / kv_per;
+  append_vec_kernel<kBF, kInterleaved>
+      <<<dim3(static_cast<unsigned>(p.T), static_cast<unsigned>(q_parts + kv_parts)), kThreads, 0, p.stream>>>(p, q_parts, q_per, kv_per);
+  return cudaGetLastError();
+}
+
+// Aligned outputs: a thread has a vector of a key head and the same of the value head.
+template <bool kBF>
+__global__ void __launch_bounds__(kThreads) read_vec_kernel(const ReadKv4Problem p) {
+  const Kv4Cache& c = p.cache;
+  const int L = c.head_dim / 8, D = c.head_dim, G = c.groups();
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x, item = i / L;
+  if (item >= p.T * c.heads) return;
+  const int x = static_cast<int>(i - item * L);
+  const int64_t t = item / c.heads;
+  const int h = static_cast<int>(item - t * c.heads);
+  int r = 0;
+  const uint8_t* tile = tile_of(c, __ldg(p.slots + t), h, &r);
+  uint32_t word[2] = {0u, 0u}, params[2] = {0u, 0u};
+  if (tile) {
+    word[0] = *reinterpret_cast<const uint32_t*>(tile + Kv4::key_byte(D, r, 4 * x));
+    word[1] = *reinterpret_cast<const uint16_t*>(tile + 8 * D + Kv4::value_byte(D, r, 4 * x)) |
+              (static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(tile + 8 * D + Kv4::value_byte(D, r, 4 * x + 2))) << 16);
+    const uint32_t* at = reinterpret_cast<const uint32_t*>(tile + 16 * D) + r * G + 8 * x / c.group;
+    params[0] = at[0];
+    params[1] = at[16 * G];
+  }
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
+    const float2 sm = ptx::pair_to_float2<kBF>(params[v]);
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {  // the products are exact
+      const float a = static_cast<float>((word[v] >> (8 * j)) & 15u) * sm.x, b = static_cast<float>((word[v] >> (8 * j + 4)) & 15u) * sm.x;
+      w[j] = pack2<kBF>(__fadd_rn(a, sm.y), __fadd_rn(b, sm.y));
+    }
+    *(reinterpret_cast<uint4*>((v ? p.v : p.k) + item * D) + x) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
 }  // namespace
 
 bool kv4_shape_supported(int64_t D, int64_t group) {
@@ -170,17 +377,27 @@ bool kv4_shape_supported(int64_t D, int64_t group) {
 }
 
 cudaError_t launch_append_kv4(const AppendKv4Problem& p) {
+  if (vectors_fit(p)) {
+    if (p.bf16) return p.interleaved ? launch_vec<true, true>(p) : launch_vec<true, false>(p);
+    return p.interleaved ? launch_vec<false, true>(p) : launch_vec<false, false>(p);
+  }
   const int64_t items = p.T * (p.Hq + 2 * p.Hkv);
   const unsigned blocks = static_cast<unsigned>((items + 7) / 8);
-  if (p.bf16) append_kernel<true><<<blocks, 256, 0, p.stream>>>(p);
-  else append_kernel<false><<<blocks, 256, 0, p.stream>>>(p);
+  if (p.bf16) append_any_kernel<true><<<blocks, 256, 0, p.stream>>>(p);
+  else append_any_kernel<false><<<blocks, 256, 0, p.stream>>>(p);
   return cudaGetLastError();
 }
 
 cudaError_t launch_read_kv4(const ReadKv4Problem& p) {
+  if (aligned(p.k, 16) && aligned(p.v, 16)) {
+    const unsigned blocks = static_cast<unsigned>((p.T * p.cache.heads * (p.cache.head_dim / 8) + kThreads - 1) / kThreads);
+    if (p.bf16) read_vec_kernel<true><<<blocks, kThreads, 0, p.stream>>>(p);
+    else read_vec_kernel<false><<<blocks, kThreads, 0, p.stream>>>(p);
+    return cudaGetLastError();
+  }
   const unsigned blocks = static_cast<unsigned>((p.T * p.cache.heads + 7) / 8);
-  if (p.bf16) read_kernel<true><<<blocks, 256, 0, p.stream>>>(p);
-  else read_kernel<false><<<blocks, 256, 0, p.stream>>>(p);
+  if (p.bf16) read_any_kernel<true><<<blocks, 256, 0, p.stream>>>(p);
+  else read_any_kernel<false><<<blocks, 256, 0, p.stream>>>(p);
   return cudaGetLastError();
 }
 

@@ -6,22 +6,23 @@
 //
 // in fp32, each output rounded once; y is formed from the unrounded h.
 #include "awq_step.cuh"
+#include "awq_ptx.cuh"
 
 namespace awq {
 namespace {
 
-template <int kThreads>
+// Sum over the block; `shared` has room for 32 numbers and is free again at the next call's first barrier.
 __device__ __forceinline__ float block_sum(float v, float* shared) {
 #pragma unroll
   for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  if constexpr (kThreads > 32) {
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = (threadIdx.x & 31) < kThreads / 32 ? shared[threadIdx.x & 31] : 0.f;
+  const int warps = blockDim.x >> 5;
+  if (warps == 1) return v;
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = (threadIdx.x & 31) < warps ? shared[threadIdx.x & 31] : 0.f;
 #pragma unroll
-    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  }
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
   return v;
 }
 
@@ -39,14 +40,14 @@ __global__ void __launch_bounds__(256) norm_any_kernel(const ResidualNormProblem
       *mean = 0.f;
       if (p.layer) {
         for (int i = threadIdx.x; i < p.W; i += 256) s += at(i);
-        *mean = block_sum<256>(s, shared) * inv;
+        *mean = block_sum(s, shared) * inv;
       }
       s = 0.f;
       for (int i = threadIdx.x; i < p.W; i += 256) {
         const float d = at(i) - *mean;
         s += d * d;
       }
-      *rstd = rsqrtf(block_sum<256>(s, shared) * inv + p.eps);
+      *rstd = rsqrtf(block_sum(s, shared) * inv + p.eps);
     };
     float pm = 0.f, pr = 1.f, m, rs;
     if (p.post_weight) stats([&](int i) { return elem_to_float<kBF>(x[i]); }, &pm, &pr);
@@ -73,13 +74,152 @@ __global__ void __launch_bounds__(256) norm_any_kernel(const ResidualNormProblem
   }
 }
 
-}  // namespace
+// Rows of whole aligned 16-byte vectors: one block per row, the row in registers (V vectors a thread), read
+// and written once.
+template <bool kBF, int V>
+__global__ void __launch_bounds__(1024) norm_vec_kernel(const ResidualNormProblem p) {
+  __shared__ float shared[32];
+  const int vectors = p.W / 8;
+  const float inv = 1.f / p.W;
+  const int64_t t = blockIdx.x;
+  const auto at = [&](int v) { return static_cast<int>(threadIdx.x + v * blockDim.x); };
+  const auto load = [](const uint16_t* row, int i) { return *(reinterpret_cast<const uint4*>(row) + i); };
+  const auto weights = [](const uint16_t* row, int i) { return __ldg(reinterpret_cast<const uint4*>(row) + i); };
+  const auto unpack = [](const uint4& u, float (&f)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 e = ptx::pair_to_float2<kBF>(w[j]);
+      f[2 * j] = e.x;
+      f[2 * j + 1] = e.y;
+    }
+  };
+  const auto pack = [](const float (&f)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w[j] = static_cast<uint32_t>(float_to_elem<kBF>(f[2 * j])) | (static_cast<uint32_t>(float_to_elem<kBF>(f[2 * j + 1])) << 16);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  };
+  uint4 raw[V], res[V], gate[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int i = at(v);
+    if (i >= vectors) continue;
+    raw[v] = load(p.x + t * p.x_st, i);
+    if (p.residual) res[v] = load(p.residual + t * p.r_st, i);
+    if (p.gate) gate[v] = load(p.gate + t * p.g_st, i);
+  }
+  float h[V][8];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    if (at(v) < vectors) {
+      unpack(raw[v], h[v]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[v][j] = 0.f;
+    }
+  }
+  const auto stats = [&](float* mean, float* rstd) {
+    float s = 0.f;
+    *mean = 0.f;
+    if (p.layer) {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s += h[v][j];
+      *mean = block_sum(s, shared) * inv;
+      s = 0.f;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (at(v) >= vectors) continue;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float d = h[v][j] - *mean;
+        s += d * d;
+      }
+    }
+    *rstd = rsqrtf(block_sum(s, shared) * inv + p.eps);
+  };
+  const auto normalize = [&](int v, const uint16_t* weight, const uint16_t* bias, float mean, float rstd, float (&to)[8]) {
+    float w[8];
+    unpack(weights(weight, at(v)), w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) to[j] = (h[v][j] - mean) * rstd * w[j];
+    if (bias) {
+      unpack(weights(bias, at(v)), w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) to[j] += w[j];
+    }
+  };
+  float mean, rstd;
+  if (p.post_weight) {
+    stats(&mean, &rstd);
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (at(v) < vectors) normalize(v, p.post_weight, p.post_bias, mean, rstd, h[v]);
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    if (at(v) >= vectors) continue;
+    float f[8];
+    if (p.gate) {
+      unpack(gate[v], f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[v][j] *= f[j];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[v][j] *= p.scale;
+    if (p.residual) {
+      unpack(res[v], f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[v][j] += f[j];
+    }
+    *(reinterpret_cast<uint4*>(p.h + t * p.W) + at(v)) = pack(h[v]);
+  }
+  if (!p.weight) return;
+  stats(&mean, &rstd);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    if (at(v) >= vectors) continue;
+    float f[8];
+    normalize(v, p.weight, p.bias, mean, rstd, f);
+    *(reinterpret_cast<uint4*>(p.y + t * p.W) + at(v)) = pack(f);
+  }
+}
 
-cudaError_t launch_residual_norm(const ResidualNormProblem& p) {
-  const unsigned blocks = static_cast<unsigned>(p.T < (1 << 20) ? p.T : (1 << 20));
-  if (p.bf16) norm_any_kernel<true><<<blocks, 256, 0, p.stream>>>(p);
-  else norm_any_kernel<false><<<blocks, 256, 0, p.stream>>>(p);
+bool vectors_fit(const ResidualNormProblem& p) {
+  return p.W % 8 == 0 && p.W <= 32768 && (p.x_st | p.r_st | p.g_st) % 8 == 0 && aligned(p.x, 16) && aligned(p.residual, 16) &&
+         aligned(p.gate, 16) && aligned(p.post_weight, 16) && aligned(p.post_bias, 16) && aligned(p.weight, 16) &&
+         aligned(p.bias, 16) && aligned(p.h, 16) && aligned(p.y, 16);
+}
+
+template <bool kBF, int V>
+cudaError_t launch_vec(const ResidualNormProblem& p) {
+  const int threads = ((p.W / 8 + V - 1) / V + 31) / 32 * 32;
+  norm_vec_kernel<kBF, V><<<static_cast<unsigned>(p.T), threads, 0, p.stream>>>(p);
   return cudaGetLastError();
 }
+
+template <bool kBF>
+cudaError_t launch(const ResidualNormProblem& p) {
+  if (vectors_fit(p)) {
+    // one vector a thread where there are few rows, two where there are many
+    const int vectors = p.W / 8, v = vectors <= 1024 && p.T <= 304 ? 1 : vectors <= 2048 ? 2 : 4;
+    switch (v) {
+      case 1: return launch_vec<kBF, 1>(p);
+      case 2: return launch_vec<kBF, 2>(p);
+      default: return launch_vec<kBF, 4>(p);
+    }
+  }
+  const unsigned blocks = static_cast<unsigned>(p.T < (1 << 20) ? p.T : (1 << 20));
+  norm_any_kernel<kBF><<<blocks, 256, 0, p.stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_residual_norm(const ResidualNormProblem& p) { return p.bf16 ? launch<true>(p) : launch<false>(p); }
 
 }  // namespace awq
