@@ -181,6 +181,7 @@ __global__ void __launch_bounds__(256) read_any_kernel(const ReadKv4Problem p) {
 // query heads (rotated and written), then keys and values, whose groups are 4, 8 or 16 neighbouring lanes.  A
 // vector's codes are one word of the keys, half a word each of two of the values.
 constexpr int kThreads = 128;
+constexpr int kFlight = 4;
 
 template <bool kBF>
 __device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
@@ -207,8 +208,8 @@ __global__ void __launch_bounds__(kThreads) append_vec_kernel(const AppendKv4Pro
   const int half = p.rot / 16;  // vectors of half the rotated part
   const bool second = !kInterleaved && x >= half;
   float cs[8], sn[8];  // interleaved: four of each
-  if (turns) {
-    const int pos = __ldg(p.positions + t);
+  const auto load_line = [&](int pos) {
+    if (!turns) return;
     if (pos >= 0 && pos < p.max_position) {
       const float* line = p.table + static_cast<int64_t>(pos) * p.rot + (kInterleaved ? 4 * x : 8 * (second ? x - half : x));
       *reinterpret_cast<float4*>(cs) = __ldg(reinterpret_cast<const float4*>(line));
@@ -221,7 +222,8 @@ __global__ void __launch_bounds__(kThreads) append_vec_kernel(const AppendKv4Pro
 #pragma unroll
       for (int j = 0; j < 8; ++j) cs[j] = sn[j] = quiet_nan();
     }
-  }
+  };
+  const int pos = turns ? __ldg(p.positions + t) : 0;
   const auto own = [&](const uint16_t* src) { return *(reinterpret_cast<const uint4*>(src) + x); };
   const auto other = [&](const uint16_t* src) {  // the vector of the pairs' other elements
     return !kInterleaved && turns ? *(reinterpret_cast<const uint4*>(src) + (second ? x - half : x + half)) : make_uint4(0u, 0u, 0u, 0u);
@@ -250,22 +252,23 @@ __global__ void __launch_bounds__(kThreads) append_vec_kernel(const AppendKv4Pro
   };
 
   if (static_cast<int>(blockIdx.y) < q_parts) {
-    // Query heads, two in flight.  In place, a vector's partner is read by one thread and written by another:
+    // Query heads, kFlight of them in flight, the first ones before the position's line.  In place, a vector's partner is read by one thread and written by another:
     // all of a step's reads come before its writes.
     const int h0 = blockIdx.y * q_per, h1 = min(p.Hq, h0 + q_per);
-    for (int base = h0; base < h1; base += 2 * R) {
-      uint4 a[2], b[2];
+    for (int base = h0; base < h1; base += kFlight * R) {
+      uint4 a[kFlight], b[kFlight];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < kFlight; ++u) {
         const int h = base + u * R + row;
         if (row >= R || h >= h1) continue;
         const uint16_t* src = p.q + t * p.q_st + h * p.q_sh;
         a[u] = own(src);
         b[u] = other(src);
       }
+      if (base == h0) load_line(pos);
       if (p.q_out == p.q) __syncthreads();
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < kFlight; ++u) {
         const int h = base + u * R + row;
         if (row >= R || h >= h1) continue;
         *(reinterpret_cast<uint4*>(p.q_out + t * p.qo_st + h * p.qo_sh) + x) = turns ? rotate(a[u], b[u]) : a[u];
@@ -275,16 +278,24 @@ __global__ void __launch_bounds__(kThreads) append_vec_kernel(const AppendKv4Pro
   }
   const int h0 = (blockIdx.y - q_parts) * kv_per, h1 = min(2 * p.Hkv, h0 + kv_per);  // key heads, then value heads
   const int per = p.cache.group / 8, G = p.cache.groups(), slot = __ldg(p.slots + t);
+  uint4 next[2];  // the next head's vector, and its pairs' others
+  const auto load = [&](int base) {
+    const int n = base + row;
+    next[0] = next[1] = make_uint4(0u, 0u, 0u, 0u);
+    if (row >= R || n >= h1) return;
+    const uint16_t* src = n >= p.Hkv ? p.v + t * p.v_st + (n - p.Hkv) * p.v_sh : p.k + t * p.k_st + n * p.k_sh;
+    next[0] = own(src);
+    if (n < p.Hkv) next[1] = other(src);
+  };
+  load(h0);
+  load_line(pos);
   for (int base = h0; base < h1; base += R) {
     const int n = base + row;
     const bool in = row < R && n < h1, value = n >= p.Hkv;
     const int h = value ? n - p.Hkv : n;
-    uint4 e = make_uint4(0u, 0u, 0u, 0u);
-    if (in) {
-      const uint16_t* src = value ? p.v + t * p.v_st + h * p.v_sh : p.k + t * p.k_st + h * p.k_sh;
-      e = own(src);
-      if (turns && !value) e = rotate(e, other(src));
-    }
+    const uint4 mine[2] = {next[0], next[1]};
+    load(base + R);
+    const uint4 e = turns && !value ? rotate(mine[0], mine[1]) : mine[0];
     float f[8];
     unpack8<kBF>(e, f);
     float low = f[0], high = f[0];
@@ -327,9 +338,9 @@ bool vectors_fit(const AppendKv4Problem& p) {
 template <bool kBF, bool kInterleaved>
 cudaError_t launch_vec(const AppendKv4Problem& p) {
   const int R = kThreads / (p.D / 8);
-  // few tokens: as many blocks as give a thread one or two heads; many: a token's query heads, its others
-  const bool few = p.T * ((p.Hq + 2 * R - 1) / (2 * R) + (2 * p.Hkv + R - 1) / R) < 1216;
-  const int q_per = few ? 2 * R : p.Hq, kv_per = few ? R : 2 * p.Hkv;
+  // few tokens: as many blocks as give a thread one head; many: a token's query heads, its others
+  const bool few = p.T * ((p.Hq + R - 1) / R + (2 * p.Hkv + R - 1) / R) < 1216;
+  const int q_per = few ? R : p.Hq, kv_per = few ? R : 2 * p.Hkv;
   const int q_parts = p.Hq ? (p.Hq + q_per - 1) / q_per : 0, kv_parts = (2 * p.Hkv + kv_per - 1) / kv_per;
   append_vec_kernel<kBF, kInterleaved>
       <<<dim3(static_cast<unsigned>(p.T), static_cast<unsigned>(q_parts + kv_parts)), kThreads, 0, p.stream>>>(p, q_parts, q_per, kv_per);

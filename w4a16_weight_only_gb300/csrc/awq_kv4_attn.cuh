@@ -14,6 +14,8 @@
 // to fp16 with s relative to the largest scale so far (a power of two, raised like the maximum).
 #pragma once
 
+#include <type_traits>
+
 #include "awq_step.cuh"
 #include "awq_attn.cuh"
 
@@ -281,16 +283,15 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
     };
     look_up();
     take_over();
-    int64_t loaded = min(static_cast<int64_t>(STAGES), tiles);
-    if (lane < loaded) issue(lane);
+    const int first_tiles = static_cast<int>(min(static_cast<int64_t>(STAGES), tiles));
+    if (lane < first_tiles) issue(lane);
     __syncwarp();
 
-    // Tile `used` has arrived.  A bounded wait; the clock is read before the test that decides, so that a
-    // pause between the two gives nothing up.
-    const auto arrived = [&](int64_t used) -> bool {
-      const uint32_t parity = static_cast<uint32_t>(used / STAGES) & 1u;
-      uint64_t* bar = &full[used % STAGES];
-      const auto there = [&] { return __all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity)) != 0; };
+    // The tile in a stage has arrived.  A bounded wait; the clock is read before the test that decides, so
+    // that a pause between the two gives nothing up.
+    const auto arrived = [&](int stage, uint32_t phase) -> bool {
+      uint64_t* bar = &full[stage];
+      const auto there = [&] { return __all_sync(0xffffffffu, ptx::mbar_try_wait(bar, phase)) != 0; };
       if (there()) return true;
       const uint64_t t0 = ptx::globaltimer_ns();
       while (true) {
@@ -301,16 +302,20 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
     };
 
     bool gave_up = false;
-    int64_t used = 0;
+    int64_t to_load = tiles - first_tiles;
+    int in_flight = first_tiles;
+    uint32_t next_load = first_tiles;  // its place in a batch: the low five bits
     int stage = 0;
+    uint32_t phase = 0;
     for (int64_t x = x0; x < x1;) {
       // ---- one run ----
       const int hk = cur.ln / a.row_tiles, row0 = (cur.ln - hk * a.row_tiles) * ROWS, rows = p.n * a.group;
       const int len = cur.r.len, begin = cur.at;
       const int end = begin + static_cast<int>(min(static_cast<int64_t>(cur.r.count - begin), x1 - x));
       const int pos0 = len - p.n + row0 / a.group, pos1 = len - p.n + min(p.n - 1, (row0 + ROWS - 1) / a.group);
-      const int64_t low0 = p.window > 0 ? static_cast<int64_t>(pos0) - p.window : -1;  // keys up to here are out of the window
-      const int64_t low1 = p.window > 0 ? static_cast<int64_t>(pos1) - p.window : -1;
+      // keys up to here are out of the window
+      const int low0 = p.window > 0 ? static_cast<int>(max(static_cast<int64_t>(pos0) - p.window, int64_t{-1})) : -1;
+      const int low1 = p.window > 0 ? static_cast<int>(max(static_cast<int64_t>(pos1) - p.window, int64_t{-1})) : -1;
       uint32_t qf[NT][U][2][2];  // word, kind, half of the contraction
       float qsum[NT][G][2];      // sums of the lane's two columns' queries over a group
       float zscale[NT][2];       // what takes a column's product to a base-2 logit
@@ -384,7 +389,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
       float unit = __uint_as_float(0x00800000u), per_unit = __uint_as_float(253u << 23);  // 2^-126, 2^126
 
       for (int i = begin; i < end; ++i) {
-        if (p.give_up || !arrived(used)) {
+        if (p.give_up || !arrived(stage, phase)) {
           gave_up = true;
           break;
         }
@@ -393,7 +398,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
         // whether some row sees a key here, and whether all see all
         const bool any = k0 <= pos1 && (k0 + kTileKeys - 1 > low0 || k0 < p.sinks);
         const bool all = k0 + kTileKeys - 1 <= pos0 && (k0 > low1 || k0 + kTileKeys <= p.sinks);
-        if (any) {
+        const auto body = [&](auto masked) {
+          constexpr bool kMasked = decltype(masked)::value;
           uint32_t kw[2][U];  // keys g and g + 8
 #pragma unroll
           for (int half = 0; half < 2; ++half)
@@ -442,7 +448,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
               }
           }
           uint32_t seen = 0xffffffffu;  // bit 4 m + 2 half + h
-          if (!all) {
+          if constexpr (kMasked) {
             seen = 0;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -464,7 +470,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
               v[half][q] = ptx::pair_to_float2<kBF>(params[16 * G + 8 * half * G + q]);
               // a key that no row sees may hold anything
               const int key = k0 + g + 8 * half;
-              if (!all && !(key <= pos1 && (key > low0 || key < p.sinks))) v[half][q] = make_float2(0.f, 0.f);
+              if (kMasked && !(key <= pos1 && (key > low0 || key < p.sinks))) v[half][q] = make_float2(0.f, 0.f);
               widest = fmaxf(widest, v[half][q].x);
             }
           bool raise = widest > unit;
@@ -475,7 +481,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
 #pragma unroll
               for (int half = 0; half < 2; ++half) {
                 z[m][half][h] *= zscale[m][h];
-                if (!all && !((seen >> (4 * m + 2 * half + h)) & 1u)) z[m][half][h] = -INFINITY;
+                if (kMasked && !((seen >> (4 * m + 2 * half + h)) & 1u)) z[m][half][h] = -INFINITY;
               }
               raise |= fmaxf(z[m][0][h], z[m][1][h]) > top[m][h] + kRaise;
             }
@@ -546,7 +552,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
               for (int half = 0; half < 2; ++half) {
                 const float s = v[half][q].x * per_unit, mn = v[half][q].y;
                 float ps[2] = {z[m][half][0] * s, z[m][half][1] * s}, pm[2] = {z[m][half][0] * mn, z[m][half][1] * mn};
-                if (!all) {  // zero times a value that is not finite
+                if constexpr (kMasked) {  // zero times a value that is not finite
 #pragma unroll
                   for (int h = 0; h < 2; ++h)
                     if (!((seen >> (4 * m + 2 * half + h)) & 1u)) ps[h] = pm[h] = 0.f;
@@ -568,18 +574,25 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
               }
             }
           }
-        }
+        };
+        if (all) body(std::false_type{});
+        else if (any) body(std::true_type{});
         __syncwarp();  // the stage has been read
-        ++used;
-        if (loaded < tiles) {
-          const int owner = static_cast<int>(loaded & 31);
+        if (to_load > 0) {
+          const uint32_t owner = next_load & 31u;
           if (owner == 16) look_up();
           if (owner == 0) take_over();
-          if (lane == owner) issue(stage);
-          ++loaded;
+          if (lane == static_cast<int>(owner)) issue(stage);
+          --to_load;
+          ++next_load;
+        } else {
+          --in_flight;
         }
         __syncwarp();
-        if (++stage == STAGES) stage = 0;
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
       if (gave_up) break;
 
@@ -643,7 +656,13 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
     }
     if (gave_up) {
       if (lane == 0) atomicOr(a.status, kStatusKv4Timeout);
-      for (; used < loaded; ++used) arrived(used);
+      for (; in_flight > 0; --in_flight) {
+        arrived(stage, phase);
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
     }
   }
 
