@@ -233,6 +233,9 @@ CASES = [
     (1, 1, 2, 1, 128, 128, [6000], 16, 0, 0),               # cut along the keys, few heads
     (33, 1, 8, 2, 128, 128, [(37 * i) % 241 for i in range(33)], 16, 0, 0),
     (9, 1, 4, 4, 64, 64, [700 + 31 * i for i in range(9)], 64, 0, 0),
+    (40, 1, 16, 8, 64, 32, [(53 * i) % 300 for i in range(40)], 16, 0, 0),   # more units than blocks at a time
+    (3, 1, 8, 2, 128, 64, [2500, 40, 3000], 16, 0, 0),      # tables too long for a unit per block
+    (2, 5, 8, 2, 96, 32, [3000, 2200], 16, 0, 0),
     (2, 1, 8, 2, 128, 128, [300, 77], 16, 64, 0),           # windows
     (2, 1, 8, 2, 128, 64, [300, 77], 16, 50, 4),
     (3, 1, 8, 8, 64, 32, [1000, 5, 130], 32, 100, 20),      # first tokens beyond a tile
@@ -242,6 +245,7 @@ CASES = [
     (2, 2, 4, 1, 256, 64, [200, 100], 16, 1000, 2000),      # both longer than the sequence
     (1, 70, 4, 2, 128, 128, [70], 16, 0, 0),                # a prompt
     (1, 130, 2, 1, 64, 64, [200], 16, 24, 2),               # a prompt under a window
+    (2, 3, 8, 2, 128, 128, [5000, 2100], 16, 2300, 70),     # a long window, cut along the keys
 ]
 
 

@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(256) read_any_kernel(const ReadKv4Problem p) {
 // query heads (rotated and written), then keys and values, whose groups are 4, 8 or 16 neighbouring lanes.  A
 // vector's codes are one word of the keys, half a word each of two of the values.
 constexpr int kThreads = 128;
-constexpr int kFlight = 4;
+constexpr int kFlight = 2;
 
 template <bool kBF>
 __device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
@@ -200,7 +200,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 
 template <bool kBF, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) append_vec_kernel(const AppendKv4Problem p, int q_parts, int q_per, int kv_per) {
+__global__ void __launch_bounds__(kThreads, 12) append_vec_kernel(const AppendKv4Problem p, int q_parts, int q_per, int kv_per) {
   const int L = p.D / 8, R = kThreads / L;  // threads of a row, rows of the block
   const int x = threadIdx.x % L, row = threadIdx.x / L;
   const int64_t t = blockIdx.x;

@@ -16,6 +16,9 @@ size_t part_bytes(const AttentionKv4Problem& p, int nt) { return static_cast<siz
 
 int most_blocks(const AttentionKv4Problem& p, int nt, int sms) { return sms * blocks_per_sm(p.cache.head_dim, nt); }
 
+// A unit per block up to this many tiles (eight warps, 16 tiles each), where all units run at once.
+constexpr int kAlignedTiles = 128;
+
 struct Layout {
   size_t firsts, line, bytes;  // parts first
 };
@@ -48,11 +51,17 @@ cudaError_t launch_attention_kv4(const AttentionKv4Problem& p, int sms) {
   a.parts = reinterpret_cast<float*>(ws);
   a.firsts = reinterpret_cast<float*>(ws + l.firsts);
   a.line = reinterpret_cast<int64_t*>(ws + l.line);
-  // no more blocks than the tiles that the page tables can hold give work
-  const int64_t tiles = static_cast<int64_t>(p.W) * a.tiles_per_page;                   // of a sequence, below 2^27
-  const int64_t units = static_cast<int64_t>(p.B) * p.cache.heads * a.row_tiles;        // below 2^32: B n Hq < 2^31
-  const int64_t need = units * tiles / (kWarps * a.per_min) + 1;
-  const int grid = static_cast<int>(need < most_blocks(p, nt, sms) ? need : most_blocks(p, nt, sms));
+  // tiles of a sequence that its table and window allow, below 2^27, and units, below 2^32 (B n Hq < 2^31)
+  int64_t tiles = static_cast<int64_t>(p.W) * a.tiles_per_page;
+  if (p.window > 0) {
+    const int64_t seen = (static_cast<int64_t>(p.window) + p.n + p.sinks) / kTileKeys + 3;
+    if (seen < tiles) tiles = seen;
+  }
+  const int64_t units = static_cast<int64_t>(p.B) * p.cache.heads * a.row_tiles;
+  const int most = most_blocks(p, nt, sms);
+  a.aligned = tiles <= kAlignedTiles && units <= most;
+  const int64_t need = a.aligned ? units : units * tiles / (kWarps * a.per_min) + 1;
+  const int grid = static_cast<int>(need < most ? need : most);
   switch (p.cache.head_dim) {
     case 64: return run_64(a, nt, grid);
     case 96: return run_96(a, nt, grid);

@@ -59,13 +59,15 @@ struct Shape {
 // where the lengths are.  A run is what a warp has of a unit.  A run that is a whole unit is written out at
 // once; the others are joined, those of a block in the block, and a unit of several blocks by the join
 // kernel: a block's part of a unit that goes on behind the block is at part 2 block + 1, of one that ends
-// in it at 2 block.
+// in it at 2 block.  Where the sequences' tables or windows are short and there are few units, a block takes
+// one unit, and there is neither line nor join.
 struct Args {
   AttentionKv4Problem p;
   int group;      // query heads per key/value head
   int row_tiles;  // of a sequence and key/value head
   int tiles_per_page;
   int per_min;
+  bool aligned;   // a unit per block instead: no line, nothing to join between blocks
   float* parts;   // [2 blocks] of PART bytes
   float* firsts;  // [blocks][warps] of PART bytes: a warp's first run, where others follow
   int64_t* line;  // per, then the sequences' first tiles (within a lane) and their number, [B + 1]
@@ -138,9 +140,17 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
   const Kv4Cache& cache = p.cache;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 
-  // coarse[i]: tiles (of one lane) of the sequences before i * gran
   const int gran = (p.B + kCoarse - 2) / (kCoarse - 1);
-  {
+  int64_t T = 0, total, per, X0;
+  if (lane < 2) entries[warp][lane].valid = 0;
+  if (lane == 2) several[warp] = false;
+  if (a.aligned) {
+    total = range_of(p, static_cast<int>(blockIdx.x % p.B)).count;
+    per = max(int64_t{1}, (total + kWarps - 1) / kWarps);
+    X0 = 0;
+    __syncthreads();
+  } else {
+    // coarse[i]: tiles (of one lane) of the sequences before i * gran
     const int64_t b0 = static_cast<int64_t>(threadIdx.x) * gran, b1 = min(b0 + gran, static_cast<int64_t>(p.B));
     int64_t sum = 0;
     for (int64_t b = b0; b < b1; ++b) sum += range_of(p, static_cast<int>(b)).count;
@@ -151,8 +161,6 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
       if (lane >= d) before += o;
     }
     if (lane == 31) of_warp[warp] = before;
-    if (lane < 2) entries[warp][lane].valid = 0;
-    if (lane == 2) several[warp] = false;
     __syncthreads();
     before -= sum;
     for (int w = 0; w < warp; ++w) before += of_warp[w];
@@ -165,12 +173,13 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
       if (threadIdx.x == kCoarse - 1) a.line[1 + p.B] = before;  // it has no sequences: (kCoarse - 1) gran >= B
     }
     __syncthreads();
+    T = coarse[kCoarse - 1];
+    total = T * (static_cast<int64_t>(cache.heads) * a.row_tiles);
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps;
+    per = max(static_cast<int64_t>(a.per_min), (total + warps - 1) / warps);
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.line[0] = per;
+    X0 = static_cast<int64_t>(blockIdx.x) * kWarps * per;
   }
-  const int64_t T = coarse[kCoarse - 1];
-  const int64_t total = T * (static_cast<int64_t>(cache.heads) * a.row_tiles);
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps;
-  const int64_t per = max(static_cast<int64_t>(a.per_min), (total + warps - 1) / warps);
-  if (blockIdx.x == 0 && threadIdx.x == 0) a.line[0] = per;
   ptx::launch_dependents();
 
   // sequences without keys: zeros
@@ -181,7 +190,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
     for (int64_t i = threadIdx.x; i < n; i += kWarps * 32) dst[i] = make_uint4(0u, 0u, 0u, 0u);
   }
 
-  const int64_t X0 = static_cast<int64_t>(blockIdx.x) * kWarps * per, X1 = min(total, X0 + kWarps * per);
+  const int64_t X1 = min(total, X0 + kWarps * per);
   if (X0 >= total) return;
   const int64_t x0 = min(total, X0 + warp * per), x1 = min(total, x0 + per);
 
@@ -202,7 +211,12 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
       Range r;
     };
     Cursor cur;
-    {  // the first tile's unit
+    if (a.aligned) {
+      cur.ln = static_cast<int>(blockIdx.x / p.B);
+      cur.b = static_cast<int>(blockIdx.x - cur.ln * p.B);
+      cur.at = static_cast<int>(x0);
+      cur.r = range_of(p, cur.b);
+    } else {  // the first tile's unit
       cur.ln = static_cast<int>(x0 / T);
       const int64_t rem = x0 - cur.ln * T;
       int lo = 0, hi = kCoarse - 1;  // coarse[lo] <= rem < coarse[hi]
@@ -761,7 +775,7 @@ cudaError_t run(const Args& a, int grid) {
   kernel<<<grid, kWarps * 32, smem, a.p.stream>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  if (grid == 1) return cudaSuccess;  // nothing to join
+  if (grid == 1 || a.aligned) return cudaSuccess;  // nothing to join
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
