@@ -534,13 +534,14 @@ cudaError_t launch(const MoeLayerProblem& p, int sms) {
     down.y = up.y;
     down.counters = up.counters;
     down.status = up.status;
-    const auto grid = [&](int64_t tiles) {
-      const int64_t units = tiles * p.T * p.k, most = 2 * static_cast<int64_t>(sms);
-      return static_cast<int>(units < most ? units : most);
-    };
-    e = launch_product<kBF, true, 8>(up, grid(p.I / 64));
+    // Few units: a block of sixteen warps for each, so that a warp has half as many rows to wait for.  Many:
+    // two blocks of eight per SM, one computing while the other adds its warps up.
+    const int64_t places = static_cast<int64_t>(p.T) * p.k, up_units = p.I / 64 * places, down_units = (p.H + 127) / 128 * places;
+    const auto grid = [&](int64_t units) { return static_cast<int>(units < 2 * sms ? units : 2 * sms); };
+    e = up_units <= sms ? launch_product<kBF, true, 16>(up, grid(up_units)) : launch_product<kBF, true, 8>(up, grid(up_units));
     if (e != cudaSuccess) return e;
-    return launch_product<kBF, false, 8>(down, grid((p.H + 127) / 128));
+    return down_units <= sms ? launch_product<kBF, false, 16>(down, grid(down_units))
+                             : launch_product<kBF, false, 8>(down, grid(down_units));
   }
   float* act = reinterpret_cast<float*>(ws);
   if (p.k > 0 && p.I > 0) {
