@@ -522,26 +522,28 @@ cudaError_t launch(const MoeLayerProblem& p, int sms) {
   const Layout l = layout(p.T, p.k, p.H, p.I);
   uint8_t* ws = static_cast<uint8_t*>(p.workspace);
   Args up{}, down{};
-  if (tensor_cores_fit(p) && make_map(&up.map, p.up, p.E, p.H, 2 * p.I) && make_map(&down.map, p.down, p.E, p.I, p.H)) {
+  if (tensor_cores_fit(p)) {
+    // First of all: it makes the device's context this host thread's, without which no tensor map is made.
+    cudaError_t e = status_word_ptr(&up.status);
+    if (e != cudaSuccess) return e;
+    if (!make_map(&up.map, p.up, p.E, p.H, 2 * p.I) || !make_map(&down.map, p.down, p.E, p.I, p.H)) return cudaErrorInvalidValue;
     up.p = p;
     up.act = reinterpret_cast<uint16_t*>(ws);
     up.y = reinterpret_cast<float*>(ws + l.y);
     up.counters = reinterpret_cast<int*>(ws + l.counters);
-    cudaError_t e = status_word_ptr(&up.status);
-    if (e != cudaSuccess) return e;
     down.p = p;
     down.act = up.act;
     down.y = up.y;
     down.counters = up.counters;
     down.status = up.status;
-    // Few units: a block of sixteen warps for each, so that a warp has half as many rows to wait for.  Many:
-    // two blocks of eight per SM, one computing while the other adds its warps up.
-    const int64_t places = static_cast<int64_t>(p.T) * p.k, up_units = p.I / 64 * places, down_units = (p.H + 127) / 128 * places;
-    const auto grid = [&](int64_t units) { return static_cast<int>(units < 2 * sms ? units : 2 * sms); };
-    e = up_units <= sms ? launch_product<kBF, true, 16>(up, grid(up_units)) : launch_product<kBF, true, 8>(up, grid(up_units));
+    const auto grid = [&](int64_t tiles) {  // two blocks per SM: one computes while the other adds its warps up
+      const int64_t units = tiles * p.T * p.k;
+      return static_cast<int>(units < 2 * sms ? units : 2 * sms);
+    };
+    // (sixteen warps a block for few units, one block per SM: no faster, 25.2 us for one token of 8 of 128)
+    e = launch_product<kBF, true, 8>(up, grid(p.I / 64));
     if (e != cudaSuccess) return e;
-    return down_units <= sms ? launch_product<kBF, false, 16>(down, grid(down_units))
-                             : launch_product<kBF, false, 8>(down, grid(down_units));
+    return launch_product<kBF, false, 8>(down, grid((p.H + 127) / 128));
   }
   float* act = reinterpret_cast<float*>(ws);
   if (p.k > 0 && p.I > 0) {
