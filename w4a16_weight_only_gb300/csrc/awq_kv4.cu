@@ -44,6 +44,28 @@ struct Quantizer {
     const float c = rintf(__fdiv_rn(__fsub_rn(x * 0.5f, low * 0.5f), s * 0.5f));
     return static_cast<uint32_t>(fminf(fmaxf(c, 0.f), 15.f));
   }
+  // The codes of eight elements.  The quotient by a reciprocal is within 2^-22 of the rounded one's 16, so both
+  // round to the same code unless they are near the middle between two: then, rarely, the division decides
+  // (8191 tokens, keys and values of 8 heads of 128: 66 us with eight divisions, which bound the kernel).
+  __device__ __forceinline__ uint32_t codes(const float (&x)[8]) const {
+    if (!(s > 0.f)) return 0u;
+    const float half = low * 0.5f, per = __frcp_rn(s * 0.5f);
+    constexpr float kWhole = 12582912.f;  // 1.5 2^23: a sum with it is rounded to a whole number
+    uint32_t word = 0;
+    bool near = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float c = __fmul_rn(__fsub_rn(x[j] * 0.5f, half), per), w = __fadd_rn(c, kWhole), r = __fsub_rn(w, kWhole);
+      near |= !(fabsf(c - r) < 0.4999f);
+      word |= (min(__float_as_uint(w), __float_as_uint(kWhole) + 15u) & 15u) << (4 * j);
+    }
+    if (near) {
+      word = 0;
+#pragma unroll 1
+      for (int j = 0; j < 8; ++j) word |= code(x[j]) << (4 * j);
+    }
+    return word;
+  }
   __device__ __forceinline__ uint32_t params() const { return sb | (static_cast<uint32_t>(mb) << 16); }
 };
 
@@ -196,11 +218,17 @@ __device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
 
 template <bool kBF>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  return static_cast<uint32_t>(float_to_elem<kBF>(lo)) | (static_cast<uint32_t>(float_to_elem<kBF>(hi)) << 16);
+  if constexpr (kBF) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
 }
 
 template <bool kBF, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads, 12) append_vec_kernel(const AppendKv4Problem p, int q_parts, int q_per, int kv_per) {
+__global__ void __launch_bounds__(kThreads, 10) append_vec_kernel(const AppendKv4Problem p, int q_parts, int q_per, int kv_per) {
   const int L = p.D / 8, R = kThreads / L;  // threads of a row, rows of the block
   const int x = threadIdx.x % L, row = threadIdx.x / L;
   const int64_t t = blockIdx.x;
@@ -315,9 +343,7 @@ __global__ void __launch_bounds__(kThreads, 12) append_vec_kernel(const AppendKv
     uint8_t* tile = in ? tile_of(p.cache, slot, h, &r) : nullptr;
     if (!tile) continue;
     const Quantizer<kBF> quantizer(low, high, bad);
-    uint32_t word = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) word |= quantizer.code(f[j]) << (4 * j);
+    const uint32_t word = quantizer.codes(f);
     if (value) {
       uint8_t* codes = tile + 8 * p.D;
       *reinterpret_cast<uint16_t*>(codes + Kv4::value_byte(p.D, r, 4 * x)) = static_cast<uint16_t>(word);

@@ -10,8 +10,8 @@
 // and the codes themselves go to the tensor cores.  A word of codes ANDed with 0x000f000f is a pair of fp16
 // subnormals c 2^-24, with 0x00f000f0 a pair c 2^-20: an operand register costs one logic operation, and
 // every second one a shift.  The two kinds have accumulators of their own, scaled back at the end.
-// Queries are fp16 for either element type (a bf16 row is scaled by a power of two first), p s is rounded
-// to fp16 with s relative to the largest scale so far (a power of two, raised like the maximum).
+// Queries are fp16 for either element type (a bf16 row is scaled by a power of two first), p s is one fp16
+// number (fp16 elements: two) with s relative to the largest scale so far (a power of two, raised like the maximum).
 #pragma once
 
 #include <type_traits>
@@ -125,6 +125,9 @@ __device__ __forceinline__ float weight(float m, float l, float top) { return l 
 template <bool kBF, int D, int G, int NT>
 __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attention_kernel(const __grid_constant__ Args a) {
   using S = Shape<D, G, NT>;
+  // fp16 results show the rounding of p s (2.4 times the error of the result's own, 16 x 4 over 2047): it is taken
+  // as two fp16 terms there.  bf16's own rounding hides it.
+  constexpr int kTerms = kBF ? 1 : 2;
   constexpr int U = S::U, W = S::W, STAGES = S::STAGES, ROWS = S::ROWS, PER_GROUP = U / G;  // words of a group
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t coarse[kCoarse];
@@ -543,7 +546,6 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
               z[m][1][h] = exp2_approx(z[m][1][h] - ref);
               sum[m][h] += z[m][0][h] + z[m][1][h];
             }
-          const float middle = 7.5f * unit;
           uint32_t vw[U][2];  // word, half of the keys
 #pragma unroll
           for (int n = 0; n < U / 2; ++n) {
@@ -560,7 +562,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
           }
 #pragma unroll
           for (int q = 0; q < G; ++q) {
-            uint32_t pf[NT][2];
+            uint32_t pf[kTerms][NT][2];
 #pragma unroll
             for (int m = 0; m < NT; ++m)
 #pragma unroll
@@ -575,16 +577,12 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
                 const uint32_t rounded = pack_half(ps[0], ps[1]);
                 low[m][q][0] += pm[0];
                 low[m][q][1] += pm[1];
-                if constexpr (!kBF) {
-                  // What the rounding of p s takes from the code in the middle goes to the minima's sum, so that
-                  // its error is that of a value's distance from there (16 x 4 over 2047, fp16: 4.9e-4 against
-                  // 64 bits without).  bf16's own rounding hides it, and it costs 2 % there.
-                  const float2 kept = __half22float2(*reinterpret_cast<const __half2*>(&rounded));
-                  low[m][q][0] += (ps[0] - kept.x) * middle;
-                  low[m][q][1] += (ps[1] - kept.y) * middle;
-                }
                 // P^T has keys along the lanes' rows; the second product wants them along the registers
-                pf[m][half] = transpose8(rounded);
+                pf[0][m][half] = transpose8(rounded);
+                if constexpr (kTerms == 2) {
+                  const float2 kept = __half22float2(*reinterpret_cast<const __half2*>(&rounded));
+                  pf[1][m][half] = transpose8(pack_half(ps[0] - kept.x, ps[1] - kept.y));
+                }
               }
 #pragma unroll
             for (int u = q * PER_GROUP; u < (q + 1) * PER_GROUP; ++u) {
@@ -594,7 +592,9 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
                 const uint32_t mask = c ? 0x00f000f0u : 0x000f000fu;
                 const uint32_t a0 = x0w & mask, a1 = y0w & mask, a2 = x1w & mask, a3 = y1w & mask;
 #pragma unroll
-                for (int m = 0; m < NT; ++m) ptx::mma16816(o[m][u][c], a0, a1, a2, a3, pf[m][0], pf[m][1]);
+                for (int m = 0; m < NT; ++m)
+#pragma unroll
+                  for (int k = 0; k < kTerms; ++k) ptx::mma16816(o[m][u][c], a0, a1, a2, a3, pf[k][m][0], pf[k][m][1]);
               }
             }
           }
