@@ -46,9 +46,13 @@ struct Shape {
   static constexpr int ROWS = 8 * NT;
   static constexpr int PART = ROWS * (D + 2) * 4;           // bytes of a partial result: sums, then (max, sum of p)
   static constexpr int BLOCKS = blocks_per_sm(D, NT);
-  static constexpr int STAGES = least(8, ((228 / BLOCKS - 1) * 1024 - 4096) / kWarps / TILE);
+  // Two blocks per SM leave 128 registers: the queries' fragments are read from shared memory for every tile.
+  static constexpr bool Q_SHARED = BLOCKS == 2;
+  static constexpr int QUERIES = Q_SHARED ? NT * U * 512 : 0;  // bytes of a warp
+  static constexpr int STAGES = least(8, (((228 / BLOCKS - 1) * 1024 - 4096) / kWarps - QUERIES) / TILE);
   static constexpr int RING = (most(STAGES * TILE, PART) + 127) / 128 * 128;  // of a warp
-  static constexpr int BARS = kWarps * RING;                // offset of the barriers
+  static constexpr int QS = kWarps * RING;                  // offset of the queries
+  static constexpr int BARS = QS + kWarps * QUERIES;        // of the barriers
   static constexpr int SMEM = BARS + kWarps * STAGES * 8;
   static_assert(STAGES >= 3 && SMEM + 4096 <= (228 / BLOCKS - 1) * 1024, "shared memory");
 };
@@ -200,6 +204,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
   uint8_t* ring = smem + warp * S::RING;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::BARS) + warp * STAGES;
   float* own_part = reinterpret_cast<float*>(ring);
+  uint4* queries = reinterpret_cast<uint4*>(smem + S::QS + warp * S::QUERIES) + lane;  // [NT][U][32]
   const auto first_part = [&](int w) { return a.firsts + (static_cast<int64_t>(blockIdx.x) * kWarps + w) * (S::PART / 4); };
 
   if (x0 < x1) {
@@ -333,7 +338,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
       // keys up to here are out of the window
       const int low0 = p.window > 0 ? static_cast<int>(max(static_cast<int64_t>(pos0) - p.window, int64_t{-1})) : -1;
       const int low1 = p.window > 0 ? static_cast<int>(max(static_cast<int64_t>(pos1) - p.window, int64_t{-1})) : -1;
-      uint32_t qf[NT][U][2][2];  // word, kind, half of the contraction
+      uint4 qf[S::Q_SHARED ? 1 : NT][S::Q_SHARED ? 1 : U];  // of a word: kind 0 (halves of the contraction), kind 1
       float qsum[NT][G][2];      // sums of the lane's two columns' queries over a group
       float zscale[NT][2];       // what takes a column's product to a base-2 logit
       int pos[NT][2];            // positions of the lane's two columns' tokens
@@ -369,10 +374,9 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
                        e45 = ptx::pair_to_float2<kBF>(raw[u].z), e67 = ptx::pair_to_float2<kBF>(raw[u].w);
           const float e[8] = {e01.x * factor, e01.y * factor, e23.x * factor, e23.y * factor,
                               e45.x * factor, e45.y * factor, e67.x * factor, e67.y * factor};
-          qf[m][u][0][0] = pack_half(e[0], e[4]);
-          qf[m][u][0][1] = pack_half(e[2], e[6]);
-          qf[m][u][1][0] = pack_half(e[1], e[5]);
-          qf[m][u][1][1] = pack_half(e[3], e[7]);
+          const uint4 f = make_uint4(pack_half(e[0], e[4]), pack_half(e[2], e[6]), pack_half(e[1], e[5]), pack_half(e[3], e[7]));
+          if constexpr (S::Q_SHARED) queries[(m * U + u) * 32] = f;  // a lane reads what it wrote
+          else qf[m][u] = f;
           gs[u / PER_GROUP] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
         }
 #pragma unroll
@@ -447,12 +451,18 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
 #pragma unroll
             for (int w = q * PER_GROUP; w < (q + 1) * PER_GROUP; ++w) {
               const uint32_t x0w = kw[0][w], x1w = kw[1][w], y0w = x0w >> 8, y1w = x1w >> 8;
+              uint4 f[NT];
+#pragma unroll
+              for (int m = 0; m < NT; ++m) {
+                if constexpr (S::Q_SHARED) f[m] = queries[(m * U + w) * 32];
+                else f[m] = qf[m][w];
+              }
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
                 const uint32_t mask = c ? 0x00f000f0u : 0x000f000fu;
                 const uint32_t a0 = x0w & mask, a1 = x1w & mask, a2 = y0w & mask, a3 = y1w & mask;
 #pragma unroll
-                for (int m = 0; m < NT; ++m) ptx::mma16816(acc[m][c], a0, a1, a2, a3, qf[m][w][c][0], qf[m][w][c][1]);
+                for (int m = 0; m < NT; ++m) ptx::mma16816(acc[m][c], a0, a1, a2, a3, c ? f[m].z : f[m].x, c ? f[m].w : f[m].y);
               }
             }
             const float2 p0 = ptx::pair_to_float2<kBF>(params[q]), p1 = ptx::pair_to_float2<kBF>(params[8 * G + q]);
