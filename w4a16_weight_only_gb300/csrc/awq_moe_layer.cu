@@ -210,7 +210,9 @@ __device__ __forceinline__ void box_load(void* dst, const CUtensorMap* map, uint
 // row.  fp16: a pair of codes ANDed out of the words is c 2^-24 or c 2^-20, a subnormal number, exact;
 // bf16: with the exponent ORed in it is 128 + c.  The zero (and 128) leaves with the sum of x, which an
 // mma against ones gives in the same layout; a group's sums are scaled into fp32 totals.
-// Each warp has a ring of stages of its own, filled by TMA across units.
+// Each warp has a ring of stages of its own, filled by TMA across units: 16 tokens of 8 of 128 experts, 4096 x
+// 1792, some 940 MB in 228 us for both products, 4.1 TB/s (words loaded ahead into registers instead: 630 us, a
+// warp waits for its newest load with its oldest).  Bound by the unpacking and the issue of 32-byte box rows.
 template <bool kBF, bool kUp, int kW>
 __global__ void __launch_bounds__(kW * 32, 16 / kW) moe_kernel(const __grid_constant__ Args args) {
   using SH = Shared<kW>;
