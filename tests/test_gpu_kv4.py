@@ -259,6 +259,23 @@ def test_attention(awq, case, dtype):
     assert torch.equal(out, awq.awq_attention_kv4(**call, window=window, sinks=sinks))
 
 
+def test_pages_beyond_four_gigabytes(awq):
+    # byte offsets of pages and cells pass 32 bits
+    call, keys, values = make(awq, 2, 2, 8, 2, 128, 128, [90, 140], 64, "bf16", seed=17)
+    nbytes = awq.awq_kv4_page_bytes(64, 128)
+    far = (9 << 29) // (2 * nbytes)  # pages: 4.5 GiB in front
+    cache = torch.empty((far + call["cache"].shape[0], 2, nbytes), dtype=torch.uint8, device="cuda")
+    cache[far:] = call["cache"]
+    check(awq.awq_attention_kv4(**dict(call, cache=cache, pages=call["pages"] + far)), call, keys, values, "bf16")
+    slots = (call["pages"][1, :2].repeat_interleave(64) * 64 + torch.arange(128, device="cuda") % 64).int()
+    k, v = awq.awq_kv4_read(call["cache"], slots, 128, dtype=torch.bfloat16)
+    for got, want in zip(awq.awq_kv4_read(cache, slots + far * 64, 128, dtype=torch.bfloat16), (k, v)):
+        assert torch.equal(got, want)
+    awq.awq_rope_append_kv4(None, v, k, None, None, cache, slots + far * 64)
+    awq.awq_rope_append_kv4(None, v, k, None, None, call["cache"], slots)
+    assert torch.equal(cache[far:], call["cache"])
+
+
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 @pytest.mark.parametrize("sharp,scale", [(8.0, None), (1.0, 0.0), (1.0, -0.2), (30.0, 0.5)])
 def test_logits(awq, dtype, sharp, scale):

@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(256) read_any_kernel(const ReadKv4Problem p) {
 // query heads (rotated and written), then keys and values, whose groups are 4, 8 or 16 neighbouring lanes.  A
 // vector's codes are one word of the keys, half a word each of two of the values.  Bound by instructions for many
 // tokens (8191 of 32 + 8 heads of 128, fp16, 176 MB: 54 us), a round trip for few; ten blocks of an SM's 48 registers
-// a thread hide it best (twelve spill, eight of 76 with four heads in flight: 57 and 66 us).
+// a thread (twelve spill: 56 us).
 constexpr int kThreads = 128;
 constexpr int kFlight = 2;
 

@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
             for (int d = 4; d < 32; d <<= 1) wide = fmaxf(wide, __shfl_xor_sync(0xffffffffu, wide, d));
             float change = 1.f;
             if (wide > unit) {
-              const uint32_t up = min((__float_as_uint(wide) & 0x7f800000u) + 0x00800000u, 250u << 23);
+              const uint32_t up = min((__float_as_uint(wide) & 0x7f800000u) + 0x00800000u, 253u << 23);
               change = unit / __uint_as_float(up);
               unit = __uint_as_float(up);
               per_unit = __uint_as_float((254u << 23) - up);
