@@ -259,6 +259,18 @@ def test_attention(awq, case, dtype):
     assert torch.equal(out, awq.awq_attention_kv4(**call, window=window, sinks=sinks))
 
 
+def test_many_short_sequences(awq):
+    # more sequences than entries of a block's table of lengths, several of them in a warp's share, some empty
+    B = 700
+    lens = [(7 * i) % 37 for i in range(B)]
+    call, keys, values = make(awq, B, 1, 8, 4, 64, 64, lens, 16, "fp16", seed=18)
+    out = awq.awq_attention_kv4(**call)
+    some = list(range(0, B, 29)) + [B - 1]
+    part = dict(call, q=call["q"][some], lens=call["lens"][some])
+    check(out[some], part, [keys[i] for i in some], [values[i] for i in some], "fp16")
+    assert (out[call["lens"] == 0] == 0).all() and torch.equal(out, awq.awq_attention_kv4(**call))
+
+
 def test_pages_beyond_four_gigabytes(awq):
     # byte offsets of pages and cells pass 32 bits
     call, keys, values = make(awq, 2, 2, 8, 2, 128, 128, [90, 140], 64, "bf16", seed=17)
