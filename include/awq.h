@@ -693,10 +693,11 @@ awq_status_t awq_kv4_read(const awq_kv4_cache_t* cache, const int32_t* slots, in
  *   pages int32 [B, W] (row stride pages_stride): the sequences' pages, in order; lens int32 [B], the n new
  *   tokens counted (one above W * page_size is cut to it).  Pages that a window leaves out may be any
  *   number: they are not read.
- * k_j and v_j are what the codes stand for, unrounded; logits, statistics and sums are fp32; the factor of a
- * value, probability times scale, is rounded to fp16's 11 bits (fp16 elements: 22).  A sequence's keys are cut
- * into parts by all sequences' lengths, so other lengths may change its result's last bits.  Values above
- * 2^100 in size (bf16) may overflow.
+ * k_j and v_j are what the codes stand for, unrounded; logits, statistics and sums are fp32.  The factor of a
+ * value, probability times scale, is rounded to fp16's 11 bits (fp16 elements: 22), in steps of at least 2^-31
+ * of the largest factor of the same query row and group of elements, and an element of a bf16 query in steps
+ * of at least 2^-28 of the row's largest.  A sequence's keys are cut into parts by all sequences' lengths, so
+ * other lengths may change its result's last bits.  Keys and values above 2^100 in size (bf16) may overflow.
  * A row uses only the keys that it sees: what the cache holds elsewhere
  * may be anything.  A page outside [0, num_pages) gives unspecified values for its sequence.  A row that
  * sees no key is zero; one whose logits are all -inf is NaN.  B, n or Hq 0: AWQ_OK, no launch.

@@ -12,8 +12,8 @@
 // 128 sequences of up to 8197, 8 heads, 765 MB in 172 us, 4.4 TB/s.  A word of codes ANDed with 0x000f000f is a pair of fp16
 // subnormals c 2^-24, with 0x00f000f0 a pair c 2^-20: an operand register costs one logic operation, and
 // every second one a shift.  The two kinds have accumulators of their own, scaled back at the end.
-// Queries are fp16 for either element type (a bf16 row is scaled by a power of two first), p s is one fp16
-// number (fp16 elements: two) with s relative to the largest scale so far (a power of two, raised like the maximum).
+// Queries are fp16 for either element type (a bf16 row is scaled by a power of two first: exact down to 2^-18 of its
+// largest element, in steps of 2^-28 below), p s is one fp16 number (fp16 elements: two) in a unit of its row and group.
 #pragma once
 
 #include <type_traits>
@@ -25,7 +25,6 @@ namespace awq {
 namespace kv4 {
 
 using attn::exp2_approx;
-using attn::kLift;
 using attn::kRaise;
 
 constexpr int kWarps = 8;
@@ -122,9 +121,58 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Two products, and two products with sums, in one instruction each.
+__device__ __forceinline__ void mul2(float (&d)[2], float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d[0]), "=f"(d[1])
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void fma2(float (&d)[2], float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%0, %1};\n\t"
+      "fma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
+      : "+f"(d[0]), "+f"(d[1])
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
 __device__ __forceinline__ float quiet_nan() { return __int_as_float(0x7fffffff); }
 
 constexpr float kTwo24 = 16777216.f, kTwo20 = 1048576.f;
+
+// A probability is kept as p = 2^(z - top), top a whole number that is raised only when a logit exceeds it by kRaise; the
+// factor of a key's codes, p times its scale, as an fp16 number in units of 2^e, e a whole number for each query row
+// and group of elements, raised only when a factor reaches 2^kFactorEnd, to where the largest is in 2^kFactorLog ..
+// 2^(kFactorLog + 1).  Both change for those rows and groups alone whose own keys ask for it: neither a key that a row
+// does not see nor one of no weight takes bits from the others.  64 over 8197, 64 / 8 heads of 128, groups of 32: 134 us,
+// 143 us where one group's values are 2^-6 of another's or less (194 us if the bound alone decided, 139 us if each tile
+// were looked at group by group); with one unit for all rows and groups 126 us, with other groups as now.  fp16 numbers have their 11 bits down to 2^-14 and steps of 2^-24 below: 2^-21 and 2^-31 of a row's
+// largest.  Units go from 2^-110 (values that small are near bf16's smallest number) to 2^126; 2^-e is kept as bf16,
+// two groups to a word.
+constexpr float kNoTop = -3.402823466e38f;
+constexpr int kFactorLog = 7, kFactorEnd = 15;
+constexpr float kLastFactor = kFactorEnd - 0.01f;  // its base-2 logarithm, by approximate ones
+constexpr int kLeastUnit = -110, kMostUnit = 126;
+constexpr uint32_t kLeastUnits = static_cast<uint32_t>(127 - kLeastUnit) << 23;
+
+template <int G>
+__device__ __forceinline__ float per_unit(const uint32_t* units, int group) {
+  return __uint_as_float(G == 1 ? units[0] : group % 2 ? units[group / 2] << 16 : units[group / 2] & 0xffff0000u);
+}
+template <int G>
+__device__ __forceinline__ int unit_log(const uint32_t* units, int group) {
+  return 127 - static_cast<int>(__float_as_uint(per_unit<G>(units, group)) >> 23);
+}
+
+__device__ __forceinline__ float log2_approx(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 2^x for whole x up to 127, 0 where that is below the normal numbers.
+__device__ __forceinline__ float whole_exp2(float x) {
+  return x < -126.f ? 0.f : __uint_as_float(static_cast<uint32_t>(static_cast<int>(x) + 127) << 23);
+}
 
 // Weight of a partial result (max m, sum l) against the maximum `top` of all.
 __device__ __forceinline__ float weight(float m, float l, float top) { return l == 0.f ? 0.f : l * exp2_approx(m - top); }
@@ -396,6 +444,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
         }
       }
       float o[NT][U][2][4], top[NT][2], sum[NT][2], low[NT][G][2];  // low: sums of p times the values' minima
+      uint32_t units[NT][2][(G + 1) / 2];
+      float least_unit[NT][2];  // of its groups, as e
 #pragma unroll
       for (int m = 0; m < NT; ++m) {
 #pragma unroll
@@ -404,13 +454,15 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
           for (int c = 0; c < 2; ++c) o[m][u][c][0] = o[m][u][c][1] = o[m][u][c][2] = o[m][u][c][3] = 0.f;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          top[m][h] = -INFINITY;
+          top[m][h] = kNoTop;
+#pragma unroll
+          for (int w = 0; w < (G + 1) / 2; ++w) units[m][h][w] = G == 1 ? kLeastUnits : kLeastUnits | kLeastUnits >> 16;
+          least_unit[m][h] = kLeastUnit;
           sum[m][h] = 0.f;
 #pragma unroll
           for (int q = 0; q < G; ++q) low[m][q][h] = 0.f;
         }
       }
-      float unit = __uint_as_float(0x00800000u), per_unit = __uint_as_float(253u << 23);  // 2^-126, 2^126
 
       for (int i = begin; i < end; ++i) {
         if (p.give_up || !arrived(stage, phase)) {
@@ -472,9 +524,15 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
 #pragma unroll
             for (int m = 0; m < NT; ++m)
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                z[m][0][h] += p0.x * (acc[m][0][h] * kTwo24 + acc[m][1][h] * kTwo20) + p0.y * qsum[m][q][h];
-                z[m][1][h] += p1.x * (acc[m][0][2 + h] * kTwo24 + acc[m][1][2 + h] * kTwo20) + p1.y * qsum[m][q][h];
+              for (int half = 0; half < 2; ++half) {
+                const float2 sm = half ? p1 : p0;
+                const float* a0 = acc[m][0] + 2 * half;
+                const float* a1 = acc[m][1] + 2 * half;
+                float both[2];
+                mul2(both, a1[0], a1[1], kTwo20, kTwo20);
+                fma2(both, a0[0], a0[1], kTwo24, kTwo24);
+                fma2(z[m][half], both[0], both[1], sm.x, sm.x);
+                fma2(z[m][half], qsum[m][q][0], qsum[m][q][1], sm.y, sm.y);
               }
           }
           uint32_t seen = 0xffffffffu;  // bit 4 m + 2 half + h
@@ -492,41 +550,55 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
             }
           }
           float2 v[2][G];  // (scale, minimum) of the values
-          float widest = 0.f;
 #pragma unroll
           for (int half = 0; half < 2; ++half)
 #pragma unroll
-            for (int q = 0; q < G; ++q) {
-              v[half][q] = ptx::pair_to_float2<kBF>(params[16 * G + 8 * half * G + q]);
-              // a key that no row sees may hold anything
-              const int key = k0 + g + 8 * half;
-              if (kMasked && !(key <= pos1 && (key > low0 || key < p.sinks))) v[half][q] = make_float2(0.f, 0.f);
-              widest = fmaxf(widest, v[half][q].x);
-            }
-          bool raise = widest > unit;
+            for (int q = 0; q < G; ++q) v[half][q] = ptx::pair_to_float2<kBF>(params[16 * G + 8 * half * G + q]);
+          float widest[2];  // of a key's scales, base-2 logarithm
 #pragma unroll
-          for (int m = 0; m < NT; ++m)
+          for (int half = 0; half < 2; ++half) {
+            widest[half] = v[half][0].x;
+#pragma unroll
+            for (int q = 1; q < G; ++q) widest[half] = fmaxf(widest[half], v[half][q].x);
+            widest[half] = log2_approx(widest[half]);
+          }
+          bool raise = false;
+#pragma unroll
+          for (int m = 0; m < NT; ++m) {
+            mul2(z[m][0], z[m][0][0], z[m][0][1], zscale[m][0], zscale[m][1]);
+            mul2(z[m][1], z[m][1][0], z[m][1][1], zscale[m][0], zscale[m][1]);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
+              if constexpr (kMasked) {
 #pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                z[m][half][h] *= zscale[m][h];
-                if (kMasked && !((seen >> (4 * m + 2 * half + h)) & 1u)) z[m][half][h] = -INFINITY;
+                for (int half = 0; half < 2; ++half)
+                  if (!((seen >> (4 * m + 2 * half + h)) & 1u)) z[m][half][h] = -INFINITY;
               }
-              raise |= fmaxf(z[m][0][h], z[m][1][h]) > top[m][h] + kRaise;
+              raise |= fmaxf(z[m][0][h], z[m][1][h]) - top[m][h] > kRaise;
+              // a key's largest factor, of several groups at most; fmaxf leaves out the NaN of a masked key
+              raise |= fmaxf(z[m][0][h] + widest[0], z[m][1][h] + widest[1]) - top[m][h] - least_unit[m][h] > kLastFactor;
             }
-          // a row's maximum is raised when a logit exceeds it by kRaise, the unit when a scale does
-          if (__any_sync(0xffffffffu, raise)) {
-            float wide = widest;
+          }
+          raise = __any_sync(0xffffffffu, raise);
+          if constexpr (G > 1) {
+            if (raise) {  // group by group: where one's values are 2^-6 of another's, that bound says yes for every tile
+              raise = false;
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) wide = fmaxf(wide, __shfl_xor_sync(0xffffffffu, wide, d));
-            float change = 1.f;
-            if (wide > unit) {
-              const uint32_t up = min((__float_as_uint(wide) & 0x7f800000u) + 0x00800000u, 253u << 23);
-              change = unit / __uint_as_float(up);
-              unit = __uint_as_float(up);
-              per_unit = __uint_as_float((254u << 23) - up);
+              for (int m = 0; m < NT; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  raise |= fmaxf(z[m][0][h], z[m][1][h]) - top[m][h] > kRaise;
+                  float scaled[2] = {0.f, 0.f};
+#pragma unroll
+                  for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int q = 0; q < G; ++q) scaled[half] = fmaxf(scaled[half], per_unit<G>(units[m][h], q) * v[half][q].x);
+                  raise |= fmaxf(z[m][0][h] + log2_approx(scaled[0]), z[m][1][h] + log2_approx(scaled[1])) - top[m][h] > kLastFactor;
+                }
+              raise = __any_sync(0xffffffffu, raise);
             }
+          }
+          if (raise) {
 #pragma unroll
             for (int m = 0; m < NT; ++m)
 #pragma unroll
@@ -534,29 +606,45 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
                 float now = fmaxf(z[m][0][h], z[m][1][h]);
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, d));
-                now = fmaxf(now, top[m][h]);
-                const float shrink = now == -INFINITY ? 1.f : exp2_approx(top[m][h] - now);
-                top[m][h] = now;
+                const float to = now - top[m][h] > kRaise ? ceilf(now) : top[m][h];
+                const float down = top[m][h] - to, shrink = whole_exp2(down);
+                top[m][h] = to;
                 sum[m][h] *= shrink;
+                const float p[2] = {exp2_approx(z[m][0][h] - to), exp2_approx(z[m][1][h] - to)};
+                uint32_t kept[(G + 1) / 2] = {};
+                float least = kMostUnit;
 #pragma unroll
-                for (int q = 0; q < G; ++q) low[m][q][h] *= shrink;
-                const float both = shrink * change;
+                for (int q = 0; q < G; ++q) {
+                  low[m][q][h] *= shrink;
+                  float wide = fmaxf(fmaxf(p[0] * v[0][q].x, p[1] * v[1][q].x), 0.f);
 #pragma unroll
-                for (int u = 0; u < U; ++u)
+                  for (int d = 4; d < 32; d <<= 1) wide = fmaxf(wide, __shfl_xor_sync(0xffffffffu, wide, d));
+                  const int log = static_cast<int>(__float_as_uint(wide) >> 23) - 127;
+                  const float was = static_cast<float>(unit_log<G>(units[m][h], q)), moved = was + down;  // the same factors' unit
+                  float unit = log - moved >= kFactorEnd ? static_cast<float>(log - kFactorLog) : moved;
+                  unit = fminf(fmaxf(unit, static_cast<float>(kLeastUnit)), static_cast<float>(kMostUnit));
+                  kept[q / 2] |= static_cast<uint32_t>(127 - static_cast<int>(unit)) << (q % 2 ? 7 : 23);
+                  least = fminf(least, unit);
+                  const float change = whole_exp2(moved - unit);
 #pragma unroll
-                  for (int c = 0; c < 2; ++c) {
-                    o[m][u][c][h] *= both;
-                    o[m][u][c][2 + h] *= both;
-                  }
+                  for (int u = q * PER_GROUP; u < (q + 1) * PER_GROUP; ++u)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                      o[m][u][c][h] *= change;
+                      o[m][u][c][2 + h] *= change;
+                    }
+                }
+#pragma unroll
+                for (int w = 0; w < (G + 1) / 2; ++w) units[m][h][w] = kept[w];
+                least_unit[m][h] = least;
               }
           }
 #pragma unroll
           for (int m = 0; m < NT; ++m)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const float ref = top[m][h] == -INFINITY ? 0.f : top[m][h] - kLift;  // a row that has seen no key yet: 0
-              z[m][0][h] = exp2_approx(z[m][0][h] - ref);
-              z[m][1][h] = exp2_approx(z[m][1][h] - ref);
+              z[m][0][h] = exp2_approx(z[m][0][h] - top[m][h]);
+              z[m][1][h] = exp2_approx(z[m][1][h] - top[m][h]);
               sum[m][h] += z[m][0][h] + z[m][1][h];
             }
           uint32_t vw[U][2];  // word, half of the keys
@@ -580,16 +668,21 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
             for (int m = 0; m < NT; ++m)
 #pragma unroll
               for (int half = 0; half < 2; ++half) {
-                const float s = v[half][q].x * per_unit, mn = v[half][q].y;
-                float ps[2] = {z[m][half][0] * s, z[m][half][1] * s}, pm[2] = {z[m][half][0] * mn, z[m][half][1] * mn};
+                const float s = v[half][q].x, mn = v[half][q].y;
+                float ps[2];
+                mul2(ps, z[m][half][0], z[m][half][1], per_unit<G>(units[m][0], q), per_unit<G>(units[m][1], q));
+                mul2(ps, ps[0], ps[1], s, s);
                 if constexpr (kMasked) {  // zero times a value that is not finite
+                  float pm[2] = {z[m][half][0] * mn, z[m][half][1] * mn};
 #pragma unroll
                   for (int h = 0; h < 2; ++h)
                     if (!((seen >> (4 * m + 2 * half + h)) & 1u)) ps[h] = pm[h] = 0.f;
+                  low[m][q][0] += pm[0];
+                  low[m][q][1] += pm[1];
+                } else {
+                  fma2(low[m][q], z[m][half][0], z[m][half][1], mn, mn);
                 }
                 const uint32_t rounded = pack_half(ps[0], ps[1]);
-                low[m][q][0] += pm[0];
-                low[m][q][1] += pm[1];
                 // P^T has keys along the lanes' rows; the second product wants them along the registers
                 pf[0][m][half] = transpose8(rounded);
                 if constexpr (kTerms == 2) {
@@ -659,6 +752,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             const float lo = inv * kTwo24, hi = inv * kTwo20, mn = lows[u / PER_GROUP] * inv;
+            const float unit = __uint_as_float(static_cast<uint32_t>(127 + unit_log<G>(units[m][h], u / PER_GROUP)) << 23);
             const float e[4] = {o[m][u][0][h] * lo * unit + mn, o[m][u][1][h] * hi * unit + mn, o[m][u][0][2 + h] * lo * unit + mn,
                                 o[m][u][1][2 + h] * hi * unit + mn};
             if (!whole) {
@@ -671,7 +765,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
             }
           }
           if (!whole && g == 0)
-            *reinterpret_cast<float2*>(to + ROWS * D + 2 * in_tile) = make_float2(top[m][h] == -INFINITY ? top[m][h] : top[m][h] - kLift, l);
+            *reinterpret_cast<float2*>(to + ROWS * D + 2 * in_tile) = make_float2(top[m][h], l);
         }
       if (!whole && lane == 0) {
         const int64_t start = x - begin, stop = start + cur.r.count;  // of the unit on the line
