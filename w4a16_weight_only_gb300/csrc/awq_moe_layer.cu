@@ -498,7 +498,11 @@ template <bool kBF, bool kUp, int kW>
 cudaError_t launch_product(const Args& args, int grid) {
   const auto kernel = moe_kernel<kBF, kUp, kW>;
   const int smem = Shared<kW>::JOBS + Jobs::bytes(args.p.T * args.p.k);
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // the attribute is the function's, not the call's: the most that any call needs, or another host thread's smaller
+  // call would lower it between this call's attribute and its launch
+  constexpr int most = Shared<kW>::JOBS + Jobs::bytes(kMaxPlaces);
+  static_assert(most <= 227 * 1024, "shared memory of a block");
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];  // the second product's weights are on their way before the first has ended
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
