@@ -58,3 +58,18 @@ def test_moe_layers_of_different_sizes(awq):
 
     failed = together([layer(1, 1), layer(16, 32), layer(3, 1), layer(16, 16), layer(2, 1), layer(16, 31), layer(1, 2), layer(16, 30)], 3000)
     assert not failed, failed[:1]
+
+
+def test_dispatches_of_different_numbers_of_experts(awq):
+    g = torch.Generator(device="cuda").manual_seed(2)
+
+    def dispatch(E):
+        x = torch.randn((600, 64), generator=g, device="cuda").half()
+        ids = torch.randint(0, E, (600, 4), generator=g, device="cuda", dtype=torch.int64).int()
+        out = (torch.empty((2400, 64), dtype=torch.float16, device="cuda"), torch.empty((E + 1,), dtype=torch.int32, device="cuda"),
+               torch.empty((600, 4), dtype=torch.int32, device="cuda"))
+        ws = torch.empty((awq.awq_moe_dispatch_workspace_size(600, 4, E),), dtype=torch.uint8, device="cuda")
+        return lambda: awq.awq_moe_dispatch(x, ids, E, out=out, workspace=ws)
+
+    failed = together([dispatch(1500), dispatch(4096), dispatch(2000), dispatch(3500), dispatch(1300), dispatch(4000)], 3000)
+    assert not failed, failed[:1]

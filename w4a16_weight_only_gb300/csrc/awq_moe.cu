@@ -577,7 +577,11 @@ cudaError_t run_dispatch(const DispatchProblem& p) {
   int* hist = dest + R;
   const int smem = (kSortWarps + 2) * bins * 4;
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(dispatch_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // the attribute is the function's, not the call's: the most that any call needs, or another host thread's call with
+    // fewer experts would lower it between this call's attribute and its launch
+    constexpr int most = (kSortWarps + 2) * (kDispatchMaxE + 1) * 4;
+    static_assert(most <= 227 * 1024, "shared memory of a block");
+    const cudaError_t e = cudaFuncSetAttribute(dispatch_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
   }
   dispatch_count_kernel<<<blocks, kSortThreads, bins * 4, p.stream>>>(p, hist);
