@@ -778,11 +778,12 @@ awq_status_t awq_device_status(awq_stream_t stream);
  * the word).  Asynchronous on `stream`; one launch.  No counterpart on the pages. */
 awq_status_t awq_selftest_wait_timeout(uint64_t limit_ns, awq_stream_t stream);
 
-/* Failure-detection self test of awq_attention_shared and awq_attention_kv4: after on != 0, the calling host
- * thread's calls give up their kernels' waits for copies as if they had run out (on == 0: back to normal).  Such a
- * call's output is unspecified, it touches nothing outside its tensors, and a following
- * awq_device_status returns AWQ_ERR_TIMEOUT; calls whose pages are copied without a wait that can run
- * out (page_size % 16 != 0, fewer than 3 steps of a block) are unaffected.  Host only. */
+/* Failure-detection self test of awq_attention_shared, awq_attention_kv4 and awq_moe_layer: after on != 0, the
+ * calling host thread's calls give up their kernels' waits for copies as if they had run out (on == 0: back to
+ * normal).  Such a call's output is unspecified, it touches nothing outside its tensors, and a following
+ * awq_device_status returns AWQ_ERR_TIMEOUT; calls whose copies have no wait that can run out
+ * (awq_attention_shared: page_size % 16 != 0, fewer than 3 steps of a block; awq_moe_layer: H or I no multiple of
+ * 64) are unaffected.  Host only. */
 awq_status_t awq_selftest_attention_give_up(int on);
 
 #ifdef __cplusplus

@@ -146,3 +146,22 @@ def test_places_left_out_and_repeated(awq, dtype):
     out = awq.awq_moe_layer(**d)
     check(out, d, dtype)
     assert torch.equal(out[3], d["base"][3])
+
+
+@pytest.mark.parametrize("size", [0, 1, 8])
+def test_waits_that_give_up(awq, size):
+    # as if no copy arrived in time: an error status, tensors around the outputs as they were, and the next call is right
+    d = inputs(*CASES[size], "bf16", seed=31, base=False)
+    T, H = d["x"].shape
+    around = torch.full((T + 2, H), 7.0, dtype=torch.bfloat16, device="cuda")
+    need = awq.awq_moe_layer_workspace_size(T, d["experts"].shape[1], H, d["down"][0].shape[1])
+    ws = torch.full((need + 512,), 7, dtype=torch.uint8, device="cuda")
+    awq.selftest_attention_give_up(True)
+    try:
+        awq.awq_moe_layer(**d, out=around[1:-1], workspace=ws[256:256 + need])
+    finally:
+        awq.selftest_attention_give_up(False)
+    with pytest.raises(awq.AwqError):
+        awq.device_status()
+    assert (around[0] == 7).all() and (around[-1] == 7).all() and (ws[:256] == 7).all() and (ws[256 + need:] == 7).all()
+    check(awq.awq_moe_layer(**d, workspace=ws[256:256 + need]), d, "bf16")

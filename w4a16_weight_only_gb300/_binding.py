@@ -509,8 +509,8 @@ def selftest_wait_timeout(limit_ns=2_000_000, stream=None):
 
 
 def selftest_attention_give_up(on):
-    """Let this thread's awq_attention_shared and awq_attention_kv4 calls
-    give up their kernels' waits (awq.h), or wait again."""
+    """Let this thread's awq_attention_shared, awq_attention_kv4 and awq_moe_layer calls give up their kernels'
+    waits (awq.h), or wait again."""
     _check(load_library().awq_selftest_attention_give_up(1 if on else 0))
 
 

@@ -13,7 +13,7 @@
 namespace {
 
 thread_local std::string g_err;
-thread_local bool g_attention_gives_up = false;  // awq_selftest_attention_give_up
+thread_local bool g_waits_give_up = false;  // awq_selftest_attention_give_up
 
 awq_status_t fail(awq_status_t st, const char* fmt, ...) {
   char buf[512];
@@ -667,7 +667,7 @@ awq_status_t awq_selftest_wait_timeout(uint64_t limit_ns, awq_stream_t stream) {
 }
 
 awq_status_t awq_selftest_attention_give_up(int on) {
-  g_attention_gives_up = on != 0;
+  g_waits_give_up = on != 0;
   return ok();
 }
 
@@ -917,7 +917,7 @@ awq_status_t awq_attention_shared(const void* q, int64_t B, int64_t n, int64_t H
   p.scale = scale;
   p.out = static_cast<uint16_t*>(out);
   p.bf16 = dtype == AWQ_DTYPE_BF16;
-  p.give_up = g_attention_gives_up;
+  p.give_up = g_waits_give_up;
   p.workspace = workspace;
   p.stream = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = awq::launch_attention(p, sms);
@@ -1224,7 +1224,7 @@ awq_status_t awq_attention_kv4(const void* q, int64_t B, int64_t n, int64_t Hq, 
   p.scale = scale;
   p.out = static_cast<uint16_t*>(out);
   p.bf16 = dtype == AWQ_DTYPE_BF16;
-  p.give_up = g_attention_gives_up;
+  p.give_up = g_waits_give_up;
   p.workspace = workspace;
   p.stream = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = awq::launch_attention_kv4(p, sms);
@@ -1308,7 +1308,7 @@ awq_status_t awq_moe_layer(const void* x, int64_t T, int64_t H, int64_t row_stri
                                static_cast<int>(I), static_cast<int>(E), I ? static_cast<int>(k) : 0,  // I == 0: nothing to add
                                static_cast<int>(group_size), experts, weights, stacked(up_qweight, up_qzeros, up_scales),
                                stacked(down_qweight, down_qzeros, down_scales), static_cast<const uint16_t*>(base),
-                               static_cast<uint16_t*>(out), dtype == AWQ_DTYPE_BF16, workspace,
+                               static_cast<uint16_t*>(out), dtype == AWQ_DTYPE_BF16, g_waits_give_up, workspace,
                                reinterpret_cast<cudaStream_t>(stream)};
   const cudaError_t e = awq::launch_moe_layer(p, sm_count());
   if (e != cudaSuccess) return cuda_fail(e, "awq_moe_layer launch");

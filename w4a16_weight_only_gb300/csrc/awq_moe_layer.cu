@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kW * 32, 16 / kW) moe_kernel(const __grid_cons
         const uint4 xf[2] = {next_x[0], next_x[1]};
         if (b + 1 < b1) load_x(row_x, b + 1, next_x);
         else if (unit + gridDim.x < units) load_x(row_of(unit + gridDim.x), b0, next_x);
-        if (!arrived(used)) {
+        if (p.give_up || !arrived(used)) {
           gave_up = true;
           break;
         }

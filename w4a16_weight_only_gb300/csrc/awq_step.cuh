@@ -110,6 +110,7 @@ struct MoeLayerProblem {
   const uint16_t* base;  // [T, H] or nullptr
   uint16_t* out;         // [T, H]
   bool bf16;
+  bool give_up;  // self test: the kernels' bounded waits give up at once
   void* workspace;
   cudaStream_t stream;
 };
