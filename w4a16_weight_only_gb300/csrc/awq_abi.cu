@@ -1146,7 +1146,7 @@ awq_status_t awq_rope_append_kv4(const void* q, const void* k, const void* v, co
   p.interleaved = interleaved != 0;
   p.bf16 = dtype == AWQ_DTYPE_BF16;
   p.stream = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = awq::launch_append_kv4(p);
+  const cudaError_t e = awq::launch_append_kv4(p, sm_count());
   if (e != cudaSuccess) return cuda_fail(e, "awq_rope_append_kv4 launch");
   return ok();
 }
@@ -1259,7 +1259,7 @@ awq_status_t awq_residual_norm(const void* x, int64_t x_stride, const void* resi
                                    u16(post_bias), u16(weight), u16(bias), scale, eps, T, static_cast<int>(W),
                                    kind == AWQ_NORM_LAYER, static_cast<uint16_t*>(h), static_cast<uint16_t*>(y),
                                    dtype == AWQ_DTYPE_BF16, reinterpret_cast<cudaStream_t>(stream)};
-  const cudaError_t e = awq::launch_residual_norm(p);
+  const cudaError_t e = awq::launch_residual_norm(p, sm_count());
   if (e != cudaSuccess) return cuda_fail(e, "awq_residual_norm launch");
   return ok();
 }

@@ -364,10 +364,14 @@ bool vectors_fit(const AppendKv4Problem& p) {
 }
 
 template <bool kBF, bool kInterleaved>
-cudaError_t launch_vec(const AppendKv4Problem& p) {
+cudaError_t launch_vec(const AppendKv4Problem& p, int sms) {
   const int R = kThreads / (p.D / 8);
-  // few tokens: as many blocks as give a thread one head; many: a token's query heads, its others
-  const bool few = p.T * ((p.Hq + R - 1) / R + (2 * p.Hkv + R - 1) / R) < 1216;
+  // Few tokens: as many blocks as give a thread one head; many: a block for a token's query heads, one for its others.
+  // By the former's blocks, 16 per SM (ten run at a time): 64 + 8 heads of 128, 64 tokens (640 blocks) 4.1 and 5.3 us, 160
+  // (1600) 5.3 and 5.5, 256 (2560) 6.4 and 6.1, 1024 16.5 and 12.5; 32 + 8 of 128, 256 tokens (1536) 5.2 and 5.9, 512
+  // (3072) 7.8 and 7.1; 40 + 40 of 96, 128 tokens (1536) 6.2 and 13.3, 512 (6144) 15.9 and 17.3; 16 + 1 of 256, 160
+  // tokens (800) 4.0 and 3.6.
+  const bool few = p.T * ((p.Hq + R - 1) / R + (2 * p.Hkv + R - 1) / R) < int64_t{16} * sms;
   const int q_per = few ? R : p.Hq, kv_per = few ? R : 2 * p.Hkv;
   const int q_parts = p.Hq ? (p.Hq + q_per - 1) / q_per : 0, kv_parts = (2 * p.Hkv + kv_per - 1) / kv_per;
   append_vec_kernel<kBF, kInterleaved>
@@ -415,10 +419,10 @@ bool kv4_shape_supported(int64_t D, int64_t group) {
   return (D == 64 || D == 96 || D == 128 || D == 256) && (group == 32 || group == 64 || group == 128) && D % group == 0;
 }
 
-cudaError_t launch_append_kv4(const AppendKv4Problem& p) {
+cudaError_t launch_append_kv4(const AppendKv4Problem& p, int sms) {
   if (vectors_fit(p)) {
-    if (p.bf16) return p.interleaved ? launch_vec<true, true>(p) : launch_vec<true, false>(p);
-    return p.interleaved ? launch_vec<false, true>(p) : launch_vec<false, false>(p);
+    if (p.bf16) return p.interleaved ? launch_vec<true, true>(p, sms) : launch_vec<true, false>(p, sms);
+    return p.interleaved ? launch_vec<false, true>(p, sms) : launch_vec<false, false>(p, sms);
   }
   const int64_t items = p.T * (p.Hq + 2 * p.Hkv);
   const unsigned blocks = static_cast<unsigned>((items + 7) / 8);

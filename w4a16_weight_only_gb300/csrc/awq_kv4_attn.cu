@@ -45,7 +45,6 @@ cudaError_t launch_attention_kv4(const AttentionKv4Problem& p, int sms) {
   a.group = p.Hq / p.cache.heads;
   a.row_tiles = static_cast<int>((static_cast<int64_t>(p.n) * a.group + 8 * nt - 1) / (8 * nt));
   a.tiles_per_page = p.cache.page_size / kTileKeys;
-  a.per_min = 1;
   const Layout l = layout(p, sms);
   uint8_t* ws = static_cast<uint8_t*>(p.workspace);
   a.parts = reinterpret_cast<float*>(ws);
@@ -60,7 +59,7 @@ cudaError_t launch_attention_kv4(const AttentionKv4Problem& p, int sms) {
   const int64_t units = static_cast<int64_t>(p.B) * p.cache.heads * a.row_tiles;
   const int most = most_blocks(p, nt, sms);
   a.aligned = tiles <= kAlignedTiles && units <= most;
-  const int64_t need = a.aligned ? units : units * tiles / (kWarps * a.per_min) + 1;
+  const int64_t need = a.aligned ? units : units * tiles / kWarps + 1;
   const int grid = static_cast<int>(need < most ? need : most);
   switch (p.cache.head_dim) {
     case 64: return run_64(a, nt, grid);

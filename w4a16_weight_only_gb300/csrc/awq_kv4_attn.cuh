@@ -72,7 +72,6 @@ struct Args {
   int group;      // query heads per key/value head
   int row_tiles;  // of a sequence and key/value head
   int tiles_per_page;
-  int per_min;
   bool aligned;   // a unit per block instead: no line, nothing to join between blocks
   float* parts;   // [2 blocks] of PART bytes
   float* firsts;  // [blocks][warps] of PART bytes: a warp's first run, where others follow
@@ -234,7 +233,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
     T = coarse[kCoarse - 1];
     total = T * (static_cast<int64_t>(cache.heads) * a.row_tiles);
     const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps;
-    per = max(static_cast<int64_t>(a.per_min), (total + warps - 1) / warps);
+    per = max(int64_t{1}, (total + warps - 1) / warps);
     if (blockIdx.x == 0 && threadIdx.x == 0) a.line[0] = per;
     X0 = static_cast<int64_t>(blockIdx.x) * kWarps * per;
   }

@@ -204,11 +204,13 @@ cudaError_t launch_vec(const ResidualNormProblem& p) {
 }
 
 template <bool kBF>
-cudaError_t launch(const ResidualNormProblem& p) {
+cudaError_t launch(const ResidualNormProblem& p, int sms) {
   if (vectors_fit(p)) {
-    // one vector a thread where there are few rows (latency: 4 rows of 8192 1 us), two where there are many, so that
-    // more rows are on an SM at a time
-    const int vectors = p.W / 8, v = vectors <= 1024 && p.T <= 304 ? 1 : vectors <= 2048 ? 2 : 4;
+    // One vector a thread where there are few rows (at most two blocks an SM), two where there are many.  Launches back to
+    // back, norms on either side, a gate per row: 1 row of 8192 3.7 us with one and 4.2 with two, 304 of 2048 3.1 and 3.9,
+    // 304 of 8192 5.6 and 5.3; 608 of 4096 5.4 and 5.3, 1024 of 8192 18.3 and 19.4, 8192 of 4096 57.6 and 58.4, of 8192
+    // 119.3 and 116.7.
+    const int vectors = p.W / 8, v = vectors <= 1024 && p.T <= 2 * sms ? 1 : vectors <= 2048 ? 2 : 4;
     switch (v) {
       case 1: return launch_vec<kBF, 1>(p);
       case 2: return launch_vec<kBF, 2>(p);
@@ -222,6 +224,6 @@ cudaError_t launch(const ResidualNormProblem& p) {
 
 }  // namespace
 
-cudaError_t launch_residual_norm(const ResidualNormProblem& p) { return p.bf16 ? launch<true>(p) : launch<false>(p); }
+cudaError_t launch_residual_norm(const ResidualNormProblem& p, int sms) { return p.bf16 ? launch<true>(p, sms) : launch<false>(p, sms); }
 
 }  // namespace awq

@@ -118,11 +118,11 @@ struct MoeLayerProblem {
 constexpr int kMoeLayerMaxT = 16;
 
 bool kv4_shape_supported(int64_t D, int64_t group);
-cudaError_t launch_append_kv4(const AppendKv4Problem& p);
+cudaError_t launch_append_kv4(const AppendKv4Problem& p, int sms);
 cudaError_t launch_read_kv4(const ReadKv4Problem& p);
 size_t attention_kv4_workspace_bytes(const AttentionKv4Problem& p, int sms);
 cudaError_t launch_attention_kv4(const AttentionKv4Problem& p, int sms);
-cudaError_t launch_residual_norm(const ResidualNormProblem& p);
+cudaError_t launch_residual_norm(const ResidualNormProblem& p, int sms);
 size_t moe_layer_workspace_bytes(int T, int k, int H, int I);
 cudaError_t launch_moe_layer(const MoeLayerProblem& p, int sms);
 
