@@ -694,8 +694,8 @@ awq_status_t awq_kv4_read(const awq_kv4_cache_t* cache, const int32_t* slots, in
  *   tokens counted (one above W * page_size is cut to it).  Pages that a window leaves out may be any
  *   number: they are not read.
  * k_j and v_j are what the codes stand for, unrounded; logits, statistics and sums are fp32.  The factor of a
- * value, probability times scale, is rounded to fp16's 11 bits (fp16 elements: 22), in steps of at least 2^-31
- * of the largest factor of the same query row and group of elements, and an element of a bf16 query in steps
+ * value's code, counted from 8, is probability times scale, rounded to fp16's 11 bits (fp16 elements: 22), in
+ * steps of at least 2^-31 of the largest factor of the same query row and group of elements, and an element of a bf16 query in steps
  * of at least 2^-28 of the row's largest.  A sequence's keys are cut into parts by all sequences' lengths, so
  * other lengths may change its result's last bits.  Keys and values above 2^100 in size (bf16) may overflow.
  * A row uses only the keys that it sees: what the cache holds elsewhere

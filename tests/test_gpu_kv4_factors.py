@@ -2,7 +2,8 @@
 times scale, is held in fp16 relative to the largest of its own query row and group of elements, so neither keys
 that the row does not see, nor seen ones of no weight, nor other groups take bits from it.
 
-Tolerance, per element of a group, y = sum_j p_j (c_j s_j + m_j) over N keys, S = sum_j p_j c_j s_j, M = sum_j p_j |m_j|:
+Tolerance, per element of a group, y = sum_j p_j s_j (c_j - 8) + p_j (m_j + 8 s_j) over N keys, S = sum_j p_j s_j |c_j - 8|,
+M = sum_j p_j |m_j + 8 s_j|:
   the result's rounding u |y| (u = 2^-11 fp16, 2^-8 bf16; below fp16's normal range half of 2^-24);
   the factor's: 2^-11 S (bf16, one fp16 term), 2^-22 S (fp16, two terms), and below fp16's normal range 2^-25 of a
   factor where the largest p s of the row and group is 2^7 or more: N * 15 * 2^-32 * max_j p_j s_j;
@@ -69,6 +70,7 @@ def plain(q, k, v, group, dtype, scale=None, window=0, sinks=0):
         s, m = np.repeat(s, group, -1), np.repeat(m, group, -1)
         parts.append((code * s, m, s))
     (kc, km, _), (vc, vm, vs) = parts
+    eight = 8 * vs
     out, tol = np.zeros(q.shape), np.zeros(q.shape)
     for i in range(n):
         at = tokens - n + i
@@ -80,14 +82,14 @@ def plain(q, k, v, group, dtype, scale=None, window=0, sinks=0):
             Z = abs(scale) * ((kc + np.abs(km))[seen, hk] @ np.abs(row))
             p = np.exp(z - z.max())
             p /= p.sum()
-            y, S, M = (p @ a[seen, hk] for a in (vc + vm, vc, np.abs(vm)))
+            y, S, M = (p @ a[seen, hk] for a in (vc + vm, np.abs(vc - eight), np.abs(vm + eight)))
             moved = 2.0 ** -23 * ((D + 16) * Z + 2 * np.abs(z) + 2 * np.abs(z).max())
             if dtype == "bf16":
                 moved += 2.0 ** -29 * np.abs(row).max() * abs(scale) * kc[seen, hk].sum(-1)
             moved *= p
             out[i, h] = y
             tol[i, h] = U[dtype] * np.abs(y) + (2.0 ** -11 if dtype == "bf16" else 2.0 ** -22) * S \
-                + moved @ (vc + np.abs(vm))[seen, hk] + (moved.sum() + 2.0 ** -22 * (N / 16 + 64)) * (S + M) \
+                + moved @ (np.abs(vc - eight) + np.abs(vm + eight))[seen, hk] + (moved.sum() + 2.0 ** -22 * (N / 16 + 64)) * (S + M) \
                 + N * 15 * 2.0 ** -32 * (p[:, None] * vs[seen, hk]).max(0) + (2.0 ** -25 if dtype == "fp16" else 0)
     return out, tol
 

@@ -43,7 +43,7 @@ def quantized(x, group):
     return code.double().mul(scale.double()).flatten(-2), wide(low), wide(scale)
 
 
-def make(awq, B, n, hq, hkv, D, group, lens, page, dtype, seed):
+def make(awq, B, n, hq, hkv, D, group, lens, page, dtype, seed, signs=True):
     g = torch.Generator(device="cuda").manual_seed(seed)
     per = -(-max(lens) // page)
     total = B * per + 1
@@ -52,8 +52,11 @@ def make(awq, B, n, hq, hkv, D, group, lens, page, dtype, seed):
     keys, values = [], []
     for b in range(B):
         k = torch.randn((lens[b], hkv, D), generator=g, device="cuda").to(DT[dtype])
-        v = torch.randint(0, 2, (lens[b], hkv, D), generator=g, device="cuda", dtype=torch.int64).mul(2).sub(1).to(DT[dtype])
-        v[..., ::group], v[..., 1::group] = 1, -1  # a group's extremes, whatever the others are
+        if signs:
+            v = torch.randint(0, 2, (lens[b], hkv, D), generator=g, device="cuda", dtype=torch.int64).mul(2).sub(1).to(DT[dtype])
+            v[..., ::group], v[..., 1::group] = 1, -1  # a group's extremes, whatever the others are
+        else:
+            v = torch.randn((lens[b], hkv, D), generator=g, device="cuda").to(DT[dtype])
         at = torch.arange(lens[b], device="cuda")
         if lens[b]:
             awq.awq_rope_append_kv4(None, k, v, None, None, cache, (pages[b, at // page] * page + at % page).int(), group_size=group)
@@ -128,7 +131,7 @@ def test_long(awq, case, dtype):
             N = at + 1 - first + few
             want = (total[at + 1] - total[first] + total[few]) / N  # [hkv, D]
             got = out[b, i].double().view(hkv, -1, D)
-            # S + M is 2 at most: (15 s + 1) of a value, rounded s
+            # sums of s |c - 8| and |m + 8 s|, 16 s / 2 and 1 at most for values of +1 and -1
             tol = U[dtype] * want.abs() + 2.0 ** -22 * 116 * 2.01
             assert ((got - want[:, None]).abs() <= tol[:, None]).all(), (b, i, ((got - want[:, None]).abs() / tol[:, None]).max())
             if N >= 64:
@@ -147,12 +150,37 @@ def test_long(awq, case, dtype):
                 moved = moved + 2.0 ** -29 / D ** 0.5 * q.abs().amax(-1, keepdim=True) * kc[keep].sum(-1).t()[:, None]
             moved = moved * p
             mean = lambda w, x: torch.einsum("hgj,jhd->hgd", w, x[keep])  # noqa: E731
-            y, S, M = mean(p, v), mean(p, cs), mean(p, low.abs())
+            y, S, M = mean(p, v), mean(p, (cs - 8 * scale).abs()), mean(p, (low + 8 * scale).abs())
             heaviest = torch.stack([(p[h, :, :, None] * scale[keep, h][None]).amax(1) for h in range(hkv)])  # [hkv, rows, D]
-            tol = U[dtype] * y.abs() + (2.0 ** -11 if dtype == "bf16" else 2.0 ** -22) * S + mean(moved, cs + low.abs()) \
+            tol = U[dtype] * y.abs() + (2.0 ** -11 if dtype == "bf16" else 2.0 ** -22) * S + mean(moved, (cs - 8 * scale).abs() + (low + 8 * scale).abs()) \
                 + (moved.sum(-1, keepdim=True) + 2.0 ** -22 * (N / 16 + 64)) * (S + M) + N * 15 * 2.0 ** -32 * heaviest + 2.0 ** -25
             err = (usual[b, i].double().view(hkv, -1, D) - y).abs()
             assert (err <= tol).all(), (b, i, (err / tol).max())
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("B,hq,hkv,D,group,longest", [(4, 64, 8, 128, 64, 60000), (7, 64, 8, 128, 128, 24000), (1, 40, 8, 64, 32, 100000),
+                                                      (2, 24, 2, 96, 32, 40000), (8, 40, 8, 256, 64, 12000)])
+def test_sums_do_not_drift(awq, B, hq, hkv, D, group, longest, dtype):
+    # A result over many keys is a small mean of values of either sign.  Tensor cores cut a sum's last bits off where they add
+    # to it: a sum that grows along a warp's keys leaves all results off to one side.  The mean of the errors is free of the
+    # results' own rounding (five times its spread over the mean's root is left for it).  Sums of both signs lose on both
+    # sides: 2^-19, half a step of 2^-21 of eight terms of the values' size, 1, is left for what they keep to one side, and
+    # 2^-20 for exponentials and fp32 sums, which round to nearest.
+    lens = [longest - 1001 * i for i in range(B)]
+    call, keys, values = make(awq, B, 1, hq, hkv, D, group, lens, 16, dtype, seed=D, signs=False)
+    out = awq.awq_attention_kv4(**call)
+    errors, sizes = [], []
+    for b in range(B):
+        (kc, km, _), (cs, low, _) = quantized(keys[b], group), quantized(values[b], group)
+        q = call["q"][b, 0].double().view(hkv, -1, D)
+        p = torch.softmax(torch.einsum("hgd,jhd->hgj", q, kc + km) / D ** 0.5, dim=-1)
+        want = torch.einsum("hgj,jhd->hgd", p, cs + low)
+        errors.append((out[b, 0].double().view(hkv, -1, D) - want).flatten())
+        sizes.append(want.flatten())
+    error, size = torch.cat(errors), torch.cat(sizes)
+    spread = U[dtype] * size.square().mean().sqrt()
+    assert abs(error.mean()) <= 2.0 ** -19 + 2.0 ** -20 + 5 * spread / len(error) ** 0.5, error.mean()
 
 
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])

@@ -5,13 +5,14 @@
 //
 // with k_j = s c + m per group of elements (codes c, scale s, minimum m), and v_j alike, so that
 //
-//   q . k_j = sum_g s_g (q_g . c_g) + m_g sum(q_g),    sum_j p_j v_j = sum_j (p_j s_j) c_j + sum_j p_j m_j
+//   q . k_j = sum_g s_g (q_g . c_g) + m_g sum(q_g),    sum_j p_j v_j = sum_j (p_j s_j) (c_j - 8) + sum_j p_j (m_j + 8 s_j)
 //
 // and the codes themselves go to the tensor cores.  Bound by instructions, some 380 for a tile of 16 keys of a head
 // of 128 (two thirds of them the codes' extraction, the softmax and the parameters; 2.2 a cycle and SM at 16 warps):
 // 128 sequences of up to 8197, 8 heads, 765 MB in 172 us, 4.4 TB/s.  A word of codes ANDed with 0x000f000f is a pair of fp16
-// subnormals c 2^-24, with 0x00f000f0 a pair c 2^-20: an operand register costs one logic operation, and
-// every second one a shift.  The two kinds have accumulators of their own, scaled back at the end.
+// subnormals c 2^-24, with 0x00f000f0 a pair c 2^-20: an operand register of keys costs one logic operation, and
+// every second one a shift; of values, ORed with 1024 and less 1032 (1024 + 128), one addition more.  The two kinds have
+// accumulators of their own, scaled back at the end.
 // Queries are fp16 for either element type (a bf16 row is scaled by a power of two first: exact down to 2^-18 of its
 // largest element, in steps of 2^-28 below), p s is one fp16 number (fp16 elements: two) in a unit of its row and group.
 #pragma once
@@ -171,6 +172,20 @@ __device__ __forceinline__ float log2_approx(float x) {
 // 2^x for whole x up to 127, 0 where that is below the normal numbers.
 __device__ __forceinline__ float whole_exp2(float x) {
   return x < -126.f ? 0.f : __uint_as_float(static_cast<uint32_t>(static_cast<int>(x) + 127) << 23);
+}
+
+// Codes of values count from 8.  Tensor cores cut off the last bits of a sum that they add to; a sum of codes that
+// count from 0 grows with the keys, while results are small differences of it and of the minima's sum: 4 over 131072,
+// fp16, had errors of 3.5 times the result's own rounding, all to one side (now: of its size; 115 -> 122 us, 128 over
+// 8197 172 -> 179).  Sums started anew every four tiles, or every tile, had 2.2 and 2.1 times; a product with -8 ahead of
+// the codes' instead of the subtraction 187 us for 128 over 8197, fp16 16 % more.
+constexpr float kMiddle = 8.f;
+
+__device__ __forceinline__ uint32_t from_middle(uint32_t words, bool high) {  // (c - 8) of the low nibbles, 16 (c - 8) of the high
+  const uint32_t raw = ptx::and_or(words, high ? 0x00f000f0u : 0x000f000fu, 0x64006400u);
+  const uint32_t middle = high ? 0xe480e480u : 0xe408e408u;  // -1152, -1032
+  const __half2 h = __hadd2(*reinterpret_cast<const __half2*>(&raw), *reinterpret_cast<const __half2*>(&middle));
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // Weight of a partial result (max m, sum l) against the maximum `top` of all.
@@ -442,7 +457,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
           pos[m][h] = len - p.n + min((row0 + 8 * m + 2 * t + h) / a.group, p.n - 1);
         }
       }
-      float o[NT][U][2][4], top[NT][2], sum[NT][2], low[NT][G][2];  // low: sums of p times the values' minima
+      float o[NT][U][2][4], top[NT][2], sum[NT][2], low[NT][G][2];  // low: sums of p times the values' code 8
       uint32_t units[NT][2][(G + 1) / 2];
       float least_unit[NT][2];  // of its groups, as e
 #pragma unroll
@@ -667,7 +682,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
             for (int m = 0; m < NT; ++m)
 #pragma unroll
               for (int half = 0; half < 2; ++half) {
-                const float s = v[half][q].x, mn = v[half][q].y;
+                const float s = v[half][q].x, mn = v[half][q].y + kMiddle * s;
                 float ps[2];
                 mul2(ps, z[m][half][0], z[m][half][1], per_unit<G>(units[m][0], q), per_unit<G>(units[m][1], q));
                 mul2(ps, ps[0], ps[1], s, s);
@@ -694,8 +709,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
               const uint32_t x0w = vw[u][0], x1w = vw[u][1], y0w = x0w >> 8, y1w = x1w >> 8;
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
-                const uint32_t mask = c ? 0x00f000f0u : 0x000f000fu;
-                const uint32_t a0 = x0w & mask, a1 = y0w & mask, a2 = x1w & mask, a3 = y1w & mask;
+                const uint32_t a0 = from_middle(x0w, c), a1 = from_middle(y0w, c), a2 = from_middle(x1w, c), a3 = from_middle(y1w, c);
 #pragma unroll
                 for (int m = 0; m < NT; ++m)
 #pragma unroll
@@ -750,7 +764,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::BLOCKS) attentio
           uint16_t* out = p.out + ((static_cast<int64_t>(cur.b) * p.n + i) * p.Hq + hk * a.group + (r - i * a.group)) * D;
 #pragma unroll
           for (int u = 0; u < U; ++u) {
-            const float lo = inv * kTwo24, hi = inv * kTwo20, mn = lows[u / PER_GROUP] * inv;
+            const float lo = inv, hi = inv * 0.0625f, mn = lows[u / PER_GROUP] * inv;
             const float unit = __uint_as_float(static_cast<uint32_t>(127 + unit_log<G>(units[m][h], u / PER_GROUP)) << 23);
             const float e[4] = {o[m][u][0][h] * lo * unit + mn, o[m][u][1][h] * hi * unit + mn, o[m][u][0][2 + h] * lo * unit + mn,
                                 o[m][u][1][2 + h] * hi * unit + mn};
