@@ -749,8 +749,8 @@ awq_status_t awq_residual_norm(const void* x, int64_t x_stride, const void* resi
  *   columns, then up columns; down_qweight [E, I, H / 8], down_qzeros [E, I / G, H / 8], down_scales [E, I /
  *   G, H]: stacked linears as awq_gemm_grouped takes them, G = group_size
  * A place whose id lies outside [0, E) (-1) is left out, whatever its weight.  Sums are fp32, of a token's
- * places in their order; act is rounded to the element type as the factor of the second product, the
- * result once more.  A token with an element that is not finite gives NaN.  Repeated calls give the same
+ * places in their order; act is the sum of two elements (22 bits of fp16, 16 of bf16; infinite beyond the type's
+ * range) as the factor of the second product, and the result is rounded once.  A token with an element that is not finite gives NaN.  Repeated calls give the same
  * bits.
  *   workspace: awq_moe_layer_workspace_size bytes, 256-byte aligned; any content.  Calls that overlap in
  *   time need workspaces of their own.

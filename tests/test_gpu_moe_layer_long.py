@@ -2,8 +2,9 @@
 loads that run on into the next unit, tiles of columns added up by the block that is last with several, half tiles at
 the end of H, groups across blocks of K.
 
-Tolerance as in test_gpu_moe_layer: the result's rounding, the rounding u of the inner activations carried through
-the second product, and fp32 sums (relative error 2^-23 per step of a group, of the groups and of the parts) of
+Tolerance as in test_gpu_moe_layer, but for the inner activations, which are two elements' sums: the result's
+rounding; u^2 of an activation, fp16 2^-25 where its second element is below the normal range, carried through
+the second product; and fp32 sums (relative error 2^-23 per step of a group, of the groups and of the parts) of
 products whose codes may carry an offset of 128 (bf16).  With weights of either sign that bound comes near the result
 for many rows of K, so each case runs a second time without cancellation: positive inputs, zeros of 0, and codes
 that are one for 64 rows of a column, so that a block of rows that is lost, taken twice or taken for another moves
@@ -93,8 +94,8 @@ def check(out, d, dtype, share=None):
         (g, v), (dg, dv) = both.chunk(2, -1), near.chunk(2, -1)
         silu = g * torch.sigmoid(g)
         act = silu * v
-        dact = 1.1 * v.abs() * dg + silu.abs() * dv + 1.1 * dg * dv + 2.0 ** -20 * act.abs()
-        y, dy = times(act, dact, d["down"], e, d["group_size"], offset, u)
+        dact = 1.1 * v.abs() * dg + silu.abs() * dv + 1.1 * dg * dv + 2.0 ** -20 * act.abs() + (2.0 ** -25 if dtype == "fp16" else 0)
+        y, dy = times(act, dact, d["down"], e, d["group_size"], offset, u * u)
         w = d["weights"][token, place].double()[:, None]
         want = want.index_add(0, token, w * y)
         bound = bound.index_add(0, token, w.abs() * (dy + 2.0 ** -21 * y.abs()))
@@ -102,6 +103,7 @@ def check(out, d, dtype, share=None):
     tol = u * want.abs() + bound * (1 + u) + (2.0 ** -24 if dtype == "fp16" else 0)
     err = (out.double() - want).abs()
     assert (err <= tol).all(), (err / tol).max()
+    return want
     if share:
         assert (tol < share * want).all()
 
@@ -134,6 +136,18 @@ def test_layer(awq, case, dtype):
     K = max(CASES[case][3:5])
     # bf16 rounds to 2^-8 twice: for the longest K four blocks' share
     check(awq.awq_moe_layer(**d), d, dtype, share=64 / K if dtype == "fp16" or K <= 4096 else 256 / K)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("case", [0, 1, 5, 8])
+def test_errors_are_the_results_rounding(awq, case, dtype):
+    # Nothing else is rounded to the element type: fp32 errors and u^2 of the activations are below a hundredth of u, and
+    # an activation of one element alone would add as much as the result's rounding, a root mean square of 1.41 times it.
+    d = inputs(*CASES[case], dtype, seed=60 + case, base=False)
+    out = awq.awq_moe_layer(**d)
+    want = check(out, d, dtype)
+    rms = lambda x: x.square().mean().sqrt()  # noqa: E731
+    assert rms(out.double() - want) <= 1.1 * rms(want.to(DT[dtype]).double() - want)
 
 
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])

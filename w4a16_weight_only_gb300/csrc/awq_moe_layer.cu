@@ -1,9 +1,10 @@
 // A mixture-of-experts layer of a few tokens on 4-bit experts, in two kernels (awq_moe_layer):
 //
-//   act[t, j] = silu(x[t] Wg) * (x[t] Wu)          of expert experts[t, j], rounded to the element type
+//   act[t, j] = silu(x[t] Wg) * (x[t] Wu)          of expert experts[t, j], as the sum of two elements
 //   out[t]    = base[t] + sum_j weights[t, j] * (act[t, j] Wd)
 //
-// with  w = (code - zero) * scale  per group of G rows, sums in fp32, the result rounded once.
+// with  w = (code - zero) * scale  per group of G rows, sums in fp32, the result rounded once.  As one element act
+// would double the variance of the result's own rounding.
 #include "awq_step.cuh"
 #include "awq_ptx.cuh"
 
@@ -11,7 +12,11 @@ namespace awq {
 namespace {
 
 constexpr int kMaxPlaces = kMoeLayerMaxT * 32;
-constexpr int kRows = 8;      // places of a job: the columns of an m16n8k16
+// Columns of an m16n8k16: eight places of a job, in the second product four with their act's two elements.  An expert
+// of more than four places is several jobs there: 16 tokens, 2 of 8, 4096 x 14336, fp16 252 us (211 with one element;
+// 231 with eight places a job and products of their own for the second elements, which cost the others 2 to 5 %: 16
+// tokens, 8 of 128, 236 and 242, one element 231; 3 tokens, 2 of 8, 131 and 136, 131).
+constexpr int kRows = 8;
 constexpr int kBlockK = 64;   // rows of a weight that a warp has in flight
 
 struct Layout {
@@ -21,7 +26,7 @@ struct Layout {
 __host__ Layout layout(int T, int k, int H, int I) {
   Layout l;
   const auto up = [](size_t n) { return (n + 255) / 256 * 256; };
-  l.y = up(static_cast<size_t>(T) * k * I * 4);  // the kernels for any shape keep act in fp32
+  l.y = up(static_cast<size_t>(T) * k * I * 4);  // act: two elements, or fp32 in the kernels for any shape
   l.counters = l.y + up(static_cast<size_t>(T) * k * H * 4);
   l.bytes = l.counters + up(static_cast<size_t>((H + 127) / 128) * 4);
   return l;
@@ -62,7 +67,7 @@ __global__ void __launch_bounds__(128) moe_up_any_kernel(const MoeLayerProblem p
   dot8<kBF>(p.up, e, p.H, 2 * p.I, p.G, c, at, gate);
   dot8<kBF>(p.up, e, p.H, 2 * p.I, p.G, p.I / 8 + c, at, up);
   for (int j = 0; j < 8; ++j)
-    act[static_cast<int64_t>(place) * p.I + 8 * c + j] = elem_to_float<kBF>(float_to_elem<kBF>(gate[j] / (1.f + expf(-gate[j])) * up[j]));
+    act[static_cast<int64_t>(place) * p.I + 8 * c + j] = gate[j] / (1.f + expf(-gate[j])) * up[j];
 }
 
 // One thread per (token, eight columns).
@@ -86,7 +91,7 @@ __global__ void __launch_bounds__(128) moe_down_any_kernel(const MoeLayerProblem
 
 // ---- tensor-core kernels ----
 
-// The places, eight of one expert at a time, in shared memory for T k of them.
+// The places, kPart of one expert at a time, in shared memory for T k of them.
 struct Jobs {
   int* expert;
   int* rows;
@@ -99,9 +104,9 @@ struct Jobs {
   __host__ __device__ static constexpr int bytes(int places) { return places * (3 * 4 + kRows * 2); }
 };
 
-// Built by every block alike from the experts' ids: place p is row (rank % 8) of its expert's job rank / 8,
+// Built by every block alike from the experts' ids: place p is row (rank % kPart) of its expert's job rank / kPart,
 // jobs in the order of their first places.
-template <int kThreads>
+template <int kThreads, int kPart>
 __device__ __forceinline__ void build_jobs(const MoeLayerProblem& p, Jobs& jobs, int* head_job, int* count) {
   const int places = p.T * p.k;
   int* ids = jobs.ids;
@@ -126,10 +131,10 @@ __device__ __forceinline__ void build_jobs(const MoeLayerProblem& p, Jobs& jobs,
     int rank = 0, head = i;
     for (int q = 0; q < i; ++q)
       if (ids[q] == e) {
-        if ((rank & (kRows - 1)) == 0) head = q;
+        if ((rank & (kPart - 1)) == 0) head = q;
         ++rank;
       }
-    row[n] = rank & (kRows - 1);
+    row[n] = rank & (kPart - 1);
     head_job[i] = row[n] == 0 ? i : head;
   }
   __syncthreads();
@@ -226,6 +231,7 @@ __global__ void __launch_bounds__(kW * 32, 16 / kW) moe_kernel(const __grid_cons
   float* y = args.y;
   int* counters = args.counters;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  constexpr int kPart = kUp ? kRows : kRows / 2;  // places of a job
   const int K = kUp ? p.H : p.I, N = kUp ? 2 * p.I : p.H, words = N / 8;
   const Stacked& w = kUp ? p.up : p.down;
   ptx::launch_dependents();
@@ -236,7 +242,7 @@ __global__ void __launch_bounds__(kW * 32, 16 / kW) moe_kernel(const __grid_cons
     for (int s = 0; s < STAGES; ++s) ptx::mbar_init(&full[s], 1);
     ptx::fence_mbar_init();
   }
-  build_jobs<kW * 32>(p, jobs, reinterpret_cast<int*>(smem), &job_count);
+  build_jobs<kW * 32, kPart>(p, jobs, reinterpret_cast<int*>(smem), &job_count);
   if (kUp && blockIdx.x == 0)
     for (int i = threadIdx.x; i < (p.H + 127) / 128; i += kW * 32) counters[i] = 0;
   const int tiles = kUp ? p.I / 64 : (p.H + 127) / 128, units = jobs.count * tiles;
@@ -275,10 +281,10 @@ __global__ void __launch_bounds__(kW * 32, 16 / kW) moe_kernel(const __grid_cons
 
   // x of block b of a unit: eight elements of the lane's place per 32 rows
   const auto row_of = [&](int unit) -> const uint16_t* {
-    const int job = unit / tiles;
-    if (g >= jobs.rows[job]) return nullptr;
-    const int place = jobs.place[job][g];
-    return (kUp ? p.x + static_cast<int64_t>(place / p.k) * p.x_st : act + static_cast<int64_t>(place) * p.I) + 8 * t;
+    const int job = unit / tiles, r = g & (kPart - 1);
+    if (r >= jobs.rows[job]) return nullptr;
+    const int place = jobs.place[job][r];
+    return (kUp ? p.x + static_cast<int64_t>(place / p.k) * p.x_st : act + (static_cast<int64_t>(g / kPart) * (p.T * p.k) + place) * p.I) + 8 * t;
   };
   const auto load_x = [&](const uint16_t* row, int b, uint4 (&v)[2]) {
 #pragma unroll
@@ -431,13 +437,20 @@ __global__ void __launch_bounds__(kW * 32, 16 / kW) moe_kernel(const __grid_cons
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
           const int r = 2 * t + (n & 1), column = 64 * tile + 8 * g + col + 4 * (n >> 1);
-          if (r < jobs.rows[job]) act[static_cast<int64_t>(jobs.place[job][r]) * p.I + column] = float_to_elem<kBF>(silu(first[n]) * second[n]);
+          if (r >= jobs.rows[job]) continue;
+          const float v = silu(first[n]) * second[n];
+          const uint16_t whole = float_to_elem<kBF>(v);
+          const float rest = v - elem_to_float<kBF>(whole);
+          const int64_t at = static_cast<int64_t>(jobs.place[job][r]) * p.I + column;
+          act[at] = whole;
+          act[at + static_cast<int64_t>(p.T * p.k) * p.I] = float_to_elem<kBF>(fabsf(rest) <= fabsf(v) ? rest : 0.f);  // none of infinities, NaN
         }
       } else {
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
+          const float y_rc = first[n] + __shfl_xor_sync(0xffffffffu, first[n], 2);  // the places' rests are four columns further
           const int r = 2 * t + (n & 1), column = 128 * tile + 64 * (warp >> 2) + 8 * g + col + 4 * (n >> 1);
-          if (r < jobs.rows[job] && column < p.H) y[static_cast<int64_t>(jobs.place[job][r]) * p.H + column] = first[n];
+          if (r < jobs.rows[job] && column < p.H) y[static_cast<int64_t>(jobs.place[job][r]) * p.H + column] = y_rc;
         }
       }
     }
