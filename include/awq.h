@@ -783,7 +783,7 @@ awq_status_t awq_selftest_wait_timeout(uint64_t limit_ns, awq_stream_t stream);
  * normal).  Such a call's output is unspecified, it touches nothing outside its tensors, and a following
  * awq_device_status returns AWQ_ERR_TIMEOUT; calls whose copies have no wait that can run out
  * (awq_attention_shared: page_size % 16 != 0, fewer than 3 steps of a block; awq_moe_layer: H or I no multiple of
- * 64) are unaffected.  Host only. */
+ * 64, group_size neither 32 nor one) are unaffected.  Host only. */
 awq_status_t awq_selftest_attention_give_up(int on);
 
 #ifdef __cplusplus

@@ -7,7 +7,11 @@ namespace {
 
 using namespace kv4;
 
-int row_tile(const AttentionKv4Problem& p) {  // query rows of a unit, in eights
+// Query rows of a unit, in eights.  Heads of 128, groups of 128, bf16, 32 sequences over up to 4096, by eight and by
+// sixteen rows: 9 rows of a head 37 and 36 us, 16 37 and 36, 24 48 and 51, 32 58 and 52, 48 77 and 67; 4 over 2048, any of
+// these, 19 and 23.  Heads of 64: 16 rows 30 and 31, 24 37 and 44, 32 44 and 44, 48 57 and 57.  (Three tiles of eight would
+// serve 17 to 24 rows better.)  Heads of 256 have no registers for sixteen.
+int row_tile(const AttentionKv4Problem& p) {
   const int64_t rows = static_cast<int64_t>(p.n) * (p.Hq / p.cache.heads);
   return rows > 8 && p.cache.head_dim <= 128 ? 2 : 1;
 }
@@ -16,7 +20,9 @@ size_t part_bytes(const AttentionKv4Problem& p, int nt) { return static_cast<siz
 
 int most_blocks(const AttentionKv4Problem& p, int nt, int sms) { return sms * blocks_per_sm(p.cache.head_dim, nt); }
 
-// A unit per block up to this many tiles (eight warps, 16 tiles each), where all units run at once.
+// A unit per block up to this many tiles (eight warps, 16 tiles each), where all units run at once.  Heads of 128, a unit
+// per block and by the line: 8 units of 256 keys 9 and 13 us, of 1024 13 and 14, of 2048 19 and 16; 96 units of 700 12 and
+// 19, of 2048 19 and 21; 296 units of 700 15 and 22, of 2048 26 and 31.
 constexpr int kAlignedTiles = 128;
 
 struct Layout {

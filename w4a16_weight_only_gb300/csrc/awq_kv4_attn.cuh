@@ -7,9 +7,11 @@
 //
 //   q . k_j = sum_g s_g (q_g . c_g) + m_g sum(q_g),    sum_j p_j v_j = sum_j (p_j s_j) (c_j - 8) + sum_j p_j (m_j + 8 s_j)
 //
-// and the codes themselves go to the tensor cores.  Bound by instructions, some 380 for a tile of 16 keys of a head
-// of 128 (two thirds of them the codes' extraction, the softmax and the parameters; 2.2 a cycle and SM at 16 warps):
-// 128 sequences of up to 8197, 8 heads, 765 MB in 172 us, 4.4 TB/s.  A word of codes ANDed with 0x000f000f is a pair of fp16
+// and the codes themselves go to the tensor cores.  Some 400 instructions for a tile of 16 keys of a head of 128, most of
+// them the codes' extraction, the softmax and the parameters.  No unit is full: 16 warps an SM, whose 128 registers spill
+// 32 to 180 bytes, issue in 56 % of the schedulers' cycles, HBM is at 43 %, the tensor pipe at 18 % (counters of 32
+// sequences); a warp waits for its own chain of words, first product, vote, exponentials and second product.  128
+// sequences of up to 8197, 8 heads, 765 MB in 179 us, 4.3 TB/s.  A word of codes ANDed with 0x000f000f is a pair of fp16
 // subnormals c 2^-24, with 0x00f000f0 a pair c 2^-20: an operand register of keys costs one logic operation, and
 // every second one a shift; of values, ORed with 1024 and less 1032 (1024 + 128), one addition more.  The two kinds have
 // accumulators of their own, scaled back at the end.
@@ -143,11 +145,11 @@ constexpr float kTwo24 = 16777216.f, kTwo20 = 1048576.f;
 // factor of a key's codes, p times its scale, as an fp16 number in units of 2^e, e a whole number for each query row
 // and group of elements, raised only when a factor reaches 2^kFactorEnd, to where the largest is in 2^kFactorLog ..
 // 2^(kFactorLog + 1).  Both change for those rows and groups alone whose own keys ask for it: neither a key that a row
-// does not see nor one of no weight takes bits from the others.  64 over 8197, 64 / 8 heads of 128, groups of 32: 134 us,
-// 143 us where one group's values are 2^-6 of another's or less (194 us if the bound alone decided, 139 us if each tile
-// were looked at group by group); with one unit for all rows and groups 126 us, with other groups as now.  fp16 numbers have their 11 bits down to 2^-14 and steps of 2^-24 below: 2^-21 and 2^-31 of a row's
-// largest.  Units go from 2^-110 (values that small are near bf16's smallest number) to 2^126; 2^-e is kept as bf16,
-// two groups to a word.
+// does not see nor one of no weight takes bits from the others.  64 over 8197, 64 / 8 heads of 128, groups of 32: 141 us,
+// 149 us where one group's values are 2^-6 of another's or less (some 60 more if the bound alone decided, 5 more for all if
+// each tile were looked at group by group); with one unit for all rows and groups 8 us less, and larger groups as now.
+// fp16 numbers have their 11 bits down to 2^-14 and steps of 2^-24 below: 2^-21 and 2^-31 of a row's largest.  Units go
+// from 2^-110 (values that small are near bf16's smallest number) to 2^126; 2^-e is kept as bf16, two groups to a word.
 constexpr float kNoTop = -3.402823466e38f;
 constexpr int kFactorLog = 7, kFactorEnd = 15;
 constexpr float kLastFactor = kFactorEnd - 0.01f;  // its base-2 logarithm, by approximate ones

@@ -54,7 +54,8 @@ __device__ __forceinline__ void dot8(const Stacked& w, int64_t e, int K, int N, 
   }
 }
 
-// One thread per (place, eight columns).
+// One thread per (place, eight columns).  Slow: 2 of 8 experts of 2040 x 1400, groups of 8, 1.2 ms for 1 to 16 tokens (of
+// 2048 x 1408, groups of 64, by the tensor-core kernels 20 to 34 us).
 template <bool kBF>
 __global__ void __launch_bounds__(128) moe_up_any_kernel(const MoeLayerProblem p, float* act) {
   const int c = blockIdx.x * 128 + threadIdx.x, place = blockIdx.y;
@@ -216,8 +217,10 @@ __device__ __forceinline__ void box_load(void* dst, const CUtensorMap* map, uint
 // bf16: with the exponent ORed in it is 128 + c.  The zero (and 128) leaves with the sum of x, which an
 // mma against ones gives in the same layout; a group's sums are scaled into fp32 totals.
 // Each warp has a ring of stages of its own, filled by TMA across units: 16 tokens of 8 of 128 experts, 4096 x
-// 1792, some 940 MB in 228 us for both products, 4.1 TB/s (words loaded ahead into registers instead: 630 us, a
-// warp waits for its newest load with its oldest).  Bound by the unpacking and the issue of 32-byte box rows.
+// 1792, some 750 MB (66 distinct experts) in 236 us for both products, 3.2 TB/s (words loaded ahead into registers
+// instead: 630 us, a warp waits for its newest load with its oldest).  No unit is full: at 15 warps an SM the schedulers
+// issue in 59 and 54 % of their cycles, HBM is at 48 and 30 %, the tensor pipe at 21 and 14 %; a warp waits for its own
+// chain of words, exchange and products, and a block for its slowest warp.
 template <bool kBF, bool kUp, int kW>
 __global__ void __launch_bounds__(kW * 32, 16 / kW) moe_kernel(const __grid_constant__ Args args) {
   using SH = Shared<kW>;
@@ -284,7 +287,8 @@ __global__ void __launch_bounds__(kW * 32, 16 / kW) moe_kernel(const __grid_cons
     const int job = unit / tiles, r = g & (kPart - 1);
     if (r >= jobs.rows[job]) return nullptr;
     const int place = jobs.place[job][r];
-    return (kUp ? p.x + static_cast<int64_t>(place / p.k) * p.x_st : act + (static_cast<int64_t>(g / kPart) * (p.T * p.k) + place) * p.I) + 8 * t;
+    const int64_t term = g / kPart;  // of act
+    return (kUp ? p.x + static_cast<int64_t>(place / p.k) * p.x_st : act + (term * (p.T * p.k) + place) * p.I) + 8 * t;
   };
   const auto load_x = [&](const uint16_t* row, int b, uint4 (&v)[2]) {
 #pragma unroll
@@ -443,7 +447,8 @@ __global__ void __launch_bounds__(kW * 32, 16 / kW) moe_kernel(const __grid_cons
           const float rest = v - elem_to_float<kBF>(whole);
           const int64_t at = static_cast<int64_t>(jobs.place[job][r]) * p.I + column;
           act[at] = whole;
-          act[at + static_cast<int64_t>(p.T * p.k) * p.I] = float_to_elem<kBF>(fabsf(rest) <= fabsf(v) ? rest : 0.f);  // none of infinities, NaN
+          // (infinities and NaN have no rest)
+          act[at + static_cast<int64_t>(p.T * p.k) * p.I] = float_to_elem<kBF>(fabsf(rest) <= fabsf(v) ? rest : 0.f);
         }
       } else {
 #pragma unroll
